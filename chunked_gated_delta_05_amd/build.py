@@ -17,6 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_host.cpp"),
            os.path.join(CSRC, "gdn_noalloc.hip"), os.path.join(CSRC, "gdn_bwd.hip")]
+# the recurrent-state operators of include/gdn_recurrent.h
+RECURRENT_HIP = ["gdn_linattn", "gdn_step", "gdn_pages"]
+RECURRENT_HOST = "gdn_recurrent_host"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
@@ -51,7 +54,19 @@ def build(verbose: bool = False) -> str:
     _run([HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           *warn, *inc, "-c", SOURCES[3], "-o", bobj], verbose)
-    _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", kobj, hobj, nobj, bobj, "-o", LIB + ".tmp"], verbose)
+    robjs = []
+    for name in RECURRENT_HIP:
+        robjs.append(os.path.join(BUILD, name + ".o"))
+        # MFMA accumulators in ordinary VGPRs, as above: the state is scaled
+        # and split by VALU ops every chunk
+        _run([HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form=1",
+              *warn, *inc, "-c", os.path.join(CSRC, name + ".hip"), "-o", robjs[-1]], verbose)
+    robjs.append(os.path.join(BUILD, RECURRENT_HOST + ".o"))
+    _run([HIPCC, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__", *warn, *inc, "-I", "/opt/rocm/include",
+          "-x", "c++", "-c", os.path.join(CSRC, RECURRENT_HOST + ".cpp"), "-o", robjs[-1]], verbose)
+    _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", kobj, hobj, nobj, bobj, *robjs, "-o", LIB + ".tmp"],
+         verbose)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

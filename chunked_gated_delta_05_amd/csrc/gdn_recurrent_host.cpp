@@ -1,0 +1,412 @@
+// Host side of the recurrent-state operators (include/gdn_recurrent.h):
+// argument validation, workspace layout and launch order. Every check runs
+// before the first HIP call, so a rejected call enqueues nothing and the
+// checks can be exercised without a GPU.
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "gdn_recurrent.h"
+#include "gdn_recurrent_internal.h"
+
+namespace {
+
+using gdn::LaJob;
+using gdn::LaJobs;
+using gdn::LaUnits;
+using gdn::RowsOf;
+
+constexpr int64_t kMaxElems = int64_t(1) << 40;   // sanity bound on any tensor
+constexpr int64_t kMaxBlocks = int64_t(1) << 30;
+constexpr int kChunk = 64;
+
+int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool width_ok(int32_t w) { return w == 64 || w == 128; }
+
+bool dtype_ok(int32_t d) { return d == GDN_DTYPE_F32 || d == GDN_DTYPE_BF16; }
+
+int64_t elem_bytes(int32_t d) { return d == GDN_DTYPE_BF16 ? 2 : 4; }
+
+// distances that keep every row 16-byte aligned and any offset below 2^62
+bool strides_ok(const int64_t* s, int64_t rows, int64_t heads, int32_t dtype) {
+    const int64_t lim = int64_t(1) << 60;
+    for (int i = 0; i < 2; ++i) {
+        if (s[i] < 0 || s[i] * elem_bytes(dtype) % 16 != 0) return false;
+        const int64_t n = i == 0 ? rows : heads;
+        if (n > 0 && s[i] > lim / n) return false;
+    }
+    return true;
+}
+
+// ------------------------------------------------------------------ prompts
+struct Prompt {
+    LaUnits u;
+    int64_t tokens, longest, chunks;
+    bool cut;      // some sequence has more than one segment
+};
+
+gdn_status check_prompt(const gdn_linattn_desc* d, Prompt* p) {
+    if (d == nullptr) return GDN_ERR_INVALID;
+    if (!width_ok(d->K) || !width_ok(d->V)) return GDN_ERR_UNSUPPORTED;
+    if (d->B < 1 || d->T < 0 || d->H < 1 || d->Hq < 1 || d->Hk < 1 || d->Hv < 1) return GDN_ERR_INVALID;
+    if (d->H % d->Hq || d->H % d->Hk || d->H % d->Hv) return GDN_ERR_INVALID;
+    if (!dtype_ok(d->dtype) || !dtype_ok(d->o_dtype) || !isfinite(d->scale)) return GDN_ERR_INVALID;
+    memset(p, 0, sizeof(*p));
+    p->tokens = int64_t(d->B) * d->T;
+    if (p->tokens * d->H > kMaxElems / 128) return GDN_ERR_INVALID;
+    if (!strides_ok(d->q_stride, p->tokens, d->Hq, d->dtype) || !strides_ok(d->k_stride, p->tokens, d->Hk, d->dtype) ||
+        !strides_ok(d->v_stride, p->tokens, d->Hv, d->dtype))
+        return GDN_ERR_INVALID;
+    LaUnits& u = p->u;
+    u.H = d->H;
+    u.T = d->T;
+    u.total = p->tokens;
+    if (d->n_units < 0) return GDN_ERR_INVALID;
+    if (d->n_units == 0) {
+        u.dense = 1;
+        u.n_units = d->B;
+        p->longest = d->T;
+        p->chunks = int64_t(d->B) * ((d->T + int64_t(kChunk) - 1) / kChunk);
+    } else {
+        if (d->B != 1 || !d->offsets_host || !d->offsets_dev) return GDN_ERR_INVALID;
+        const int32_t* o = d->offsets_host;
+        if (o[0] != 0 || o[d->n_units] != p->tokens) return GDN_ERR_INVALID;
+        for (int32_t i = 0; i < d->n_units; ++i) {
+            if (o[i] >= o[i + 1]) return GDN_ERR_INVALID;
+            const int64_t len = int64_t(o[i + 1]) - o[i];
+            p->longest = len > p->longest ? len : p->longest;
+            p->chunks += (len + kChunk - 1) / kChunk;
+        }
+        u.n_units = d->n_units;
+        u.offsets = d->offsets_dev;
+    }
+    // Segments: enough of them to give every compute unit its two
+    // workgroups, none shorter than four chunks.
+    const int64_t want = 512;
+    int64_t seg = (p->chunks * d->H + want - 1) / want;
+    if (seg < 4) seg = 4;
+    if (seg > p->longest / kChunk + 1) seg = p->longest / kChunk + 1;
+    u.seg_tokens = (int32_t)(seg * kChunk);
+    int64_t n = 0;
+    for (int32_t i = 0; i < u.n_units; ++i) {
+        const int64_t len = u.dense ? d->T : int64_t(d->offsets_host[i + 1]) - d->offsets_host[i];
+        const int64_t k = len > 0 ? (len + u.seg_tokens - 1) / u.seg_tokens : 1;
+        n += k;
+        if (k > 1) p->cut = true;
+        if (u.dense) {
+            n = k * u.n_units;
+            break;
+        }
+    }
+    if (n * d->H * gdn::LA_MAX_JOBS > kMaxBlocks || int64_t(u.n_units) * d->H * 16 > kMaxBlocks) return GDN_ERR_INVALID;
+    u.n_segs = (int32_t)n;
+    return GDN_OK;
+}
+
+// The size query and the checks of a given workspace.
+gdn_status check_workspace(int64_t need, void* workspace, size_t* workspace_bytes, bool* query) {
+    if (workspace_bytes == nullptr) return GDN_ERR_INVALID;
+    if (need < 256) need = 256;
+    *query = workspace == nullptr;
+    if (*query || *workspace_bytes < (size_t)need) {
+        const gdn_status st = *query ? GDN_OK : GDN_ERR_CAPACITY;
+        *workspace_bytes = (size_t)need;
+        return st;
+    }
+    return reinterpret_cast<uintptr_t>(workspace) % 256 == 0 ? GDN_OK : GDN_ERR_INVALID;
+}
+
+int64_t slot_bytes(const Prompt& p, const gdn_linattn_desc* d) {
+    return p.cut ? align256(int64_t(p.u.n_segs) * d->H * d->K * d->V * 4) : 0;
+}
+
+RowsOf rows(const void* ptr, const int64_t* stride, int32_t share) { return RowsOf{ptr, stride[0], stride[1], share}; }
+
+// contiguous [tokens][h][W]
+RowsOf rows(const void* ptr, int32_t h, int32_t W) { return RowsOf{ptr, int64_t(h) * W, W, 1}; }
+
+gdn_status run(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_DEVICE; }
+
+}  // namespace
+
+extern "C" gdn_status gdn_linattn_fwd(const gdn_linattn_desc* d, const void* q, const void* k, const void* v,
+                                      const float* decay, const float* s_in, const int32_t* in_pages, float* s_out,
+                                      const int32_t* out_pages, int32_t n_pages, void* o, void* workspace,
+                                      size_t* workspace_bytes, hipStream_t stream) {
+    Prompt p;
+    gdn_status st = check_prompt(d, &p);
+    if (st != GDN_OK) return st;
+    bool query = false;
+    st = check_workspace(slot_bytes(p, d), workspace, workspace_bytes, &query);
+    if (st != GDN_OK || query) return st;
+    if (!decay || (p.tokens > 0 && (!q || !k || !v || !o))) return GDN_ERR_INVALID;
+    if (n_pages < 0 || (in_pages && !s_in) || (out_pages && !s_out)) return GDN_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(s_in) || !aligned16(s_out))
+        return GDN_ERR_INVALID;
+    p.u.n_pages = n_pages;
+    p.u.decay = decay;
+    LaJobs jobs;
+    memset(&jobs, 0, sizeof(jobs));
+    jobs.n = 1;
+    LaJob& j = jobs.job[0];
+    j.q = rows(q, d->q_stride, d->H / d->Hq);
+    j.k = rows(k, d->k_stride, d->H / d->Hk);
+    j.v = rows(v, d->v_stride, d->H / d->Hv);
+    j.s_in = s_in;
+    j.in_pages = in_pages;
+    j.s_out = s_out;
+    j.out_pages = out_pages;
+    j.e = 1;
+    j.o_f32 = d->o_dtype == GDN_DTYPE_F32;
+    j.o = o;
+    j.s_p = j.s_o = d->scale;
+    j.s_w = 1.0f;
+    if (p.cut) {
+        j.slots = static_cast<float*>(workspace);
+        if (gdn::launch_la_summary(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
+        if (gdn::launch_la_merge(p.u, jobs, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    }
+    return run(gdn::launch_la_main(p.u, jobs, d->dtype, d->K, d->V, stream));
+}
+
+extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, const void* k, const void* v,
+                                      const float* decay, const float* s_in, const void* dout, const float* dht,
+                                      void* dq, void* dk, void* dv, float* dh0, void* workspace,
+                                      size_t* workspace_bytes, hipStream_t stream) {
+    Prompt p;
+    gdn_status st = check_prompt(d, &p);
+    if (st != GDN_OK) return st;
+    // slots of S and of its gradient, then the per-head gradients of shared heads
+    const int64_t slots = slot_bytes(p, d);
+    auto part_bytes = [&](int32_t h, int32_t W) {
+        return h == d->H ? int64_t(0) : align256(p.tokens * d->H * W * 4);
+    };
+    const int64_t bq = part_bytes(d->Hq, d->K), bk = part_bytes(d->Hk, d->K), bv = part_bytes(d->Hv, d->V);
+    bool query = false;
+    st = check_workspace(2 * slots + bq + bk + bv, workspace, workspace_bytes, &query);
+    if (st != GDN_OK || query) return st;
+    if (!decay || (p.tokens > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv))) return GDN_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(s_in) || !aligned16(dht) ||
+        !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(dh0))
+        return GDN_ERR_INVALID;
+    p.u.decay = decay;
+    char* base = static_cast<char*>(workspace);
+    float* s_slots = p.cut ? reinterpret_cast<float*>(base) : nullptr;
+    float* d_slots = p.cut ? reinterpret_cast<float*>(base + slots) : nullptr;
+    float* pq = bq ? reinterpret_cast<float*>(base + 2 * slots) : nullptr;
+    float* pk = bk ? reinterpret_cast<float*>(base + 2 * slots + bq) : nullptr;
+    float* pv = bv ? reinterpret_cast<float*>(base + 2 * slots + bq + bk) : nullptr;
+    const RowsOf rq = rows(q, d->q_stride, d->H / d->Hq), rk = rows(k, d->k_stride, d->H / d->Hk),
+                 rv = rows(v, d->v_stride, d->H / d->Hv), rd = rows(dout, d->H, d->V);
+    const int32_t f32 = d->dtype == GDN_DTYPE_F32;
+
+    // dq_i = scale [sum_{j <= i} d^{i-j} (do_i . v_j) k_j + d^{i+1} S do_i]
+    LaJob jq;
+    memset(&jq, 0, sizeof(jq));
+    jq.q = rd;
+    jq.k = rv;
+    jq.v = rk;
+    jq.s_in = s_in;
+    jq.slots = s_slots;
+    jq.transposed = 1;
+    jq.e = 1;
+    jq.o = pq ? pq : dq;
+    jq.o_f32 = pq || f32;
+    jq.s_p = jq.s_o = d->scale;
+    jq.s_w = 1.0f;
+    // dk_j = sum_{i >= j} d^{i-j} scale (v_j . do_i) q_i + d^{T-1-j} D v_j, D the gradient arriving
+    // at the end; in reversed time D's power starts at 0
+    LaJob jk;
+    memset(&jk, 0, sizeof(jk));
+    jk.q = rv;
+    jk.k = rd;
+    jk.v = rq;
+    jk.s_in = dht;
+    jk.slots = d_slots;
+    jk.transposed = 1;
+    jk.rev = 1;
+    jk.o = pk ? pk : dk;
+    jk.o_f32 = pk || f32;
+    jk.s_p = jk.s_w = d->scale;
+    jk.s_o = 1.0f;
+    // dv_j = sum_{i >= j} d^{i-j} scale (k_j . q_i) do_i + d^{T-1-j} D^T k_j; its state ends as dh0
+    LaJob jv;
+    memset(&jv, 0, sizeof(jv));
+    jv.q = rk;
+    jv.k = rq;
+    jv.v = rd;
+    jv.s_in = dht;
+    jv.s_out = dh0;
+    jv.slots = d_slots;
+    jv.rev = 1;
+    jv.o = pv ? pv : dv;
+    jv.o_f32 = pv || f32;
+    jv.s_p = jv.s_w = d->scale;
+    jv.s_o = 1.0f;
+
+    LaJobs jobs;
+    memset(&jobs, 0, sizeof(jobs));
+    if (p.cut) {
+        jobs.n = 2;
+        LaJob& a = jobs.job[0];   // the forward states
+        a.k = rk;
+        a.v = rv;
+        a.s_in = s_in;
+        a.slots = s_slots;
+        a.e = 1;
+        a.s_w = 1.0f;
+        jobs.job[1] = jv;         // their gradients
+        if (gdn::launch_la_summary(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
+        if (gdn::launch_la_merge(p.u, jobs, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    }
+    jobs.job[0] = jq;
+    jobs.job[1] = jk;
+    jobs.n = 2;
+    if (d->K == d->V) {
+        jobs.job[2] = jv;
+        jobs.n = 3;
+    }
+    if (gdn::launch_la_main(p.u, jobs, d->dtype, d->V, d->K, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    if (d->K != d->V) {
+        jobs.job[0] = jv;
+        jobs.n = 1;
+        if (gdn::launch_la_main(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    }
+    if (pq && gdn::launch_la_group(pq, dq, p.tokens, d->H, d->Hq, d->K, d->dtype, stream) != hipSuccess)
+        return GDN_ERR_DEVICE;
+    if (pk && gdn::launch_la_group(pk, dk, p.tokens, d->H, d->Hk, d->K, d->dtype, stream) != hipSuccess)
+        return GDN_ERR_DEVICE;
+    if (pv && gdn::launch_la_group(pv, dv, p.tokens, d->H, d->Hv, d->V, d->dtype, stream) != hipSuccess)
+        return GDN_ERR_DEVICE;
+    return GDN_OK;
+}
+
+// ------------------------------------------------------------------ single tokens
+namespace {
+
+gdn_status check_step(const gdn_step_desc* d, const void* q, const void* k, const void* v, const int32_t* pages,
+                      float* state, void* o, gdn::StepArgs* a) {
+    if (d == nullptr) return GDN_ERR_INVALID;
+    if (!width_ok(d->K) || !width_ok(d->V)) return GDN_ERR_UNSUPPORTED;
+    if (d->N < 0 || d->H < 1 || d->Hq < 1 || d->Hk < 1 || d->Hv < 1 || d->n_pages < 0) return GDN_ERR_INVALID;
+    if (d->H % d->Hq || d->H % d->Hk || d->H % d->Hv) return GDN_ERR_INVALID;
+    if (!dtype_ok(d->dtype) || !dtype_ok(d->o_dtype) || !isfinite(d->scale)) return GDN_ERR_INVALID;
+    if (int64_t(d->N) * d->H * 4 > kMaxBlocks) return GDN_ERR_INVALID;
+    if (int64_t(d->n_pages) * d->H > kMaxElems / (128 * 128)) return GDN_ERR_INVALID;
+    if (!strides_ok(d->q_stride, d->N, d->Hq, d->dtype) || !strides_ok(d->k_stride, d->N, d->Hk, d->dtype) ||
+        !strides_ok(d->v_stride, d->N, d->Hv, d->dtype))
+        return GDN_ERR_INVALID;
+    if (d->N > 0 && (!q || !k || !v || !o || (d->n_pages > 0 && !state))) return GDN_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(state)) return GDN_ERR_INVALID;
+    memset(a, 0, sizeof(*a));
+    a->N = d->N;
+    a->H = d->H;
+    a->n_pages = d->n_pages;
+    a->dtype = d->dtype;
+    a->o_dtype = d->o_dtype;
+    a->scale = d->scale;
+    a->q = rows(q, d->q_stride, d->H / d->Hq);
+    a->k = rows(k, d->k_stride, d->H / d->Hk);
+    a->v = rows(v, d->v_stride, d->H / d->Hv);
+    a->pages = pages;
+    a->state = state;
+    a->o = o;
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" gdn_status gdn_linattn_step(const gdn_step_desc* d, const void* q, const void* k, const void* v,
+                                       const float* decay, const int32_t* pages, float* state, void* o,
+                                       hipStream_t stream) {
+    gdn::StepArgs a;
+    const gdn_status st = check_step(d, q, k, v, pages, state, o, &a);
+    if (st != GDN_OK) return st;
+    if (!decay) return GDN_ERR_INVALID;
+    a.decay = decay;
+    return run(gdn::launch_step(a, d->K, d->V, stream));
+}
+
+extern "C" gdn_status gdn_recurrent_step(const gdn_step_desc* d, int32_t gate_kind, int32_t use_exp2, const void* q,
+                                         const void* k, const void* v, const float* g, const void* beta,
+                                         const int32_t* pages, float* state, void* o, int32_t flags,
+                                         hipStream_t stream) {
+    gdn::StepArgs a;
+    const gdn_status st = check_step(d, q, k, v, pages, state, o, &a);
+    if (st != GDN_OK) return st;
+    if (d->K != 128 || d->V != 128) return GDN_ERR_UNSUPPORTED;
+    if (gate_kind != GDN_GATE_SCALAR && gate_kind != GDN_GATE_PER_KEY) return GDN_ERR_INVALID;
+    if (use_exp2 != 0 && use_exp2 != 1) return GDN_ERR_INVALID;
+    if (flags & ~(GDN_FLAG_QK_L2NORM | GDN_FLAG_BETA_SIGMOID)) return GDN_ERR_INVALID;
+    if (d->N > 0 && (!g || !beta)) return GDN_ERR_INVALID;
+    a.g = g;
+    a.beta = beta;
+    a.kind = gate_kind == GDN_GATE_PER_KEY ? 2 : 1;
+    a.use_exp2 = use_exp2;
+    a.qk_norm = (flags & GDN_FLAG_QK_L2NORM) != 0;
+    a.beta_sig = (flags & GDN_FLAG_BETA_SIGMOID) != 0;
+    return run(gdn::launch_step(a, d->K, d->V, stream));
+}
+
+// ------------------------------------------------------------------ pages
+namespace {
+
+gdn_status check_pool(const void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes) {
+    if (n_layers < 0 || n_pages < 0 || page_bytes < 16 || page_bytes % 16 != 0) return GDN_ERR_INVALID;
+    if (page_bytes > (kMaxElems * 16) / (int64_t(n_layers) * n_pages + 1)) return GDN_ERR_INVALID;
+    if (int64_t(n_layers) * n_pages > 0 && !pool) return GDN_ERR_INVALID;
+    return aligned16(pool) ? GDN_OK : GDN_ERR_INVALID;
+}
+
+}  // namespace
+
+extern "C" size_t gdn_pages_workspace_ints(int32_t n) { return 1 + 2 * (size_t)(n > 0 ? n : 0); }
+
+extern "C" gdn_status gdn_pages_copy(void* dst_pool, int32_t dst_n_pages, const void* src_pool, int32_t src_n_pages,
+                                     int32_t n_layers, int64_t page_bytes, const int32_t* dst_pages,
+                                     const int32_t* src_pages, int32_t n, hipStream_t stream) {
+    gdn_status st = check_pool(dst_pool, n_layers, dst_n_pages, page_bytes);
+    if (st == GDN_OK) st = check_pool(src_pool, n_layers, src_n_pages, page_bytes);
+    if (st != GDN_OK) return st;
+    if (n < 0 || (n > 0 && (!dst_pages || !src_pages))) return GDN_ERR_INVALID;
+    const gdn::PoolArgs a{static_cast<char*>(dst_pool), static_cast<const char*>(src_pool), n_layers, dst_n_pages,
+                          src_n_pages, page_bytes};
+    return run(gdn::launch_pages_copy(a, dst_pages, src_pages, n, nullptr, stream));
+}
+
+extern "C" gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes,
+                                     const int32_t* table, const int32_t* parent, int32_t n_slots,
+                                     const int32_t* spare, int32_t n_spare, int32_t* new_table, int32_t* left,
+                                     int32_t* workspace, hipStream_t stream) {
+    const gdn_status st = check_pool(pool, n_layers, n_pages, page_bytes);
+    if (st != GDN_OK) return st;
+    if (n_slots < 0 || n_spare < 0) return GDN_ERR_INVALID;
+    if (n_slots > gdn::FORK_MAX || n_spare > gdn::FORK_MAX) return GDN_ERR_UNSUPPORTED;
+    if (n_slots > 0 && (!table || !parent || !new_table || new_table == table)) return GDN_ERR_INVALID;
+    if ((n_spare > 0 && !spare) || (n_slots + n_spare > 0 && !left) || !workspace) return GDN_ERR_INVALID;
+    if (gdn::launch_fork_plan(n_pages, table, parent, n_slots, spare, n_spare, new_table, left, workspace, stream) !=
+        hipSuccess)
+        return GDN_ERR_DEVICE;
+    const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
+                          page_bytes};
+    return run(gdn::launch_pages_copy(a, workspace + 1 + n_slots, workspace + 1, n_slots, workspace, stream));
+}
+
+extern "C" gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes,
+                                        const int32_t* table, int32_t n_slots, int32_t* new_table, int32_t* count,
+                                        int32_t* workspace, hipStream_t stream) {
+    const gdn_status st = check_pool(pool, n_layers, n_pages, page_bytes);
+    if (st != GDN_OK) return st;
+    if (n_slots < 0) return GDN_ERR_INVALID;
+    if (n_pages > gdn::COMPACT_MAX) return GDN_ERR_UNSUPPORTED;
+    if (n_slots > 0 && (!table || !new_table || new_table == table)) return GDN_ERR_INVALID;
+    if (!count || !workspace) return GDN_ERR_INVALID;
+    if (gdn::launch_compact_plan(n_pages, table, n_slots, new_table, count, workspace, stream) != hipSuccess)
+        return GDN_ERR_DEVICE;
+    const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
+                          page_bytes};
+    return run(gdn::launch_pages_copy(a, workspace + 1 + n_pages, workspace + 1, n_pages, workspace, stream));
+}

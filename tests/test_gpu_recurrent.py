@@ -1,0 +1,459 @@
+"""The recurrent-state operators on the GPU against 64-bit references.
+
+Bounds are derived, elementwise, against A, the operator's formula over
+absolute values (so the sum of what was added up):
+
+- an output in bf16 (8 significant bits) is rounded once: 2^-8 |x|;
+- fp32 sums of n products: (n + 2) 2^-24 A. A prompt's o sums at most 64
+  scores (each of 128 products) and 128 state rows: n = 320, 2^-15 A with
+  the factors d^n (1 ulp each); the two-term splits of scores and state with
+  bf16 inputs (2^-16 each) fit into 2^-14 A for both types;
+- a state sums a chunk's 64 products at a time, then chunks: 2^-17 A holds
+  n = 128, for up to 60 chunks;
+- a step sums 128 rows and a product or two: (128 + 6) 2^-24 < 2^-16 A, and
+  a state element three products: 2^-21 A, over A's own sums (the delta
+  rule's A includes k^T S, 128 products: 2^-16 A)."""
+import pytest
+import torch
+
+import recurrent_ref as ref
+from chunked_gated_delta_05_amd import binding as gb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def randn(gen, *shape):
+    return torch.randn(*shape, generator=gen)
+
+
+def within(x, want, A, rel, dtype, what):
+    """|x - want| <= rel A (+ the rounding of bf16)."""
+    x = x.detach().cpu().double().reshape(want.shape)
+    bound = rel * A + (2.0 ** -8 * want.abs() if dtype == torch.bfloat16 else 0) + 1e-30
+    over = ((x - want).abs() / bound).max().item() if x.numel() else 0.0
+    assert torch.isfinite(x).all(), f"{what}: not finite"
+    assert over <= 1.0, f"{what}: {over:.2f} times the bound"
+
+
+def decays(H, kind):
+    if kind == "mixed":   # no decay, total forgetting, strong and weak
+        d = [0.0, float("-inf"), -3.0, -0.01, -0.3, -40.0, -1e-4, -0.1]
+        return torch.tensor([d[i % 8] for i in range(H)])
+    return -0.7 * 0.3 ** torch.arange(H).float()
+
+
+# (name, lengths, packed, H, Hq, Hk, Hv)
+PROMPTS = [
+    ("one token", [1], False, 2, 2, 2, 2),
+    ("below a chunk", [31], False, 3, 3, 3, 3),
+    ("a chunk", [64, 64], False, 2, 2, 2, 2),
+    ("a chunk and one", [65], False, 2, 1, 2, 2),
+    ("segments", [700], False, 2, 2, 1, 2),
+    ("rows of segments", [530, 530, 530], False, 1, 1, 1, 1),
+    ("documents", [1, 64, 200, 63, 2, 33], True, 4, 4, 2, 2),
+    ("long and short documents", [5, 601, 1, 257, 256], True, 2, 2, 2, 1),
+    ("many documents", [1 + i % 3 for i in range(70)], True, 1, 1, 1, 1),
+]
+
+
+def prompt(case, dtype, K, V, kind, seed=0, states=True):
+    name, lens, packed, H, Hq, Hk, Hv = case
+    gen = torch.Generator().manual_seed(seed)
+    offs = [0]
+    for n in lens:
+        offs.append(offs[-1] + n)
+    lead = (offs[-1],) if packed else (len(lens), lens[0])
+    x = {"q": randn(gen, *lead, Hq, K), "k": randn(gen, *lead, Hk, K), "v": randn(gen, *lead, Hv, V)}
+    x = {n: t.to(DT[dtype]).to(DEV) for n, t in x.items()}
+    x["decay"] = decays(H, kind).to(DEV)
+    x["S0"] = randn(gen, len(lens), H, K, V).to(DEV) if states else None
+    x["dout"] = randn(gen, *lead, H, V).to(DT[dtype]).to(DEV)
+    x["dht"] = randn(gen, len(lens), H, K, V).to(DEV) if states else None
+    x["meta"] = gb.make_meta(offs, offs[-1], DEV) if packed else None
+    x["offs"], x["scale"] = offs, 0.7 * K ** -0.5
+    return x
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", PROMPTS, ids=lambda c: c[0])
+def test_linattn_forward(case, dtype, K, V):
+    x = prompt(case, dtype, K, V, "mixed")
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], x["scale"], meta=x["meta"],
+                                initial_state=x["S0"], output_final_state=True)
+    args = (x["q"], x["k"], x["v"], x["decay"], x["scale"], x["offs"], x["S0"])
+    want, wfin = ref.linattn(*args)
+    A, Afin = ref.linattn(*args, absolute=True)
+    assert o.dtype == DT[dtype] and o.shape == (*x["q"].shape[:-2], x["decay"].shape[0], V)
+    within(o, want, A, 2.0 ** -14, o.dtype, "o")
+    within(fin, wfin, Afin, 2.0 ** -17, fin.dtype, "final state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_linattn_forward_without_states_and_with_fp32_output(dtype):
+    x = prompt(PROMPTS[4], dtype, 128, 128, "spread", states=False)
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], o_dtype=torch.float32)
+    assert fin is None
+    args = (x["q"], x["k"], x["v"], x["decay"], 128 ** -0.5, x["offs"], None)
+    within(o, ref.linattn(*args)[0], ref.linattn(*args, absolute=True)[0], 2.0 ** -14, o.dtype, "o")
+
+
+def test_linattn_no_tokens():
+    q = torch.empty(2, 0, 3, 128, dtype=torch.bfloat16, device=DEV)
+    S0 = torch.randn(2, 3, 128, 128, device=DEV)
+    decay = torch.full((3,), -0.1, device=DEV)
+    o, fin = gb.gdn_linattn_fwd(q, q, q, decay, initial_state=S0, output_final_state=True)
+    assert o.shape == (2, 0, 3, 128) and torch.equal(fin, S0)
+    r = gb.gdn_linattn_bwd(q, q, q, decay, o, initial_state=S0, dht=S0)
+    assert torch.equal(r["dh0"], S0) and r["dq"].shape == q.shape
+
+
+def test_linattn_strided_rows_equal_contiguous_ones():
+    # q, k, v as views of one projection, heads-first too
+    H, K, T = 3, 128, 150
+    gen = torch.Generator().manual_seed(5)
+    qkv = randn(gen, 2, T, 3 * H * K).bfloat16().to(DEV)
+    q, k, v = (qkv[..., i * H * K:(i + 1) * H * K].unflatten(-1, (H, K)) for i in range(3))
+    decay = decays(H, "spread").to(DEV)
+    dense = [t.contiguous() for t in (q, k, v)]
+    want = gb.gdn_linattn_fwd(*dense, decay)[0]
+    assert torch.equal(gb.gdn_linattn_fwd(q, k, v, decay)[0], want)
+    hfirst = [t[0].transpose(0, 1).contiguous().transpose(0, 1) for t in dense]
+    meta = gb.make_meta([0, T], T, DEV)
+    assert torch.equal(gb.gdn_linattn_fwd(*hfirst, decay, meta=meta)[0], want[0])
+    g = gb.gdn_linattn_bwd(q, k, v, decay, want)
+    for n, t in gb.gdn_linattn_bwd(*dense, decay, want).items():
+        assert torch.equal(g[n], t), n
+
+
+def test_linattn_does_not_read_other_documents():
+    # NaN and infinities in the neighbours of a document, inside the same tiles
+    offs, H = [0, 40, 111, 170], 2
+    x = prompt(("", [40, 71, 59], True, H, H, H, H), "bf16", 128, 128, "spread")
+    meta = gb.make_meta(offs, offs[-1], DEV)
+    run = lambda: (gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], meta=meta, initial_state=x["S0"],
+                                      output_final_state=True),
+                   gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], meta=meta,
+                                      initial_state=x["S0"], dht=x["dht"]))
+    (o, fin), g = run()
+    for n in ("q", "k", "v", "dout"):
+        x[n][:40] = float("nan")
+        x[n][111:] = float("inf")
+    x["S0"][0], x["S0"][2] = float("nan"), float("inf")
+    x["dht"][0], x["dht"][2] = float("nan"), float("inf")
+    (o2, fin2), g2 = run()
+    assert torch.equal(o[40:111], o2[40:111]) and torch.equal(fin[1], fin2[1])
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(g[n][40:111], g2[n][40:111]), n
+    assert torch.equal(g["dh0"][1], g2["dh0"][1])
+
+
+@pytest.mark.parametrize("lens", [[100, 30, 64], [600, 30, 300]])
+def test_linattn_states_in_pages(lens):
+    H, K, V = 2, 128, 64
+    x = prompt(("", lens, True, H, H, H, H), "bf16", K, V, "spread")
+    pool = torch.randn(6, H, K, V, device=DEV)
+    before = pool.clone()
+    pages = torch.tensor([4, -1, 1], dtype=torch.int32, device=DEV)
+    S0 = torch.stack([pool[4], torch.zeros_like(pool[0]), pool[1]])
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], meta=x["meta"], initial_state=S0,
+                                output_final_state=True)
+    out_pages = torch.tensor([4, 99, 1], dtype=torch.int32, device=DEV)   # in place; out of range: not written
+    o2, fin2 = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], meta=x["meta"], initial_state=pool,
+                                  initial_pages=pages, final_out=pool, final_pages=out_pages)
+    assert torch.equal(o, o2) and fin2 is pool
+    assert torch.equal(pool[4], fin[0]) and torch.equal(pool[1], fin[2])
+    for p in (0, 2, 3, 5):
+        assert torch.equal(pool[p], before[p])
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", PROMPTS, ids=lambda c: c[0])
+def test_linattn_gradients(case, dtype, K, V):
+    x = prompt(case, dtype, K, V, "mixed", seed=1)
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], meta=x["meta"],
+                           initial_state=x["S0"], dht=x["dht"])
+    args = (x["q"], x["k"], x["v"], x["decay"], x["scale"], x["offs"], x["S0"], x["dout"], x["dht"])
+    want, A = ref.linattn_grads(*args), ref.linattn_grads(*args, absolute=True)
+    for i, (n, t) in enumerate((("dq", "q"), ("dk", "k"), ("dv", "v"))):
+        h = x[t].shape[-2]
+        assert r[n].shape == x[t].shape and r[n].dtype == x[t].dtype
+        within(r[n], ref.shared(want[i], h), ref.shared(A[i], h), 2.0 ** -14, r[n].dtype, n)
+    within(r["dh0"], want[3], A[3], 2.0 ** -17, torch.float32, "dh0")
+
+
+@pytest.mark.parametrize("case", [PROMPTS[4], PROMPTS[7]], ids=lambda c: c[0])
+def test_linattn_gradients_against_differences(case):
+    # o and the final state are linear in each of q, k, v and S0 alone, so a
+    # central difference of step 1 along a direction is exact but for the
+    # fp32 rounding of the two forwards: 2^-14 of the absolute sums
+    x = prompt(case, "fp32", 128, 128, "spread", seed=2)
+    names = ["q", "k", "v", "S0"]
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], meta=x["meta"],
+                           initial_state=x["S0"], dht=x["dht"])
+    gen = torch.Generator().manual_seed(3)
+
+    def loss(y):
+        o, fin = gb.gdn_linattn_fwd(y["q"], y["k"], y["v"], x["decay"], x["scale"], meta=x["meta"],
+                                    initial_state=y["S0"], output_final_state=True)
+        parts = torch.cat([(o.double() * x["dout"].double()).flatten(), (fin.double() * x["dht"].double()).flatten()])
+        return parts.sum().item(), parts.abs().sum().item()
+
+    for n, gname in zip(names, ("dq", "dk", "dv", "dh0")):
+        d = randn(gen, *x[n].shape).to(DEV)
+        hi, a = loss({**x, n: x[n] + d})
+        lo, b = loss({**x, n: x[n] - d})
+        got = (r[gname].double() * d.double()).sum().item()
+        assert abs((hi - lo) / 2 - got) <= 2.0 ** -14 * (a + b), n
+
+
+def test_linattn_autograd():
+    x = prompt(PROMPTS[6], "fp32", 64, 64, "spread")
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v", "S0")]
+    o, fin = gb.LinearAttention.apply(*leaves[:3], x["decay"], leaves[3], x["scale"], x["meta"])
+    torch.autograd.backward([o, fin], [x["dout"], x["dht"]])
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], meta=x["meta"],
+                           initial_state=x["S0"], dht=x["dht"])
+    for t, n in zip(leaves, ("dq", "dk", "dv", "dh0")):
+        assert torch.equal(t.grad, r[n]), n
+    # one output unused; no state
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v")]
+    o, fin = gb.LinearAttention.apply(*leaves, x["decay"], None, x["scale"], x["meta"])
+    fin.backward(x["dht"])
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], torch.zeros_like(x["dout"]), x["scale"],
+                           meta=x["meta"], dht=x["dht"])
+    for t, n in zip(leaves, ("dq", "dk", "dv")):
+        assert torch.equal(t.grad, r[n]), n
+
+
+def test_linattn_repeats_bit_for_bit_and_on_another_stream():
+    x = prompt(PROMPTS[7], "bf16", 128, 128, "spread")
+    run = lambda: gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], meta=x["meta"],
+                                     initial_state=x["S0"], dht=x["dht"])
+    a = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = run()
+    torch.cuda.current_stream().wait_stream(side)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+# ------------------------------------------------------------------ single tokens
+def step_rows(gen, N, h, W, dtype):
+    return randn(gen, N, h, W).to(DT[dtype]).to(DEV)
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,H,Hq,Hk,Hv", [(1, 1, 1, 1, 1), (3, 4, 4, 2, 1), (140, 4, 1, 4, 4)])
+def test_linattn_step(N, H, Hq, Hk, Hv, dtype, K, V):
+    gen = torch.Generator().manual_seed(N)
+    q, k, v = (step_rows(gen, N, h, w, dtype) for h, w in ((Hq, K), (Hk, K), (Hv, V)))
+    decay = decays(H, "mixed").to(DEV)
+    pool = randn(gen, N + 3, H, K, V).to(DEV)
+    before = pool.clone()
+    pages = torch.randperm(N + 3, generator=gen)[:N].to(torch.int32)
+    if N > 1:
+        pages[0], pages[N - 1] = -1, N + 3       # no page
+    o = gb.gdn_linattn_step(q, k, v, decay, pool, pages=pages.to(DEV))
+    assert o.dtype == DT[dtype] and o.shape == (N, H, V)
+    on = ((pages >= 0) & (pages < N + 3)).nonzero().flatten()
+    at = pages[on].long()
+    args = (q[on.to(DEV)], k[on.to(DEV)], v[on.to(DEV)], decay, K ** -0.5, before[at.to(DEV)])
+    want, S = ref.linattn_step(*args)
+    A, AS = ref.linattn_step(*args, absolute=True)
+    within(o[on.to(DEV)], want, A, 2.0 ** -16, o.dtype, "o")
+    within(pool[at.to(DEV)], S, AS, 2.0 ** -21, torch.float32, "state")
+    off = torch.ones(N, dtype=torch.bool)
+    off[on] = False
+    assert (o[off.to(DEV)] == 0).all()
+    rest = torch.ones(N + 3, dtype=torch.bool)
+    rest[at] = False
+    assert torch.equal(pool[rest.to(DEV)], before[rest.to(DEV)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("per_key,exp2,norm,sigmoid", [(False, False, False, False), (True, True, False, False),
+                                                       (False, True, True, True), (True, False, True, False)])
+@pytest.mark.parametrize("N,H,Hk", [(1, 2, 2), (5, 4, 2), (70, 8, 1)])
+def test_delta_step(N, H, Hk, per_key, exp2, norm, sigmoid, dtype):
+    gen = torch.Generator().manual_seed(N + H)
+    q, k = step_rows(gen, N, Hk, 128, dtype), step_rows(gen, N, Hk, 128, dtype)
+    if not norm:
+        q, k = ((t.float() / t.float().norm(dim=-1, keepdim=True)).to(t.dtype) for t in (q, k))
+    v = step_rows(gen, N, H, 128, dtype)
+    g = -torch.nn.functional.softplus(randn(gen, *((N, H, 128) if per_key else (N, H)))).to(DEV)
+    g[0] = -1e4                                   # total forgetting
+    beta = torch.rand(N, H, generator=gen).to(DT[dtype]).to(DEV)
+    pool = randn(gen, N + 2, H, 128, 128).to(DEV)
+    before = pool.clone()
+    pages = torch.randperm(N + 2, generator=gen)[:N].to(torch.int32).to(DEV)
+    o = gb.gdn_recurrent_step(q, k, v, g, beta, pool, pages=pages, use_exp2=exp2, qk_l2norm=norm,
+                              beta_sigmoid=sigmoid, o_dtype=torch.float32)
+    args = (q, k, v, g, beta, 128 ** -0.5, before[pages.long()], exp2, norm, sigmoid)
+    want, S = ref.delta_step(*args)
+    A, AS = ref.delta_step(*args, absolute=True)
+    within(o, want, A, 2.0 ** -15, torch.float32, "o")
+    within(pool[pages.long()], S, AS, 2.0 ** -16, torch.float32, "state")
+
+
+@pytest.mark.parametrize("per_key", [False, True])
+def test_delta_steps_equal_the_chunked_forward(per_key):
+    # 70 steps against gdn_chunk_fwd on the same tokens, at the chunked
+    # forward's own tolerance for fp32 inputs (1e-4 of the rms)
+    T, H = 70, 2
+    gen = torch.Generator().manual_seed(9)
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True)
+    q, k = (unit(randn(gen, 1, T, H, 128)).to(DEV) for _ in range(2))
+    v = randn(gen, 1, T, H, 128).to(DEV)
+    g = (-0.1 * torch.rand(*((1, T, H, 128) if per_key else (1, T, H)), generator=gen)).to(DEV)
+    beta = torch.rand(1, T, H, generator=gen).to(DEV)
+    o, fin, _ = gb.gdn_chunk_fwd(q, k, v, g, beta, output_final_state=True)
+    state = torch.zeros(1, H, 128, 128, device=DEV)
+    steps = torch.stack([gb.gdn_recurrent_step(q[:, t], k[:, t], v[:, t], g[:, t].contiguous(),
+                                               beta[:, t].contiguous(), state) for t in range(T)], 1)
+    for x, y in ((steps, o), (state, fin)):
+        assert (x - y).abs().max() <= 1e-4 * y.square().mean().sqrt()
+
+
+def test_linattn_steps_equal_the_prompt():
+    # both sum in fp32: 2^-14 and 2^-17 of the absolute sums, twice
+    x = prompt(("", [90], False, 3, 3, 3, 3), "fp32", 128, 128, "spread")
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], initial_state=x["S0"], output_final_state=True)
+    state = x["S0"].clone()
+    steps = torch.stack([gb.gdn_linattn_step(x["q"][:, t], x["k"][:, t], x["v"][:, t], x["decay"], state)
+                         for t in range(90)], 1)
+    A, AS = ref.linattn(x["q"], x["k"], x["v"], x["decay"], 128 ** -0.5, x["offs"], x["S0"], absolute=True)
+    within(steps, o.cpu().double().view(A.shape), A, 2.0 ** -13, torch.float32, "o")
+    within(state, fin.cpu().double(), AS, 2.0 ** -16, torch.float32, "state")
+
+
+def test_steps_in_a_graph():
+    gen = torch.Generator().manual_seed(4)
+    N, H = 3, 4
+    q, k, v = (step_rows(gen, N, H, 128, "bf16") for _ in range(3))
+    decay = decays(H, "spread").to(DEV)
+    g, beta = -torch.rand(N, H, generator=gen).to(DEV), torch.rand(N, H, generator=gen).bfloat16().to(DEV)
+    pages = torch.tensor([2, 0, -1], dtype=torch.int32, device=DEV)
+    start = randn(gen, 2, 3, H, 128, 128).to(DEV)
+    k2 = k / k.float().norm(dim=-1, keepdim=True).to(k.dtype)
+
+    def both(a, b):
+        return (gb.gdn_linattn_step(q, k, v, decay, a, pages=pages),
+                gb.gdn_recurrent_step(q, k2, v, g, beta, b, pages=pages))
+
+    s1, s2 = start.clone(), start.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(s2[0], s2[1])
+    torch.cuda.current_stream().wait_stream(side)
+    s2.copy_(start)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both(s2[0], s2[1])
+    s2.copy_(start)
+    for _ in range(4):
+        want = both(s1[0], s1[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs)) and torch.equal(s1, s2)
+
+
+# ------------------------------------------------------------------ pages
+def pool_of(layers, pages, shape=(3, 4), dtype=torch.float32):
+    n = layers * pages * shape[0] * shape[1]
+    return torch.arange(n, device=DEV).to(dtype).view(layers, pages, *shape)
+
+
+def moved(pool, copies):
+    want = pool.clone()
+    for s, d in copies:
+        want[:, d] = pool[:, s]
+    return want
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def test_pages_copy():
+    for shape, dtype in (((1, 4), torch.float32), ((2, 128, 64), torch.float32), ((5, 1000), torch.bfloat16)):
+        src = torch.randn(3, 7, *shape, device=DEV).to(dtype)
+        dst = torch.randn(3, 5, *shape, device=DEV).to(dtype)
+        want = dst.clone()
+        want[:, 4], want[:, 0], want[:, 2] = src[:, 6], src[:, 0], src[:, 6]
+        gb.gdn_pages_copy(dst, src, ints([4, 0, 2, -1, 5, 3]), ints([6, 0, 6, 1, 1, 7]))   # three out of range
+        assert torch.equal(dst, want)
+    one = pool_of(2, 6)
+    want = moved(one, [(1, 4), (0, 5)])
+    gb.gdn_pages_copy(one, one, ints([4, 5]), ints([1, 0]))
+    assert torch.equal(one, want)
+    gb.gdn_pages_copy(one, one, ints([]), ints([]))
+    assert torch.equal(one, want)
+
+
+@pytest.mark.parametrize("table,parent,spare", [
+    ([3, 1, 0], [0, 1, 2], []),                       # nothing moves
+    ([3, 1, 0], [1, 1, 1], []),                       # one survivor
+    ([3, 1, 0], [2, 0, 2], [5]),
+    ([3, 1, 0], [-1, 7, -1], [5, 2]),                 # all end
+    ([3, -1, 0, 99], [1, 3, 0, 0], []),               # slots without a page
+    ([3, -1, -1], [0, 0, 0], []),                     # too few free pages
+    ([3, -1, -1], [0, 0, 0], [-1, 4, 77]),
+    ([2], [0], []),
+    ([], [], [1]),
+])
+def test_pages_fork_small(table, parent, spare):
+    pool = pool_of(2, 6)
+    new, copies, left = ref.fork(table, parent, spare, 6)
+    want = moved(pool, copies)
+    t = ints(table)
+    got, gleft = gb.gdn_pages_fork(pool, t, ints(parent), spare=ints(spare))
+    assert got.tolist() == new and gleft.tolist() == left
+    assert torch.equal(pool, want) and t.tolist() == table
+
+
+@pytest.mark.parametrize("n,pages,m", [(64, 70, 6), (1023, 1100, 40), (1025, 3000, 1000), (5000, 8192, 3000)])
+def test_pages_fork_random(n, pages, m):
+    gen = torch.Generator().manual_seed(n)
+    order = torch.randperm(pages, generator=gen).tolist()
+    table, spare = order[:n], order[n:n + m]
+    parent = torch.randint(-1, max(2, n // 3), (n,), generator=gen).tolist()
+    for i in range(0, n, 17):
+        table[i] = -1
+    pool = pool_of(2, pages, (1, 4), torch.int32)
+    new, copies, left = ref.fork(table, parent, spare, pages)
+    want = moved(pool, copies)
+    got, gleft = gb.gdn_pages_fork(pool, ints(table), ints(parent), spare=ints(spare))
+    assert got.tolist() == new and gleft.tolist() == left and torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("pages,table", [
+    (6, [5, 4, 3]), (6, [0, 1, 2]), (6, [5]), (6, []), (6, [0, 5, 5, 0]), (6, [-1, 3, 9]), (6, [5, 4, 3, 2, 1, 0]),
+    (1, [0]), (33, [32, 0]), (0, []),
+])
+def test_pages_compact_small(pages, table):
+    pool = pool_of(2, pages)
+    new, moves, count = ref.compact(table, pages)
+    want = moved(pool, moves)
+    got, n = gb.gdn_pages_compact(pool, ints(table))
+    assert got.tolist() == new and n.tolist() == [count] and torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("pages,n", [(1000, 300), (40000, 9000), (131072, 70000)])
+def test_pages_compact_random(pages, n):
+    gen = torch.Generator().manual_seed(n)
+    table = torch.randint(-1, pages, (n,), generator=gen).tolist()
+    pool = pool_of(1, pages, (1, 4), torch.int32)
+    new, moves, count = ref.compact(table, pages)
+    s, d = (torch.tensor(x, device=DEV) for x in zip(*moves))
+    want = pool.clone()
+    want[:, d] = pool[:, s]
+    got, c = gb.gdn_pages_compact(pool, ints(table))
+    assert got.tolist() == new and c.tolist() == [count] and torch.equal(pool, want)
