@@ -5,8 +5,8 @@
 //     o_i = sum_{j <= i} d^{i-j} (q_i . k_j) v_j + d^{i+1} q_i S
 //     S  <- d^C S + sum_j d^{C-1-j} k_j v_j^T
 // so a chunk is four matrix products. A workgroup walks the chunks of one
-// segment of one head: each of its four waves keeps a quarter of S's value
-// columns in MFMA accumulators for the whole walk, and those registers are at
+// segment of one head: each of its V / 16 waves keeps 16 of S's value columns
+// in MFMA accumulators for the whole walk, and those registers are at
 // once the operand of q S (an accumulator tile and an operand hold the same
 // elements if the contraction's order is chosen to match). Long sequences
 // with too few heads to fill the GPU are cut into segments: a first pass sums
@@ -30,7 +30,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 256;   // of the elementwise kernels; a walk has 4 V threads
 constexpr int NXCD = 8;
 
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -134,46 +134,73 @@ __device__ __forceinline__ int page_of(const int32_t* pages, int unit, int n_pag
 }
 
 // ------------------------------------------------------------------ tiles
-// C rows of W elements in LDS in 16-byte units, a row's units exchanged by
-// an XOR with the row number: 16 rows read at one column, and 4 rows read
-// across, both spread over the banks.
+// Rows of W elements in LDS in 16-byte units, a row's units exchanged by an
+// XOR with the row number, so that 16 rows read at one column and 4 rows read
+// across both spread over the banks. Everything a lane reads of a tile is at
+// one byte offset of the lane, XOR a multiple of 16 below the row length,
+// plus a constant; the offsets are made anew from the lane's in each chunk
+// (fresh), since holding all of them would cost more registers than the
+// state does.
 template <typename T, int W>
 struct Tile {
     static constexpr int EPU = 16 / sizeof(T);
     static constexpr int UNITS = W / EPU;
+    static constexpr int RB = W * sizeof(T);   // bytes of a row
     static constexpr int MASK = (UNITS < 16 ? UNITS : 16) - 1;
-    __device__ static __forceinline__ int at(int row, int unit) { return row * W + (unit ^ (row & MASK)) * EPU; }
-    // element offset of (row, col); col's unit is swizzled, its place in the unit kept
-    __device__ static __forceinline__ int el(int row, int col) { return at(row, col / EPU) + col % EPU; }
+    __device__ static __forceinline__ int at(int row, int unit) { return row * RB + (unit ^ (row & MASK)) * 16; }
 };
 
-// One chunk of one tensor on its way from memory to its tile: each thread
-// carries rows r0, r0 + STEP, ...
-template <typename T, int W, int C>
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+template <typename V>
+__device__ __forceinline__ V lds_get(const char* base, int at) {
+    return *reinterpret_cast<const V*>(base + at);
+}
+
+// One tensor's chunk on its way from memory to its tile: each of NT threads
+// carries rows row0, row0 + STEP, ...
+template <typename T, int W, int C, int NT>
 struct Carrier {
     using TL = Tile<T, W>;
     static constexpr int STEP = NT / TL::UNITS;
     static constexpr int N = C / STEP;
-    static_assert(N >= 1, "");
+    static_assert(N >= 1 && (STEP & (STEP - 1)) == 0, "");
     u32x4 x[N];
+    const char* p;        // row0 of the next full chunk
+    int64_t step, chunk;  // bytes to the next row of this thread, to the next chunk
 
-    // tt0: time of tile row 0 (negative rows of a partial chunk stay zero)
-    __device__ __forceinline__ void load(const RowsOf& r, int h, int64_t start, int len, int rev, int tt0, int shift) {
+    // time of the first tile row: t0
+    __device__ __forceinline__ void init(const RowsOf& r, int h, int64_t start, int len, int rev, int t0) {
         const int row0 = threadIdx.x / TL::UNITS, unit = threadIdx.x % TL::UNITS;
-        const int64_t t = (int64_t)tt0 + row0;
+        const int64_t t = (int64_t)t0 + row0;
         const int64_t tok = rev ? start + len - 1 - t : start + t;
-        const T* p = static_cast<const T*>(r.p) + tok * r.ts + (int64_t)(h / r.share) * r.hs + unit * TL::EPU;
-        const int64_t step = (rev ? -STEP : STEP) * r.ts;
+        p = static_cast<const char*>(r.p) + (tok * r.ts + (int64_t)(h / r.share) * r.hs + unit * TL::EPU) * (int)sizeof(T);
+        step = (rev ? -STEP : STEP) * r.ts * (int)sizeof(T);
+        chunk = step * N;
+    }
+    __device__ __forceinline__ void load() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const u32x4*>(p + i * step);
+        p += chunk;
+    }
+    // a last, partial chunk: its first row is tile row `shift`, zero rows before
+    __device__ __forceinline__ void load_partial(int shift) {
+        const int row0 = threadIdx.x / TL::UNITS;
+        const char* q = p - shift * (step / STEP);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             x[i] = u32x4{0, 0, 0, 0};
-            if (row0 + i * STEP >= shift) x[i] = *reinterpret_cast<const u32x4*>(p + i * step);
+            if (row0 + i * STEP >= shift) x[i] = *reinterpret_cast<const u32x4*>(q + i * step);
         }
     }
-    __device__ __forceinline__ void store(T* tile) const {
-        const int row0 = threadIdx.x / TL::UNITS, unit = threadIdx.x % TL::UNITS;
+    __device__ static __forceinline__ int lane_at() {
+        return TL::at(threadIdx.x / TL::UNITS, threadIdx.x % TL::UNITS);
+    }
+    __device__ __forceinline__ void store(char* tile, int at) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + TL::at(row0 + i * STEP, unit)) = x[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (at ^ ((i * STEP & TL::MASK) * 16)) + i * STEP * TL::RB) = x[i];
     }
 };
 
@@ -192,8 +219,8 @@ __device__ __forceinline__ f32x4 mfma(f32x4 a, f32x4 b, f32x4 c) {
 }
 
 // 4 x 16 bf16 read across: lane p gets column p of the four rows
-__device__ __forceinline__ s16x4 read_across(const bf16* p) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, p));
+__device__ __forceinline__ s16x4 read_across(const char* base, int at) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, base + at));
 }
 __device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -208,181 +235,161 @@ template <>
 struct Shape<bf16> {
     static constexpr int C = 64;    // tokens per chunk
     static constexpr int KS = 32;   // contraction of one operand
+    typedef bf16x8 frag;
 };
 template <>
 struct Shape<float> {
     static constexpr int C = 32;
     static constexpr int KS = 16;
+    typedef f32x4 frag;
 };
 
+// Row 16 it + p of a tile as an operand, contraction block t; at:
+// row_lane<T, W>()
+template <typename T, int W>
+__device__ __forceinline__ int row_lane() {
+    return Tile<T, W>::at(threadIdx.x & 15, (threadIdx.x & 63) >> 4);
+}
+template <typename T, int W>
+__device__ __forceinline__ typename Shape<T>::frag row_frag(const char* tile, int at, int it, int t) {
+    return lds_get<typename Shape<T>::frag>(tile, (at ^ (64 * t)) + it * 16 * Tile<T, W>::RB);
+}
+
+// Column c0 + p of a tile as an operand, tokens of block s (32 or 16 of
+// them). bf16: c0's columns are four groups of four that the lanes p % 4
+// name, GAP apart; across_lane gives the address of the lane's group.
+template <int W>
+__device__ __forceinline__ int across_lane(int col) {   // col: of this lane's group
+    const int p = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    return Tile<bf16, W>::at(8 * g + (p >> 2), col / 8) + col % 8 * 2;
+}
+template <int W>
+__device__ __forceinline__ bf16x8 across_frag(const char* tile, int at, int s, int flip, int add) {
+    constexpr int RB = Tile<bf16, W>::RB;
+    // four rows on, the row number's bit 2 flips the units' bit 2
+    return join(read_across(tile, (at ^ flip) + 32 * s * RB + add),
+                read_across(tile, (at ^ flip ^ 64) + (32 * s + 4) * RB + add));
+}
+template <int W>
+__device__ __forceinline__ int column_lane(int col) {   // col: of this lane
+    const int g = (threadIdx.x & 63) >> 4;
+    return Tile<float, W>::at(4 * g, col / 4) + col % 4 * 4;
+}
+template <int W>
+__device__ __forceinline__ f32x4 column_frag(const char* tile, int at, int s, int flip) {
+    constexpr int RB = Tile<float, W>::RB;
+    f32x4 x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = lds_get<float>(tile, (at ^ flip ^ (16 * r)) + (16 * s + r) * RB);
+    return x;
+}
+
 // ------------------------------------------------------------------ the state
-// A wave's part of S: CG groups of 16 value columns, KD / 16 tiles of 16 keys.
+// A wave's part of S: 16 value columns, KD / 16 tiles of 16 keys.
 // bf16: row m of tile 2 t + u is key 32 t + 8 (m / 4) + 4 u + m % 4, so that
 // tiles 2 t and 2 t + 1 hold, in each lane, the eight consecutive keys of an
 // operand; fp32: row m of tile t is key 16 t + m.
 template <typename T, int KD, int VD>
 struct State {
-    static constexpr int KT = KD / 16, CG = VD / 64;
-    f32x4 s[KT][CG];
+    static constexpr int KT = KD / 16;
+    f32x4 s[KT];
 
     __device__ static __forceinline__ int key0(int kt, int g) {   // of the lane's four rows
         if constexpr (sizeof(T) == 2) return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1);
         return 16 * kt + 4 * g;
     }
-    __device__ static __forceinline__ int col(int cg) {
-        return (threadIdx.x >> 6) * (VD / 4) + 16 * cg + (threadIdx.x & 15);
-    }
+    __device__ static __forceinline__ int col() { return (threadIdx.x >> 6) * 16 + (threadIdx.x & 15); }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f32x4{0, 0, 0, 0};
+        for (int kt = 0; kt < KT; ++kt) s[kt] = f32x4{0, 0, 0, 0};
     }
     __device__ void load(const float* p, int transposed) {
         const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt) {
+            if (transposed) {
+                s[kt] = *reinterpret_cast<const f32x4*>(p + col() * KD + key0(kt, g));
+            } else {
 #pragma unroll
-            for (int cg = 0; cg < CG; ++cg) {
-                if (transposed) {
-                    s[kt][cg] = *reinterpret_cast<const f32x4*>(p + col(cg) * KD + key0(kt, g));
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * VD + col(cg)];
-                }
+                for (int r = 0; r < 4; ++r) s[kt][r] = p[(key0(kt, g) + r) * VD + col()];
             }
+        }
     }
     __device__ void store(float* p) const {
         const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col(cg)] = s[kt][cg][r];
+            for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col()] = s[kt][r];
     }
     __device__ __forceinline__ void scale(const Factor& f) {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f * s[kt][cg];
+        for (int kt = 0; kt < KT; ++kt) s[kt] = f * s[kt];
     }
-};
-
-// A wave's columns of v as operands, rows of 32 (16) tokens each.
-template <typename T, int VD>
-struct ValueFrags;
-template <int VD>
-struct ValueFrags<bf16, VD> {
-    static constexpr int CG = VD / 64, NS = 2;
-    bf16x8 f[NS][CG];
-    __device__ __forceinline__ void load(const bf16* tile) {
-        const int lane = threadIdx.x & 63, p = lane & 15, g = lane >> 4, w = threadIdx.x >> 6;
+    // the lane's offset in the tile of k, for add
+    __device__ static __forceinline__ int key_lane() {
+        if constexpr (sizeof(T) == 2) return across_lane<KD>(8 * (threadIdx.x & 3));
+        else return column_lane<KD>(threadIdx.x & 15);
+    }
+    // S += sum_j wt[j] k_j v_j^T over a chunk; v as operands
+    __device__ __forceinline__ void add(const char* kt_, int at, const typename Shape<T>::frag* v, const float* wt) {
+        const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
+        for (int s_ = 0; s_ < 2; ++s_) {
+            if constexpr (sizeof(T) == 2) {
+                f32x8 x = *reinterpret_cast<const f32x8*>(wt + 32 * s_ + 8 * g) * __builtin_convertvector(v[s_], f32x8);
+                const bf16x8 b0 = top(x);
+                x = rest(x, b0);
+                const bf16x8 b1 = top(x), b2 = top(rest(x, b1));
 #pragma unroll
-            for (int cg = 0; cg < CG; ++cg) {
-                const int row = 32 * s + 8 * g + (p >> 2), c = w * (VD / 4) + 16 * cg + 4 * (p & 3);
-                f[s][cg] = join(read_across(tile + Tile<bf16, VD>::el(row, c)),
-                                read_across(tile + Tile<bf16, VD>::el(row + 4, c)));
+                for (int kt = 0; kt < KT; ++kt) {
+                    const bf16x8 a = across_frag<KD>(kt_, at, s_, 64 * (kt >> 1), 8 * (kt & 1));
+                    s[kt] = mfma(a, b0, s[kt]);
+                    s[kt] = mfma(a, b1, s[kt]);
+                    s[kt] = mfma(a, b2, s[kt]);
+                }
+            } else {
+                const f32x4 b = *reinterpret_cast<const f32x4*>(wt + 16 * s_ + 4 * g) * v[s_];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) s[kt] = mfma(column_frag<KD>(kt_, at, s_, 64 * kt), b, s[kt]);
             }
-    }
-};
-template <int VD>
-struct ValueFrags<float, VD> {
-    static constexpr int CG = VD / 64, NS = 2;
-    f32x4 f[NS][CG];
-    __device__ __forceinline__ void load(const float* tile) {
-        const int lane = threadIdx.x & 63, p = lane & 15, g = lane >> 4, w = threadIdx.x >> 6;
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    f[s][cg][r] = tile[Tile<float, VD>::el(16 * s + 4 * g + r, w * (VD / 4) + 16 * cg + p)];
+        }
     }
 };
 
-// S += sum_j wt[j] k_j v_j^T over a chunk
-template <int KD, int VD>
-__device__ __forceinline__ void add_outer(State<bf16, KD, VD>& st, const bf16* kt_, const ValueFrags<bf16, VD>& v,
-                                          const float* wt) {
-    const int lane = threadIdx.x & 63, p = lane & 15, g = lane >> 4;
-    constexpr int CG = VD / 64;
+// The wave's 16 columns of v as operands, two blocks of tokens.
+template <typename T, int VD>
+__device__ __forceinline__ int value_lane() {
+    const int p = threadIdx.x & 15, w = threadIdx.x >> 6;
+    if constexpr (sizeof(T) == 2) return across_lane<VD>(16 * w + 4 * (p & 3));
+    else return column_lane<VD>(16 * w + p);
+}
+template <typename T, int VD>
+__device__ __forceinline__ void value_frags(const char* tile, int at, typename Shape<T>::frag* v) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const f32x8 w = *reinterpret_cast<const f32x8*>(wt + 32 * s + 8 * g);
-        bf16x8 b[CG][3];
-#pragma unroll
-        for (int cg = 0; cg < CG; ++cg) {
-            f32x8 x = w * __builtin_convertvector(v.f[s][cg], f32x8);
-            b[cg][0] = top(x);
-            x = rest(x, b[cg][0]);
-            b[cg][1] = top(x);
-            b[cg][2] = top(rest(x, b[cg][1]));
-        }
-        const int row = 32 * s + 8 * g + (p >> 2);
-#pragma unroll
-        for (int kt = 0; kt < KD / 16; ++kt) {
-            const int c = 32 * (kt >> 1) + 8 * (p & 3) + 4 * (kt & 1);
-            const bf16x8 a = join(read_across(kt_ + Tile<bf16, KD>::el(row, c)),
-                                  read_across(kt_ + Tile<bf16, KD>::el(row + 4, c)));
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg)
-#pragma unroll
-                for (int x = 0; x < 3; ++x) st.s[kt][cg] = mfma(a, b[cg][x], st.s[kt][cg]);
-        }
+        if constexpr (sizeof(T) == 2) v[s] = across_frag<VD>(tile, at, s, 0, 0);
+        else v[s] = column_frag<VD>(tile, at, s, 0);
     }
-}
-template <int KD, int VD>
-__device__ __forceinline__ void add_outer(State<float, KD, VD>& st, const float* kt_, const ValueFrags<float, VD>& v,
-                                          const float* wt) {
-    const int lane = threadIdx.x & 63, p = lane & 15, g = lane >> 4;
-    constexpr int CG = VD / 64;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const f32x4 w = *reinterpret_cast<const f32x4*>(wt + 16 * s + 4 * g);
-        f32x4 b[CG];
-#pragma unroll
-        for (int cg = 0; cg < CG; ++cg) b[cg] = w * v.f[s][cg];
-#pragma unroll
-        for (int kt = 0; kt < KD / 16; ++kt) {
-            f32x4 a;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a[r] = kt_[Tile<float, KD>::el(16 * s + 4 * g + r, 16 * kt + p)];
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) st.s[kt][cg] = mfma(a, b[cg], st.s[kt][cg]);
-        }
-    }
-}
-
-// row `16 it + p` of a tile as an operand, contraction block t
-template <int W>
-__device__ __forceinline__ bf16x8 row_frag(const bf16* tile, int it, int t) {
-    const int lane = threadIdx.x & 63;
-    return *reinterpret_cast<const bf16x8*>(tile + Tile<bf16, W>::at(16 * it + (lane & 15), 4 * t + (lane >> 4)));
-}
-template <int W>
-__device__ __forceinline__ f32x4 row_frag(const float* tile, int it, int t) {
-    const int lane = threadIdx.x & 63;
-    return *reinterpret_cast<const f32x4*>(tile + Tile<float, W>::at(16 * it + (lane & 15), 4 * t + (lane >> 4)));
 }
 
 // ------------------------------------------------------------------ kernels
 template <typename T, int KD, int VD>
-__global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
-    constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, CG = VD / 64;
+__global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um, LaJobs jobs) {
+    constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, NT = 4 * VD, WAVES = VD / 16;
     constexpr bool BF = sizeof(T) == 2;
-    __shared__ __attribute__((aligned(16))) T qt[C * KD];
-    __shared__ __attribute__((aligned(16))) T kt[C * KD];
-    __shared__ __attribute__((aligned(16))) T vt[C * VD];
-    __shared__ __attribute__((aligned(16))) T pt[BF ? 2 : 1][C * C];   // scores; bf16: in two terms
-    __shared__ __attribute__((aligned(32))) float wt[C];
-    __shared__ float pw[2 * C], rf[C];
+    constexpr int PB = C * C * sizeof(T);   // bytes of the scores; bf16: of each of their two terms
     using PT = Tile<T, C>;
+    using frag = typename Shape<T>::frag;
+    __shared__ __attribute__((aligned(32))) char qt[C * KD * sizeof(T)];
+    __shared__ __attribute__((aligned(32))) char kt[C * KD * sizeof(T)];
+    __shared__ __attribute__((aligned(32))) char vt[C * VD * sizeof(T)];
+    __shared__ __attribute__((aligned(32))) char pt[(BF ? 2 : 1) * PB];
+    __shared__ __attribute__((aligned(32))) float wt[C];
+    __shared__ float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
 
-    const int tid = threadIdx.x, lane = tid & 63, p = lane & 15, g = lane >> 4, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, p = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int id = xcd_order(blockIdx.x, gridDim.x);
     const LaJob& jb = jobs.job[id % jobs.n];
     const int h = (id / jobs.n) % um.H, seg_id = id / jobs.n / um.H;
@@ -391,24 +398,33 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
     const int seg0 = sg.index * um.seg_tokens;
     const int seg1 = min(sg.len, seg0 + um.seg_tokens);
     const int nch = seg1 > seg0 ? (seg1 - seg0 + C - 1) / C : 0;
+    const int last_shift = nch * C - max(0, seg1 - seg0);   // zero rows of the last chunk
 
-    Carrier<T, KD, C> cq, ck;
-    Carrier<T, VD, C> cv;
+    Carrier<T, KD, C, NT> cq, ck;
+    Carrier<T, VD, C, NT> cv;
+    cq.init(jb.q, h, sg.start, sg.len, jb.rev, seg0);
+    ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
+    cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
     auto fetch = [&](int c) {
-        const int t0 = seg0 + c * C, shift = max(0, C - (seg1 - t0));
-        cq.load(jb.q, h, sg.start, sg.len, jb.rev, t0 - shift, shift);
-        ck.load(jb.k, h, sg.start, sg.len, jb.rev, t0 - shift, shift);
-        cv.load(jb.v, h, sg.start, sg.len, jb.rev, t0 - shift, shift);
+        if (c + 1 < nch || last_shift == 0) {
+            cq.load();
+            ck.load();
+            cv.load();
+        } else {
+            cq.load_partial(last_shift);
+            ck.load_partial(last_shift);
+            cv.load_partial(last_shift);
+        }
     };
+    const int at_q = decltype(cq)::lane_at(), at_v = decltype(cv)::lane_at();
     auto stage = [&]() {
-        cq.store(qt);
-        ck.store(kt);
-        cv.store(vt);
+        cq.store(qt, at_q);
+        ck.store(kt, at_q);
+        cv.store(vt, at_v);
     };
     if (nch > 0) fetch(0);
 
     State<T, KD, VD> st;
-    const double gd = um.decay[h];
     {
         const float* from = nullptr;
         if (jb.slots) {
@@ -420,99 +436,88 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
         if (from) st.load(from, jb.transposed);
         else st.zero();
     }
+    const double gd = um.decay[h];
     for (int i = tid; i < 2 * C; i += NT) pw[i] = i < C ? 0.0f : (float)(jb.s_p * dpow(gd, i - C));
-    if (tid < C) {
-        wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
-        rf[tid] = (float)(jb.s_o * dpow(gd, tid + jb.e));
+    if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
+    if (tid < 2 * C) {
+        const int i = tid % C - (tid < C ? 0 : last_shift);
+        rf[tid / C][tid % C] = i < 0 ? 0.0f : (float)(jb.s_o * dpow(gd, i + jb.e));
     }
+    const Factor full(dpow(gd, C)), last(dpow(gd, C - last_shift));
     // score tiles above the diagonal that an operand reaches stay zero
-    for (int i = tid; i < (BF ? 2 : 1) * C * C / PT::EPU; i += NT)
-        reinterpret_cast<u32x4*>(&pt[0][0])[i] = u32x4{0, 0, 0, 0};
-    const Factor full(dpow(gd, C));
+    for (int i = tid; i < (BF ? 2 : 1) * PB / 16; i += NT) reinterpret_cast<u32x4*>(pt)[i] = u32x4{0, 0, 0, 0};
     if (nch > 0) stage();
     lds_barrier();
 
-    for (int c = 0; c < nch; ++c) {
-        const int t0 = seg0 + c * C, L = min(C, seg1 - t0), shift = C - L;
-        if (c + 1 < nch) fetch(c + 1);
-        if (L < C) {   // the last chunk of a unit
-            if (tid < C) rf[tid] = tid < shift ? 0.0f : (float)(jb.s_o * dpow(gd, tid - shift + jb.e));
-            lds_barrier();
-        }
+    const int row_at0 = row_lane<T, KD>(), key_at0 = State<T, KD, VD>::key_lane(), val_at0 = value_lane<T, VD>(),
+              p_at0 = row_lane<T, C>();
+    // the lane's part of row p of the first chunk's o, and the bytes of a row
+    const int64_t orow = (jb.rev ? -1 : 1) * (int64_t)um.H * VD * (jb.o_f32 ? 4 : 2);
+    char* op = static_cast<char*>(jb.o) +
+               (((jb.rev ? sg.start + sg.len - 1 : sg.start) * um.H + h) * VD + 16 * wave + 4 * g) * (jb.o_f32 ? 4 : 2) +
+               (seg0 + p) * orow;
 
-        // scores of the lower triangle, transposed: tile n of the list for wave n % 4
+    for (int c = 0; c < nch; ++c) {
+        const int shift = c + 1 < nch ? 0 : last_shift;
+        const float* rfc = rf[shift ? 1 : 0];
+        if (c + 1 < nch) fetch(c + 1);
+        const int row_at = fresh(row_at0), key_at = fresh(key_at0), val_at = fresh(val_at0), p_at = fresh(p_at0);
+
+        // scores of the lower triangle, transposed: tile n of the list for wave n % WAVES
         constexpr int TILES = IT * (IT + 1) / 2;
 #pragma unroll
-        for (int n0 = 0; n0 < TILES; n0 += 4) {
+        for (int n0 = 0; n0 < TILES; n0 += WAVES) {
             const int n = n0 + wave;
             if (n < TILES) {
                 const int it = BF ? (n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0) : (n >= 1 ? 1 : 0);
                 const int jt = n - it * (it + 1) / 2;
                 f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < KD / KS; ++t) acc = mfma(row_frag<KD>(kt, jt, t), row_frag<KD>(qt, it, t), acc);
-                const int gap = 16 * (it - jt) + p - 4 * g;
+                for (int t = 0; t < KD / KS; ++t)
+                    acc = mfma(row_frag<T, KD>(kt, row_at, jt, t), row_frag<T, KD>(qt, row_at, it, t), acc);
+                const float* pwl = pw + C + 16 * (it - jt) + p - 4 * g;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] *= pw[C + gap - r];
-                const int at = PT::el(16 * it + p, 16 * jt + 4 * g);
+                for (int r = 0; r < 4; ++r) acc[r] *= pwl[-r];
+                // row 16 it + p, columns 16 jt + 4 g ..
+                const int at = 16 * it * PT::RB + PT::at(p, (16 * jt + 4 * g) / PT::EPU) + (16 * jt + 4 * g) % PT::EPU * (int)sizeof(T);
                 if constexpr (BF) {
                     const bf16x4 hi = __builtin_convertvector(acc, bf16x4);
-                    *reinterpret_cast<bf16x4*>(&pt[0][at]) = hi;
-                    *reinterpret_cast<bf16x4*>(&pt[1][at]) =
+                    *reinterpret_cast<bf16x4*>(pt + at) = hi;
+                    *reinterpret_cast<bf16x4*>(pt + PB + at) =
                         __builtin_convertvector(acc - __builtin_convertvector(hi, f32x4), bf16x4);
                 } else {
-                    *reinterpret_cast<f32x4*>(&pt[0][at]) = acc;
+                    *reinterpret_cast<f32x4*>(pt + at) = acc;
                 }
             }
         }
 
-        ValueFrags<T, VD> vf;
-        vf.load(vt);
-
         // o^T = (q S)^T, rows scaled by their distance from the chunk's start
-        f32x4 o[IT][CG];
+        f32x4 o[IT];
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) o[it][cg] = f32x4{0, 0, 0, 0};
+        for (int it = 0; it < IT; ++it) o[it] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < KD / KS; ++t) {
             if constexpr (BF) {
-                bf16x8 hi[CG], lo[CG];
-#pragma unroll
-                for (int cg = 0; cg < CG; ++cg) {
-                    const f32x8 x = __builtin_shufflevector(st.s[2 * t][cg], st.s[2 * t + 1][cg], 0, 1, 2, 3, 4, 5, 6, 7);
-                    hi[cg] = top(x);
-                    lo[cg] = top(rest(x, hi[cg]));
-                }
+                const f32x8 x = __builtin_shufflevector(st.s[2 * t], st.s[2 * t + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+                const bf16x8 hi = top(x), lo = top(rest(x, hi));
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    const bf16x8 b = row_frag<KD>(qt, it, t);
-#pragma unroll
-                    for (int cg = 0; cg < CG; ++cg) {
-                        o[it][cg] = mfma(hi[cg], b, o[it][cg]);
-                        o[it][cg] = mfma(lo[cg], b, o[it][cg]);
-                    }
+                    const bf16x8 b = row_frag<T, KD>(qt, row_at, it, t);
+                    o[it] = mfma(hi, b, o[it]);
+                    o[it] = mfma(lo, b, o[it]);
                 }
             } else {
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const f32x4 b = row_frag<KD>(qt, it, t);
-#pragma unroll
-                    for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(st.s[t][cg], b, o[it][cg]);
-                }
+                for (int it = 0; it < IT; ++it) o[it] = mfma(st.s[t], row_frag<T, KD>(qt, row_at, it, t), o[it]);
             }
         }
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const float f = rf[16 * it + p];
-#pragma unroll
-            for (int cg = 0; cg < CG; ++cg) o[it][cg] *= f;
-        }
+        for (int it = 0; it < IT; ++it) o[it] *= rfc[16 * it + p];
 
-        if (L < C) st.scale(Factor(dpow(gd, L)));
-        else st.scale(full);
-        add_outer<KD, VD>(st, kt, vf, wt);
+        frag vf[2];
+        value_frags<T, VD>(vt, val_at, vf);
+        st.scale(shift ? last : full);
+        st.add(kt, key_at, vf, wt);
 
         lds_barrier();   // scores written, tiles read
         if (c + 1 < nch) stage();
@@ -520,34 +525,16 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
         for (int it = 0; it < IT; ++it) {
 #pragma unroll
             for (int s = 0; s <= (it * 16) / KS; ++s) {
-                if constexpr (BF) {
-                    const bf16x8 hi = row_frag<C>(pt[0], it, s), lo = row_frag<C>(pt[1], it, s);
-#pragma unroll
-                    for (int cg = 0; cg < CG; ++cg) {
-                        o[it][cg] = mfma(vf.f[s][cg], hi, o[it][cg]);
-                        o[it][cg] = mfma(vf.f[s][cg], lo, o[it][cg]);
-                    }
-                } else {
-                    const f32x4 b = row_frag<C>(pt[0], it, s);
-#pragma unroll
-                    for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(vf.f[s][cg], b, o[it][cg]);
-                }
+                o[it] = mfma(vf[s], row_frag<T, C>(pt, p_at, it, s), o[it]);
+                if constexpr (BF) o[it] = mfma(vf[s], row_frag<T, C>(pt + PB, p_at, it, s), o[it]);
             }
-            const int row = 16 * it + p;
-            if (row >= shift) {
-                const int64_t t = (int64_t)t0 + row - shift;
-                const int64_t tok = jb.rev ? sg.start + sg.len - 1 - t : sg.start + t;
-                const int64_t at = (tok * um.H + h) * VD + wave * (VD / 4) + 4 * g;
-#pragma unroll
-                for (int cg = 0; cg < CG; ++cg) {
-                    if (jb.o_f32)
-                        *reinterpret_cast<f32x4*>(static_cast<float*>(jb.o) + at + 16 * cg) = o[it][cg];
-                    else
-                        *reinterpret_cast<bf16x4*>(static_cast<bf16*>(jb.o) + at + 16 * cg) =
-                            __builtin_convertvector(o[it][cg], bf16x4);
-                }
+            if (16 * it + p >= shift) {
+                char* to = op + (16 * it - shift) * orow;
+                if (jb.o_f32) *reinterpret_cast<f32x4*>(to) = o[it];
+                else *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(o[it], bf16x4);
             }
         }
+        op += C * orow;
         lds_barrier();   // scores read, the next tiles written
     }
 
@@ -560,10 +547,10 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
 // A segment's own contribution to the state after it, into the next slot of
 // its unit. The last segment of a unit has no next one.
 template <typename T, int KD, int VD>
-__global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
-    constexpr int C = Shape<T>::C;
-    __shared__ __attribute__((aligned(16))) T kt[2][C * KD];
-    __shared__ __attribute__((aligned(16))) T vt[2][C * VD];
+__global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_summary(LaUnits um, LaJobs jobs) {
+    constexpr int C = Shape<T>::C, NT = 4 * VD;
+    __shared__ __attribute__((aligned(32))) char kt[2][C * KD * sizeof(T)];
+    __shared__ __attribute__((aligned(32))) char vt[2][C * VD * sizeof(T)];
     __shared__ __attribute__((aligned(32))) float wt[C];
     const int tid = threadIdx.x;
     const int id = xcd_order(blockIdx.x, gridDim.x);
@@ -572,27 +559,32 @@ __global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
     const Seg sg = find_seg(um, seg_id);
     if (sg.unit < 0 || sg.index == sg.count - 1 || seg_id + 1 >= um.n_segs) return;
     const int seg0 = sg.index * um.seg_tokens, nch = um.seg_tokens / C;
-    Carrier<T, KD, C> ck;
-    Carrier<T, VD, C> cv;
-    ck.load(jb.k, h, sg.start, sg.len, jb.rev, seg0, 0);
-    cv.load(jb.v, h, sg.start, sg.len, jb.rev, seg0, 0);
+    Carrier<T, KD, C, NT> ck;
+    Carrier<T, VD, C, NT> cv;
+    ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
+    cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
+    ck.load();
+    cv.load();
+    const int at_k = decltype(ck)::lane_at(), at_v = decltype(cv)::lane_at();
+    const int key_at0 = State<T, KD, VD>::key_lane(), val_at0 = value_lane<T, VD>();
     const double gd = um.decay[h];
     if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
     const Factor full(dpow(gd, C));
     State<T, KD, VD> st;
     st.zero();
     for (int c = 0; c < nch; ++c) {
-        ck.store(kt[c & 1]);
-        cv.store(vt[c & 1]);
+        ck.store(kt[c & 1], at_k);
+        cv.store(vt[c & 1], at_v);
         if (c + 1 < nch) {
-            ck.load(jb.k, h, sg.start, sg.len, jb.rev, seg0 + (c + 1) * C, 0);
-            cv.load(jb.v, h, sg.start, sg.len, jb.rev, seg0 + (c + 1) * C, 0);
+            ck.load();
+            cv.load();
         }
         lds_barrier();
-        ValueFrags<T, VD> vf;
-        vf.load(vt[c & 1]);
+        const int key_at = fresh(key_at0), val_at = fresh(val_at0);
+        typename Shape<T>::frag vf[2];
+        value_frags<T, VD>(vt[c & 1], val_at, vf);
         st.scale(full);
-        add_outer<KD, VD>(st, kt[c & 1], vf, wt);
+        st.add(kt[c & 1], key_at, vf, wt);
     }
     st.store(jb.slots + ((int64_t)(seg_id + 1) * um.H + h) * (KD * VD));
 }
@@ -662,20 +654,20 @@ __global__ __launch_bounds__(NT) void la_group(const float* x, T* out, int64_t n
 template <typename T>
 hipError_t main_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    if (K == 128 && V == 128) la_main<T, 128, 128><<<n, NT, 0, s>>>(u, j);
-    else if (K == 128) la_main<T, 128, 64><<<n, NT, 0, s>>>(u, j);
-    else if (V == 128) la_main<T, 64, 128><<<n, NT, 0, s>>>(u, j);
-    else la_main<T, 64, 64><<<n, NT, 0, s>>>(u, j);
+    if (K == 128 && V == 128) la_main<T, 128, 128><<<n, 512, 0, s>>>(u, j);
+    else if (K == 128) la_main<T, 128, 64><<<n, 256, 0, s>>>(u, j);
+    else if (V == 128) la_main<T, 64, 128><<<n, 512, 0, s>>>(u, j);
+    else la_main<T, 64, 64><<<n, 256, 0, s>>>(u, j);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t summary_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    if (K == 128 && V == 128) la_summary<T, 128, 128><<<n, NT, 0, s>>>(u, j);
-    else if (K == 128) la_summary<T, 128, 64><<<n, NT, 0, s>>>(u, j);
-    else if (V == 128) la_summary<T, 64, 128><<<n, NT, 0, s>>>(u, j);
-    else la_summary<T, 64, 64><<<n, NT, 0, s>>>(u, j);
+    if (K == 128 && V == 128) la_summary<T, 128, 128><<<n, 512, 0, s>>>(u, j);
+    else if (K == 128) la_summary<T, 128, 64><<<n, 256, 0, s>>>(u, j);
+    else if (V == 128) la_summary<T, 64, 128><<<n, 512, 0, s>>>(u, j);
+    else la_summary<T, 64, 64><<<n, 256, 0, s>>>(u, j);
     return hipGetLastError();
 }
 
