@@ -47,7 +47,10 @@ __device__ __forceinline__ double dpow(double g, int64_t n) { return n == 0 ? 1.
 // over a long sequence does not add its own rounding up
 struct Factor {
     float hi, lo;
-    __device__ explicit Factor(double x) : hi((float)x), lo((float)(x - (double)(float)x)) {}
+    __device__ explicit Factor(double x) {   // x wave-uniform
+        hi = u2f(__builtin_amdgcn_readfirstlane(f2u((float)x)));
+        lo = u2f(__builtin_amdgcn_readfirstlane(f2u((float)(x - (double)(float)x))));
+    }
     __device__ __forceinline__ f32x4 operator*(f32x4 x) const {
         f32x4 y;
 #pragma unroll
@@ -138,9 +141,8 @@ __device__ __forceinline__ int page_of(const int32_t* pages, int unit, int n_pag
 // XOR with the row number, so that 16 rows read at one column and 4 rows read
 // across both spread over the banks. Everything a lane reads of a tile is at
 // one byte offset of the lane, XOR a multiple of 16 below the row length,
-// plus a constant; the offsets are made anew from the lane's in each chunk
-// (fresh), since holding all of them would cost more registers than the
-// state does.
+// plus a constant; the offsets are made anew from the thread's number in each
+// chunk (fresh), since held in registers they would cost more than the state.
 template <typename T, int W>
 struct Tile {
     static constexpr int EPU = 16 / sizeof(T);
@@ -168,37 +170,35 @@ struct Carrier {
     static constexpr int N = C / STEP;
     static_assert(N >= 1 && (STEP & (STEP - 1)) == 0, "");
     u32x4 x[N];
-    const char* p;        // row0 of the next full chunk
-    int64_t step, chunk;  // bytes to the next row of this thread, to the next chunk
+    const char* p;        // the next chunk's lowest token (wave-uniform)
+    int64_t row;          // bytes from a tile row to the next (negative in reversed time)
 
-    // time of the first tile row: t0
+    // t0: time of the first tile row
     __device__ __forceinline__ void init(const RowsOf& r, int h, int64_t start, int len, int rev, int t0) {
-        const int row0 = threadIdx.x / TL::UNITS, unit = threadIdx.x % TL::UNITS;
-        const int64_t t = (int64_t)t0 + row0;
-        const int64_t tok = rev ? start + len - 1 - t : start + t;
-        p = static_cast<const char*>(r.p) + (tok * r.ts + (int64_t)(h / r.share) * r.hs + unit * TL::EPU) * (int)sizeof(T);
-        step = (rev ? -STEP : STEP) * r.ts * (int)sizeof(T);
-        chunk = step * N;
+        const int64_t low = rev ? start + len - t0 - C : start + t0;
+        p = static_cast<const char*>(r.p) + (low * r.ts + (int64_t)(h / r.share) * r.hs) * (int)sizeof(T);
+        row = (rev ? -r.ts : r.ts) * (int)sizeof(T);
     }
-    __device__ __forceinline__ void load() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const u32x4*>(p + i * step);
-        p += chunk;
-    }
-    // a last, partial chunk: its first row is tile row `shift`, zero rows before
-    __device__ __forceinline__ void load_partial(int shift) {
-        const int row0 = threadIdx.x / TL::UNITS;
-        const char* q = p - shift * (step / STEP);
+    // shift: the chunk's first row is tile row `shift`; the rows before it
+    // are loaded from it and zeroed when they are stored
+    __device__ __forceinline__ void load(int shift, int tid) {
+        const int row0 = tid / TL::UNITS, unit = tid % TL::UNITS;
+        const char* q = p - shift * row;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[i] = u32x4{0, 0, 0, 0};
-            if (row0 + i * STEP >= shift) x[i] = *reinterpret_cast<const u32x4*>(q + i * step);
+            const int r = max(row0 + i * STEP, shift);
+            const uint32_t at = (uint32_t)(row < 0 ? C - 1 - r : r) * (uint32_t)(row < 0 ? -row : row) + 16 * unit;
+            x[i] = *reinterpret_cast<const u32x4*>(q + at);
         }
+        p += C * row;
     }
-    __device__ static __forceinline__ int lane_at() {
-        return TL::at(threadIdx.x / TL::UNITS, threadIdx.x % TL::UNITS);
-    }
-    __device__ __forceinline__ void store(char* tile, int at) const {
+    __device__ __forceinline__ void store(char* tile, int shift, int tid) {
+        if (shift) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (tid / TL::UNITS + i * STEP < shift) x[i] = u32x4{0, 0, 0, 0};
+        }
+        const int at = TL::at(tid / TL::UNITS, tid % TL::UNITS);
 #pragma unroll
         for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (at ^ ((i * STEP & TL::MASK) * 16)) + i * STEP * TL::RB) = x[i];
     }
@@ -245,10 +245,10 @@ struct Shape<float> {
 };
 
 // Row 16 it + p of a tile as an operand, contraction block t; at:
-// row_lane<T, W>()
+// row_lane<T, W>(tid)
 template <typename T, int W>
-__device__ __forceinline__ int row_lane() {
-    return Tile<T, W>::at(threadIdx.x & 15, (threadIdx.x & 63) >> 4);
+__device__ __forceinline__ int row_lane(int tid) {
+    return Tile<T, W>::at(tid & 15, (tid & 63) >> 4);
 }
 template <typename T, int W>
 __device__ __forceinline__ typename Shape<T>::frag row_frag(const char* tile, int at, int it, int t) {
@@ -259,8 +259,8 @@ __device__ __forceinline__ typename Shape<T>::frag row_frag(const char* tile, in
 // them). bf16: c0's columns are four groups of four that the lanes p % 4
 // name, GAP apart; across_lane gives the address of the lane's group.
 template <int W>
-__device__ __forceinline__ int across_lane(int col) {   // col: of this lane's group
-    const int p = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ int across_lane(int tid, int col) {   // col: of this lane's group
+    const int p = tid & 15, g = (tid & 63) >> 4;
     return Tile<bf16, W>::at(8 * g + (p >> 2), col / 8) + col % 8 * 2;
 }
 template <int W>
@@ -271,8 +271,8 @@ __device__ __forceinline__ bf16x8 across_frag(const char* tile, int at, int s, i
                 read_across(tile, (at ^ flip ^ 64) + (32 * s + 4) * RB + add));
 }
 template <int W>
-__device__ __forceinline__ int column_lane(int col) {   // col: of this lane
-    const int g = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ int column_lane(int tid, int col) {   // col: of this lane
+    const int g = (tid & 63) >> 4;
     return Tile<float, W>::at(4 * g, col / 4) + col % 4 * 4;
 }
 template <int W>
@@ -327,13 +327,13 @@ struct State {
         for (int kt = 0; kt < KT; ++kt) s[kt] = f * s[kt];
     }
     // the lane's offset in the tile of k, for add
-    __device__ static __forceinline__ int key_lane() {
-        if constexpr (sizeof(T) == 2) return across_lane<KD>(8 * (threadIdx.x & 3));
-        else return column_lane<KD>(threadIdx.x & 15);
+    __device__ static __forceinline__ int key_lane(int tid) {
+        if constexpr (sizeof(T) == 2) return across_lane<KD>(tid, 8 * (tid & 3));
+        else return column_lane<KD>(tid, tid & 15);
     }
     // S += sum_j wt[j] k_j v_j^T over a chunk; v as operands
-    __device__ __forceinline__ void add(const char* kt_, int at, const typename Shape<T>::frag* v, const float* wt) {
-        const int g = (threadIdx.x & 63) >> 4;
+    __device__ __forceinline__ void add(const char* kt_, int tid, const typename Shape<T>::frag* v, const float* wt) {
+        const int at = key_lane(tid), g = (tid & 63) >> 4;
 #pragma unroll
         for (int s_ = 0; s_ < 2; ++s_) {
             if constexpr (sizeof(T) == 2) {
@@ -359,13 +359,11 @@ struct State {
 
 // The wave's 16 columns of v as operands, two blocks of tokens.
 template <typename T, int VD>
-__device__ __forceinline__ int value_lane() {
-    const int p = threadIdx.x & 15, w = threadIdx.x >> 6;
-    if constexpr (sizeof(T) == 2) return across_lane<VD>(16 * w + 4 * (p & 3));
-    else return column_lane<VD>(16 * w + p);
-}
-template <typename T, int VD>
-__device__ __forceinline__ void value_frags(const char* tile, int at, typename Shape<T>::frag* v) {
+__device__ __forceinline__ void value_frags(const char* tile, int tid, typename Shape<T>::frag* v) {
+    const int p = tid & 15, w = tid >> 6;
+    int at;
+    if constexpr (sizeof(T) == 2) at = across_lane<VD>(tid, 16 * w + 4 * (p & 3));
+    else at = column_lane<VD>(tid, 16 * w + p);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if constexpr (sizeof(T) == 2) v[s] = across_frag<VD>(tile, at, s, 0, 0);
@@ -388,8 +386,7 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     __shared__ __attribute__((aligned(32))) float wt[C];
     __shared__ float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
 
-    const int tid = threadIdx.x, lane = tid & 63, p = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int id = xcd_order(blockIdx.x, gridDim.x);
     const LaJob& jb = jobs.job[id % jobs.n];
     const int h = (id / jobs.n) % um.H, seg_id = id / jobs.n / um.H;
@@ -405,24 +402,18 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     cq.init(jb.q, h, sg.start, sg.len, jb.rev, seg0);
     ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
-    auto fetch = [&](int c) {
-        if (c + 1 < nch || last_shift == 0) {
-            cq.load();
-            ck.load();
-            cv.load();
-        } else {
-            cq.load_partial(last_shift);
-            ck.load_partial(last_shift);
-            cv.load_partial(last_shift);
-        }
+    auto shift_of = [&](int c) { return c + 1 < nch ? 0 : last_shift; };
+    auto fetch = [&](int c, int tid) {
+        cq.load(shift_of(c), tid);
+        ck.load(shift_of(c), tid);
+        cv.load(shift_of(c), tid);
     };
-    const int at_q = decltype(cq)::lane_at(), at_v = decltype(cv)::lane_at();
-    auto stage = [&]() {
-        cq.store(qt, at_q);
-        ck.store(kt, at_q);
-        cv.store(vt, at_v);
+    auto stage = [&](int c, int tid) {
+        cq.store(qt, shift_of(c), tid);
+        ck.store(kt, shift_of(c), tid);
+        cv.store(vt, shift_of(c), tid);
     };
-    if (nch > 0) fetch(0);
+    if (nch > 0) fetch(0, tid);
 
     State<T, KD, VD> st;
     {
@@ -446,22 +437,21 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     const Factor full(dpow(gd, C)), last(dpow(gd, C - last_shift));
     // score tiles above the diagonal that an operand reaches stay zero
     for (int i = tid; i < (BF ? 2 : 1) * PB / 16; i += NT) reinterpret_cast<u32x4*>(pt)[i] = u32x4{0, 0, 0, 0};
-    if (nch > 0) stage();
+    if (nch > 0) stage(0, tid);
     lds_barrier();
 
-    const int row_at0 = row_lane<T, KD>(), key_at0 = State<T, KD, VD>::key_lane(), val_at0 = value_lane<T, VD>(),
-              p_at0 = row_lane<T, C>();
-    // the lane's part of row p of the first chunk's o, and the bytes of a row
-    const int64_t orow = (jb.rev ? -1 : 1) * (int64_t)um.H * VD * (jb.o_f32 ? 4 : 2);
+    // o: bytes from a row to the next, the lowest of the next 16 rows, the lane's part from there
+    const int es = jb.o_f32 ? 4 : 2;
+    const int64_t orow = (jb.rev ? -1 : 1) * (int64_t)um.H * VD * es;
     char* op = static_cast<char*>(jb.o) +
-               (((jb.rev ? sg.start + sg.len - 1 : sg.start) * um.H + h) * VD + 16 * wave + 4 * g) * (jb.o_f32 ? 4 : 2) +
-               (seg0 + p) * orow;
+               ((jb.rev ? sg.start + sg.len - seg0 - 16 : sg.start + seg0) * um.H + h) * (VD * es);
 
     for (int c = 0; c < nch; ++c) {
-        const int shift = c + 1 < nch ? 0 : last_shift;
+        const int shift = shift_of(c);
         const float* rfc = rf[shift ? 1 : 0];
-        if (c + 1 < nch) fetch(c + 1);
-        const int row_at = fresh(row_at0), key_at = fresh(key_at0), val_at = fresh(val_at0), p_at = fresh(p_at0);
+        if (c + 1 < nch) fetch(c + 1, fresh(tid));
+        const int t_ = fresh(tid), p = t_ & 15, g = (t_ & 63) >> 4;
+        const int row_at = row_lane<T, KD>(t_);
 
         // scores of the lower triangle, transposed: tile n of the list for wave n % WAVES
         constexpr int TILES = IT * (IT + 1) / 2;
@@ -491,6 +481,10 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
             }
         }
 
+        frag vf[2];
+        value_frags<T, VD>(vt, t_, vf);
+        lds_barrier();   // scores written
+
         // o^T = (q S)^T, rows scaled by their distance from the chunk's start
         f32x4 o[IT];
 #pragma unroll
@@ -514,13 +508,8 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
 #pragma unroll
         for (int it = 0; it < IT; ++it) o[it] *= rfc[16 * it + p];
 
-        frag vf[2];
-        value_frags<T, VD>(vt, val_at, vf);
-        st.scale(shift ? last : full);
-        st.add(kt, key_at, vf, wt);
-
-        lds_barrier();   // scores written, tiles read
-        if (c + 1 < nch) stage();
+        const int p_at = row_lane<T, C>(t_);
+        const uint32_t o_at = (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * VD * es) + (16 * wave + 4 * g) * es;
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
 #pragma unroll
@@ -529,13 +518,20 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
                 if constexpr (BF) o[it] = mfma(vf[s], row_frag<T, C>(pt + PB, p_at, it, s), o[it]);
             }
             if (16 * it + p >= shift) {
-                char* to = op + (16 * it - shift) * orow;
+                char* to = op + (16 * it - shift) * orow + o_at;
                 if (jb.o_f32) *reinterpret_cast<f32x4*>(to) = o[it];
                 else *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(o[it], bf16x4);
             }
         }
         op += C * orow;
-        lds_barrier();   // scores read, the next tiles written
+
+        st.scale(shift ? last : full);
+        st.add(kt, fresh(tid), vf, wt);
+        if (c + 1 < nch) {
+            lds_barrier();   // scores and tiles read
+            stage(c + 1, fresh(tid));
+            lds_barrier();
+        }
     }
 
     if (jb.s_out && sg.index == sg.count - 1) {
@@ -563,28 +559,26 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_summary(LaUnits 
     Carrier<T, VD, C, NT> cv;
     ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
-    ck.load();
-    cv.load();
-    const int at_k = decltype(ck)::lane_at(), at_v = decltype(cv)::lane_at();
-    const int key_at0 = State<T, KD, VD>::key_lane(), val_at0 = value_lane<T, VD>();
+    ck.load(0, tid);
+    cv.load(0, tid);
     const double gd = um.decay[h];
     if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
     const Factor full(dpow(gd, C));
     State<T, KD, VD> st;
     st.zero();
     for (int c = 0; c < nch; ++c) {
-        ck.store(kt[c & 1], at_k);
-        cv.store(vt[c & 1], at_v);
+        const int t_ = fresh(tid);
+        ck.store(kt[c & 1], 0, t_);
+        cv.store(vt[c & 1], 0, t_);
         if (c + 1 < nch) {
-            ck.load();
-            cv.load();
+            ck.load(0, t_);
+            cv.load(0, t_);
         }
         lds_barrier();
-        const int key_at = fresh(key_at0), val_at = fresh(val_at0);
         typename Shape<T>::frag vf[2];
-        value_frags<T, VD>(vt[c & 1], val_at, vf);
+        value_frags<T, VD>(vt[c & 1], t_, vf);
         st.scale(full);
-        st.add(kt[c & 1], key_at, vf, wt);
+        st.add(kt[c & 1], fresh(tid), vf, wt);
     }
     st.store(jb.slots + ((int64_t)(seg_id + 1) * um.H + h) * (KD * VD));
 }

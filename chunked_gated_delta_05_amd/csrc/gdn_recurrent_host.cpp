@@ -60,6 +60,12 @@ gdn_status check_prompt(const gdn_linattn_desc* d, Prompt* p) {
     if (!strides_ok(d->q_stride, p->tokens, d->Hq, d->dtype) || !strides_ok(d->k_stride, p->tokens, d->Hk, d->dtype) ||
         !strides_ok(d->v_stride, p->tokens, d->Hv, d->dtype))
         return GDN_ERR_INVALID;
+    // a chunk's rows are reached by 32-bit offsets
+    const int64_t span = (int64_t(1) << 31) / kChunk;
+    const int64_t es = elem_bytes(d->dtype);
+    if (int64_t(d->H) * 128 * 4 > span || d->q_stride[0] * es > span || d->k_stride[0] * es > span ||
+        d->v_stride[0] * es > span)
+        return GDN_ERR_UNSUPPORTED;
     LaUnits& u = p->u;
     u.H = d->H;
     u.T = d->T;

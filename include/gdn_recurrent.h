@@ -47,7 +47,8 @@ extern "C" {
  * q, k and v may each have fewer heads than H (Hq, Hk, Hv dividing H): head h
  * reads head h / (H / Hx). Rows (the K or V values of one token and head) are
  * contiguous; tokens and heads may lie at any distance that keeps every row
- * 16-byte aligned (strides in elements).
+ * 16-byte aligned (strides in elements); a token stride of 32 MiB or more,
+ * or 65536 heads, is GDN_ERR_UNSUPPORTED.
  *
  * Sequences are the B rows of T tokens (n_units = 0) or packed documents of
  * one row, offsets as in gdn_desc (a sequence's tokens are contiguous).
