@@ -36,6 +36,7 @@ constexpr int NXCD = 8;
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 // d^n of a log decay g, in fp64: n runs over whole sequences, and the error
@@ -169,7 +170,9 @@ struct Carrier {
     static constexpr int STEP = NT / TL::UNITS;
     static constexpr int N = C / STEP;
     static_assert(N >= 1 && (STEP & (STEP - 1)) == 0, "");
-    u32x4 x[N];
+    struct Data {
+        u32x4 x[N];
+    };
     const char* p;        // the next chunk's lowest token (wave-uniform)
     int64_t row;          // bytes from a tile row to the next (negative in reversed time)
 
@@ -181,26 +184,26 @@ struct Carrier {
     }
     // shift: the chunk's first row is tile row `shift`; the rows before it
     // are loaded from it and zeroed when they are stored
-    __device__ __forceinline__ void load(int shift, int tid) {
+    __device__ __forceinline__ void load(Data& d, int shift, int tid) {
         const int row0 = tid / TL::UNITS, unit = tid % TL::UNITS;
         const char* q = p - shift * row;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int r = max(row0 + i * STEP, shift);
             const uint32_t at = (uint32_t)(row < 0 ? C - 1 - r : r) * (uint32_t)(row < 0 ? -row : row) + 16 * unit;
-            x[i] = *reinterpret_cast<const u32x4*>(q + at);
+            d.x[i] = *reinterpret_cast<const u32x4*>(q + at);
         }
         p += C * row;
     }
-    __device__ __forceinline__ void store(char* tile, int shift, int tid) {
+    __device__ static __forceinline__ void store(Data& d, char* tile, int shift, int tid) {
         if (shift) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (tid / TL::UNITS + i * STEP < shift) x[i] = u32x4{0, 0, 0, 0};
+                if (tid / TL::UNITS + i * STEP < shift) d.x[i] = u32x4{0, 0, 0, 0};
         }
         const int at = TL::at(tid / TL::UNITS, tid % TL::UNITS);
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (at ^ ((i * STEP & TL::MASK) * 16)) + i * STEP * TL::RB) = x[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (at ^ ((i * STEP & TL::MASK) * 16)) + i * STEP * TL::RB) = d.x[i];
     }
 };
 
@@ -226,8 +229,28 @@ __device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-__device__ __forceinline__ bf16x8 top(f32x8 x) { return __builtin_convertvector(x, bf16x8); }
-__device__ __forceinline__ f32x8 rest(f32x8 x, bf16x8 t) { return x - __builtin_convertvector(t, f32x8); }
+// The leading bf16 term of x, with x left holding what it leaves. The pairs'
+// bits are taken apart by hand: from the vector conversion the compiler
+// converts every element a second time.
+template <int N>
+struct Term {
+    typedef bf16 vec __attribute__((ext_vector_type(N)));
+    typedef float wide __attribute__((ext_vector_type(N)));
+    typedef uint32_t words __attribute__((ext_vector_type(N / 2)));
+};
+template <int N>
+__device__ __forceinline__ typename Term<N>::vec split(typename Term<N>::wide& x) {
+    typename Term<N>::words w;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const f32x2 y = {x[2 * i], x[2 * i + 1]};
+        const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
+        w[i] = u;
+        x[2 * i] -= u2f(u << 16);
+        x[2 * i + 1] -= u2f(u & 0xffff0000u);
+    }
+    return __builtin_bit_cast(typename Term<N>::vec, w);
+}
 
 template <typename T>
 struct Shape;
@@ -338,9 +361,7 @@ struct State {
         for (int s_ = 0; s_ < 2; ++s_) {
             if constexpr (sizeof(T) == 2) {
                 f32x8 x = *reinterpret_cast<const f32x8*>(wt + 32 * s_ + 8 * g) * __builtin_convertvector(v[s_], f32x8);
-                const bf16x8 b0 = top(x);
-                x = rest(x, b0);
-                const bf16x8 b1 = top(x), b2 = top(rest(x, b1));
+                const bf16x8 b0 = split<8>(x), b1 = split<8>(x), b2 = __builtin_convertvector(x, bf16x8);
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     const bf16x8 a = across_frag<KD>(kt_, at, s_, 64 * (kt >> 1), 8 * (kt & 1));
@@ -403,17 +424,24 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
     auto shift_of = [&](int c) { return c + 1 < nch ? 0 : last_shift; };
-    auto fetch = [&](int c, int tid) {
-        cq.load(shift_of(c), tid);
-        ck.load(shift_of(c), tid);
-        cv.load(shift_of(c), tid);
+    // the data of a chunk lives from its fetch to its staging only, so that
+    // nothing but the staging waits for it
+    struct Data {
+        typename Carrier<T, KD, C, NT>::Data q, k;
+        typename Carrier<T, VD, C, NT>::Data v;
     };
-    auto stage = [&](int c, int tid) {
-        cq.store(qt, shift_of(c), tid);
-        ck.store(kt, shift_of(c), tid);
-        cv.store(vt, shift_of(c), tid);
+    auto fetch = [&](Data& d, int c, int tid) {
+        cq.load(d.q, shift_of(c), tid);
+        ck.load(d.k, shift_of(c), tid);
+        cv.load(d.v, shift_of(c), tid);
     };
-    if (nch > 0) fetch(0, tid);
+    auto stage = [&](Data& d, int c, int tid) {
+        cq.store(d.q, qt, shift_of(c), tid);
+        ck.store(d.k, kt, shift_of(c), tid);
+        cv.store(d.v, vt, shift_of(c), tid);
+    };
+    Data first;
+    if (nch > 0) fetch(first, 0, tid);
 
     State<T, KD, VD> st;
     {
@@ -437,7 +465,10 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     const Factor full(dpow(gd, C)), last(dpow(gd, C - last_shift));
     // score tiles above the diagonal that an operand reaches stay zero
     for (int i = tid; i < (BF ? 2 : 1) * PB / 16; i += NT) reinterpret_cast<u32x4*>(pt)[i] = u32x4{0, 0, 0, 0};
-    if (nch > 0) stage(0, tid);
+    if (nch > 0) stage(first, 0, tid);
+    // the state's loads end here: a wait for them inside the loop would also
+    // wait for the next chunk's
+    __builtin_amdgcn_s_waitcnt(0);
     lds_barrier();
 
     // o: bytes from a row to the next, the lowest of the next 16 rows, the lane's part from there
@@ -449,7 +480,8 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     for (int c = 0; c < nch; ++c) {
         const int shift = shift_of(c);
         const float* rfc = rf[shift ? 1 : 0];
-        if (c + 1 < nch) fetch(c + 1, fresh(tid));
+        Data next;
+        if (c + 1 < nch) fetch(next, c + 1, fresh(tid));
         const int t_ = fresh(tid), p = t_ & 15, g = (t_ & 63) >> 4;
         const int row_at = row_lane<T, KD>(t_);
 
@@ -471,10 +503,8 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
                 // row 16 it + p, columns 16 jt + 4 g ..
                 const int at = 16 * it * PT::RB + PT::at(p, (16 * jt + 4 * g) / PT::EPU) + (16 * jt + 4 * g) % PT::EPU * (int)sizeof(T);
                 if constexpr (BF) {
-                    const bf16x4 hi = __builtin_convertvector(acc, bf16x4);
-                    *reinterpret_cast<bf16x4*>(pt + at) = hi;
-                    *reinterpret_cast<bf16x4*>(pt + PB + at) =
-                        __builtin_convertvector(acc - __builtin_convertvector(hi, f32x4), bf16x4);
+                    *reinterpret_cast<bf16x4*>(pt + at) = split<4>(acc);
+                    *reinterpret_cast<bf16x4*>(pt + PB + at) = __builtin_convertvector(acc, bf16x4);
                 } else {
                     *reinterpret_cast<f32x4*>(pt + at) = acc;
                 }
@@ -492,8 +522,8 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
 #pragma unroll
         for (int t = 0; t < KD / KS; ++t) {
             if constexpr (BF) {
-                const f32x8 x = __builtin_shufflevector(st.s[2 * t], st.s[2 * t + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-                const bf16x8 hi = top(x), lo = top(rest(x, hi));
+                f32x8 x = __builtin_shufflevector(st.s[2 * t], st.s[2 * t + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+                const bf16x8 hi = split<8>(x), lo = __builtin_convertvector(x, bf16x8);
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     const bf16x8 b = row_frag<T, KD>(qt, row_at, it, t);
@@ -529,7 +559,7 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
         st.add(kt, fresh(tid), vf, wt);
         if (c + 1 < nch) {
             lds_barrier();   // scores and tiles read
-            stage(c + 1, fresh(tid));
+            stage(next, c + 1, fresh(tid));
             lds_barrier();
         }
     }
@@ -559,8 +589,10 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_summary(LaUnits 
     Carrier<T, VD, C, NT> cv;
     ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
-    ck.load(0, tid);
-    cv.load(0, tid);
+    typename decltype(ck)::Data dk;
+    typename decltype(cv)::Data dv;
+    ck.load(dk, 0, tid);
+    cv.load(dv, 0, tid);
     const double gd = um.decay[h];
     if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
     const Factor full(dpow(gd, C));
@@ -568,11 +600,11 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_summary(LaUnits 
     st.zero();
     for (int c = 0; c < nch; ++c) {
         const int t_ = fresh(tid);
-        ck.store(kt[c & 1], 0, t_);
-        cv.store(vt[c & 1], 0, t_);
+        ck.store(dk, kt[c & 1], 0, t_);
+        cv.store(dv, vt[c & 1], 0, t_);
         if (c + 1 < nch) {
-            ck.load(0, t_);
-            cv.load(0, t_);
+            ck.load(dk, 0, t_);
+            cv.load(dv, 0, t_);
         }
         lds_barrier();
         typename Shape<T>::frag vf[2];
