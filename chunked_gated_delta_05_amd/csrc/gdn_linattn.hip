@@ -5,8 +5,8 @@
 //     o_i = sum_{j <= i} d^{i-j} (q_i . k_j) v_j + d^{i+1} q_i S
 //     S  <- d^C S + sum_j d^{C-1-j} k_j v_j^T
 // so a chunk is four matrix products. A workgroup walks the chunks of one
-// segment of one head: each of its V / 16 waves keeps 16 of S's value columns
-// in MFMA accumulators for the whole walk, and those registers are at
+// segment of one head: each of its four waves keeps a quarter of S's value
+// columns in MFMA accumulators for the whole walk, and those registers are at
 // once the operand of q S (an accumulator tile and an operand hold the same
 // elements if the contraction's order is chosen to match). Long sequences
 // with too few heads to fill the GPU are cut into segments: a first pass sums
@@ -15,14 +15,13 @@
 //
 // Products of bf16 inputs: bf16 MFMA, fp32 accumulation. Where a value
 // computed in fp32 meets a bf16 operand it is split into bf16 terms, not
-// rounded: two terms (16 bits) for the scores and for S in q S, whose result
-// is rounded to the output's type, three (24 bits) for the decayed v that
-// enters S, which is carried over the whole sequence and returned in fp32.
-// fp32 inputs: fp32 MFMA.
+// rounded: two terms (16 bits) for what ends in o, whose result is rounded to
+// the output's type - the scores, S in q S, the decayed v that enters S - and
+// three (24 bits) for the decayed v where S itself is returned in fp32. fp32
+// inputs: fp32 MFMA.
 //
-// A partial chunk fills the last rows of its tile, with zero rows before
-// them: the factors that enter S then stay those of a full chunk, and only
-// d^{i+1} and d^C change.
+// A partial chunk fills the last rows of its tile: the factors that enter S
+// then stay those of a full chunk, and only d^{i+1} and d^C change.
 #include "gdn_device.h"
 #include "gdn_recurrent_internal.h"
 
@@ -30,7 +29,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int NT = 256;   // of the elementwise kernels; a walk has 4 V threads
+constexpr int NT = 256;
 constexpr int NXCD = 8;
 
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -44,18 +43,20 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 // g = -inf too.
 __device__ __forceinline__ double dpow(double g, int64_t n) { return n == 0 ? 1.0 : exp((double)n * g); }
 
-// x d^n with d^n held in two terms, so that a factor applied once a chunk
-// over a long sequence does not add its own rounding up
+// x d^n without adding up the rounding of d^n over the chunks of a long
+// sequence: near 1 it is x + x (d^n - 1), whose error is that of d^n - 1;
+// below 1/2 a value does not live long enough to add anything up.
 struct Factor {
-    float hi, lo;
+    float f;
+    bool near_one;
     __device__ explicit Factor(double x) {   // x wave-uniform
-        hi = u2f(__builtin_amdgcn_readfirstlane(f2u((float)x)));
-        lo = u2f(__builtin_amdgcn_readfirstlane(f2u((float)(x - (double)(float)x))));
+        near_one = __builtin_amdgcn_readfirstlane(x > 0.5);
+        f = u2f(__builtin_amdgcn_readfirstlane(f2u((float)(near_one ? x - 1.0 : x))));
     }
     __device__ __forceinline__ f32x4 operator*(f32x4 x) const {
         f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = fmaf(x[i], hi, x[i] * lo);
+        for (int i = 0; i < 4; ++i) y[i] = fmaf(x[i], f, near_one ? x[i] : 0.0f);
         return y;
     }
 };
@@ -139,18 +140,27 @@ __device__ __forceinline__ int page_of(const int32_t* pages, int unit, int n_pag
 
 // ------------------------------------------------------------------ tiles
 // Rows of W elements in LDS in 16-byte units, a row's units exchanged by an
-// XOR with the row number, so that 16 rows read at one column and 4 rows read
-// across both spread over the banks. Everything a lane reads of a tile is at
-// one byte offset of the lane, XOR a multiple of 16 below the row length,
-// plus a constant; the offsets are made anew from the thread's number in each
-// chunk (fresh), since held in registers they would cost more than the state.
+// XOR with some of the row number's bits. Everything a lane reads of a tile
+// is at one byte offset of the lane, XOR a multiple of 16 below the row
+// length, plus a constant; the offsets are made anew from the thread's number
+// in each chunk (fresh), since held in registers they would crowd out the
+// state.
 template <typename T, int W>
 struct Tile {
     static constexpr int EPU = 16 / sizeof(T);
     static constexpr int UNITS = W / EPU;
     static constexpr int RB = W * sizeof(T);   // bytes of a row
-    static constexpr int MASK = (UNITS < 16 ? UNITS : 16) - 1;
-    __device__ static __forceinline__ int at(int row, int unit) { return row * RB + (unit ^ (row & MASK)) * 16; }
+    // A permutation of four row bits over the unit bits, in which the rows
+    // that are read together - 16 at one column, four at four neighbouring
+    // units - take all the banks: for bf16 the four are rows r .. r + 3, for
+    // fp32 rows r, r + 4, r + 8, r + 12; a 128-byte row is half the banks, so
+    // its lowest row bit needs no place.
+    __device__ static constexpr int swizzle(int row) {
+        const int lo = row & 3, hi = (row >> 2) & 3;
+        if (UNITS < 16) return 4 * (lo >> 1) | hi;
+        return sizeof(T) == 2 ? 4 * lo | hi : 4 * hi | lo;
+    }
+    __device__ static __forceinline__ int at(int row, int unit) { return row * RB + (unit ^ swizzle(row)) * 16; }
 };
 
 __device__ __forceinline__ int fresh(int x) {
@@ -162,19 +172,40 @@ __device__ __forceinline__ V lds_get(const char* base, int at) {
     return *reinterpret_cast<const V*>(base + at);
 }
 
-// One tensor's chunk on its way from memory to its tile: each of NT threads
-// carries rows row0, row0 + STEP, ...
-template <typename T, int W, int C, int NT>
-struct Carrier {
+// 64 x 16 bytes from base + at (per lane, unsigned) to the 1 KiB of LDS at
+// `lds`, straight from memory: no register is written, so nothing the
+// compiler knows of is outstanding and it waits for nothing; data_arrived and
+// a barrier come before the first read. Written in assembly because the
+// builtin makes the compiler wait for every copy before any LDS read.
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t at, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(at), "s"(base)
+                 : "memory", "m0");
+}
+// waits until at most the LATER youngest of this wave's memory accesses are
+// in flight
+template <int LATER>
+__device__ __forceinline__ void data_arrived() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LATER) : "memory");
+}
+// lds_barrier for tiles that copy_to_lds writes behind the compiler's back
+__device__ __forceinline__ void tile_barrier() {
+    asm volatile("" ::: "memory");
+    lds_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// One tensor's chunks on their way from memory to a tile. A wave's i-th copy
+// brings the rows ROWS (4 i + wave) .. of the tile, 64 / UNITS of them.
+template <typename T, int W, int C>
+struct Feeder {
     using TL = Tile<T, W>;
-    static constexpr int STEP = NT / TL::UNITS;
-    static constexpr int N = C / STEP;
-    static_assert(N >= 1 && (STEP & (STEP - 1)) == 0, "");
-    struct Data {
-        u32x4 x[N];
-    };
-    const char* p;        // the next chunk's lowest token (wave-uniform)
-    int64_t row;          // bytes from a tile row to the next (negative in reversed time)
+    static constexpr int ROWS = 64 / TL::UNITS;     // rows of a copy
+    static constexpr int N = C / (4 * ROWS);        // copies of a wave
+    static_assert(N >= 1, "");
+    const char* p;   // the next chunk's lowest token (wave-uniform)
+    int64_t row;     // bytes from a tile row to the next (negative in reversed time)
 
     // t0: time of the first tile row
     __device__ __forceinline__ void init(const RowsOf& r, int h, int64_t start, int len, int rev, int t0) {
@@ -182,28 +213,25 @@ struct Carrier {
         p = static_cast<const char*>(r.p) + (low * r.ts + (int64_t)(h / r.share) * r.hs) * (int)sizeof(T);
         row = (rev ? -r.ts : r.ts) * (int)sizeof(T);
     }
-    // shift: the chunk's first row is tile row `shift`; the rows before it
-    // are loaded from it and zeroed when they are stored
-    __device__ __forceinline__ void load(Data& d, int shift, int tid) {
-        const int row0 = tid / TL::UNITS, unit = tid % TL::UNITS;
+    // shift: the chunk's first row is tile row `shift`; the rows before it get
+    // a copy of it
+    __device__ __forceinline__ void load(char* tile, int shift, int tid) {
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int row0 = ROWS * wave + lane / TL::UNITS, unit = lane % TL::UNITS;
+        const uint32_t len = (uint32_t)(row < 0 ? -row : row);
+        const uint32_t to = (uint32_t)(uintptr_t)LDS_PTR(char, tile) + 1024 * wave;
         const char* q = p - shift * row;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = max(row0 + i * STEP, shift);
-            const uint32_t at = (uint32_t)(row < 0 ? C - 1 - r : r) * (uint32_t)(row < 0 ? -row : row) + 16 * unit;
-            d.x[i] = *reinterpret_cast<const u32x4*>(q + at);
+            const int r = max(row0 + 4 * ROWS * i, shift);
+            const int u = unit ^ TL::swizzle(row0 + 4 * ROWS * i);
+            copy_to_lds(q, (uint32_t)(row < 0 ? C - 1 - r : r) * len + 16 * u, to + 4096 * i);
         }
         p += C * row;
     }
-    __device__ static __forceinline__ void store(Data& d, char* tile, int shift, int tid) {
-        if (shift) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (tid / TL::UNITS + i * STEP < shift) d.x[i] = u32x4{0, 0, 0, 0};
-        }
-        const int at = TL::at(tid / TL::UNITS, tid % TL::UNITS);
-#pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + (at ^ ((i * STEP & TL::MASK) * 16)) + i * STEP * TL::RB) = d.x[i];
+    // clears the rows before `shift`
+    __device__ static __forceinline__ void clear(char* tile, int shift, int tid) {
+        for (int i = tid; i < shift * TL::UNITS; i += NT) reinterpret_cast<u32x4*>(tile)[i] = u32x4{0, 0, 0, 0};
     }
 };
 
@@ -278,9 +306,9 @@ __device__ __forceinline__ typename Shape<T>::frag row_frag(const char* tile, in
     return lds_get<typename Shape<T>::frag>(tile, (at ^ (64 * t)) + it * 16 * Tile<T, W>::RB);
 }
 
-// Column c0 + p of a tile as an operand, tokens of block s (32 or 16 of
-// them). bf16: c0's columns are four groups of four that the lanes p % 4
-// name, GAP apart; across_lane gives the address of the lane's group.
+// Columns of a tile as an operand, tokens of block s (32 or 16 of them).
+// bf16: four groups of four columns that the lanes p % 4 name; across_lane
+// gives the address of the lane's group. fp32: the lane's column.
 template <int W>
 __device__ __forceinline__ int across_lane(int tid, int col) {   // col: of this lane's group
     const int p = tid & 15, g = (tid & 63) >> 4;
@@ -289,9 +317,9 @@ __device__ __forceinline__ int across_lane(int tid, int col) {   // col: of this
 template <int W>
 __device__ __forceinline__ bf16x8 across_frag(const char* tile, int at, int s, int flip, int add) {
     constexpr int RB = Tile<bf16, W>::RB;
-    // four rows on, the row number's bit 2 flips the units' bit 2
+    // four rows on is another value of one row bit
     return join(read_across(tile, (at ^ flip) + 32 * s * RB + add),
-                read_across(tile, (at ^ flip ^ 64) + (32 * s + 4) * RB + add));
+                read_across(tile, (at ^ flip ^ 16 * Tile<bf16, W>::swizzle(4)) + (32 * s + 4) * RB + add));
 }
 template <int W>
 __device__ __forceinline__ int column_lane(int tid, int col) {   // col: of this lane
@@ -303,107 +331,170 @@ __device__ __forceinline__ f32x4 column_frag(const char* tile, int at, int s, in
     constexpr int RB = Tile<float, W>::RB;
     f32x4 x;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = lds_get<float>(tile, (at ^ flip ^ (16 * r)) + (16 * s + r) * RB);
+    for (int r = 0; r < 4; ++r)
+        x[r] = lds_get<float>(tile, (at ^ flip ^ (16 * Tile<float, W>::swizzle(r))) + (16 * s + r) * RB);
     return x;
 }
 
+// Scores in LDS: blocks of 16 rows x one contraction block (64 bytes a row),
+// those on and below the diagonal only.
+template <typename T>
+struct Scores {
+    static constexpr int C = Shape<T>::C, KS = Shape<T>::KS;
+    static constexpr int block(int it, int s) {   // it: 16 rows, s: KS columns
+        return KS == 32 ? (it < 2 ? it : 2 * it - 2) + s : it * (it + 1) / 2 + s;
+    }
+    static constexpr int BYTES = 1024 * (block(C / 16 - 1, C / KS - 1) + 1);   // of one term
+    // unit u (16 bytes) of row p
+    __device__ static __forceinline__ int at(int p, int u) { return p * 64 + (u ^ (p >> 2)) * 16; }
+};
+
 // ------------------------------------------------------------------ the state
-// A wave's part of S: 16 value columns, KD / 16 tiles of 16 keys.
+// A wave's part of S: CG groups of 16 value columns, KD / 16 tiles of 16 keys.
+// Two groups (V = 128) rather than eight waves of one: an operand read from
+// LDS then meets both.
 // bf16: row m of tile 2 t + u is key 32 t + 8 (m / 4) + 4 u + m % 4, so that
 // tiles 2 t and 2 t + 1 hold, in each lane, the eight consecutive keys of an
 // operand; fp32: row m of tile t is key 16 t + m.
 template <typename T, int KD, int VD>
 struct State {
-    static constexpr int KT = KD / 16;
-    f32x4 s[KT];
+    static constexpr int KT = KD / 16, CG = VD / 64;
+    using frag = typename Shape<T>::frag;
+    f32x4 s[KT][CG];
 
     __device__ static __forceinline__ int key0(int kt, int g) {   // of the lane's four rows
         if constexpr (sizeof(T) == 2) return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1);
         return 16 * kt + 4 * g;
     }
-    __device__ static __forceinline__ int col() { return (threadIdx.x >> 6) * 16 + (threadIdx.x & 15); }
+    __device__ static __forceinline__ int col(int cg) {
+        return (threadIdx.x >> 6) * 16 * CG + 16 * cg + (threadIdx.x & 15);
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) s[kt] = f32x4{0, 0, 0, 0};
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f32x4{0, 0, 0, 0};
     }
-    __device__ void load(const float* p, int transposed) {
+    __device__ __forceinline__ void load(const float* p, int transposed) {
         const int g = (threadIdx.x & 63) >> 4;
+        if (transposed) {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            if (transposed) {
-                s[kt] = *reinterpret_cast<const f32x4*>(p + col() * KD + key0(kt, g));
-            } else {
+            for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[kt][r] = p[(key0(kt, g) + r) * VD + col()];
-            }
+                for (int cg = 0; cg < CG; ++cg)
+                    s[kt][cg] = *reinterpret_cast<const f32x4*>(p + col(cg) * KD + key0(kt, g));
+        } else {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * VD + col(cg)];
         }
     }
-    __device__ void store(float* p) const {
+    __device__ __forceinline__ void store(float* p) const {
         const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col()] = s[kt][r];
+            for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col(cg)] = s[kt][cg][r];
     }
     __device__ __forceinline__ void scale(const Factor& f) {
+        if (f.near_one) {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) s[kt] = f * s[kt];
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = fmaf(s[kt][cg][r], f.f, s[kt][cg][r]);
+        } else {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg) s[kt][cg] *= f.f;
+        }
     }
-    // the lane's offset in the tile of k, for add
-    __device__ static __forceinline__ int key_lane(int tid) {
-        if constexpr (sizeof(T) == 2) return across_lane<KD>(tid, 8 * (tid & 3));
-        else return column_lane<KD>(tid, tid & 15);
-    }
-    // S += sum_j wt[j] k_j v_j^T over a chunk; v as operands
-    __device__ __forceinline__ void add(const char* kt_, int tid, const typename Shape<T>::frag* v, const float* wt) {
-        const int at = key_lane(tid), g = (tid & 63) >> 4;
+    // S += sum_j wt[j] k_j v_j^T over a chunk; v as operands. bf16: wt v in
+    // TERMS terms
+    template <int TERMS>
+    __device__ __forceinline__ void add(const char* kt_, int tid, const frag (*v)[CG], const float* wt) {
+        const int g = (tid & 63) >> 4;
 #pragma unroll
         for (int s_ = 0; s_ < 2; ++s_) {
             if constexpr (sizeof(T) == 2) {
-                f32x8 x = *reinterpret_cast<const f32x8*>(wt + 32 * s_ + 8 * g) * __builtin_convertvector(v[s_], f32x8);
-                const bf16x8 b0 = split<8>(x), b1 = split<8>(x), b2 = __builtin_convertvector(x, bf16x8);
+                const int at = across_lane<KD>(tid, 8 * (tid & 3));
+                const f32x8 w = *reinterpret_cast<const f32x8*>(wt + 32 * s_ + 8 * g);
+                bf16x8 b[CG][TERMS];
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg) {
+                    f32x8 x = w * __builtin_convertvector(v[s_][cg], f32x8);
+#pragma unroll
+                    for (int i = 0; i + 1 < TERMS; ++i) b[cg][i] = split<8>(x);
+                    b[cg][TERMS - 1] = __builtin_convertvector(x, bf16x8);
+                }
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     const bf16x8 a = across_frag<KD>(kt_, at, s_, 64 * (kt >> 1), 8 * (kt & 1));
-                    s[kt] = mfma(a, b0, s[kt]);
-                    s[kt] = mfma(a, b1, s[kt]);
-                    s[kt] = mfma(a, b2, s[kt]);
+#pragma unroll
+                    for (int i = 0; i < TERMS; ++i)
+#pragma unroll
+                        for (int cg = 0; cg < CG; ++cg) s[kt][cg] = mfma(a, b[cg][i], s[kt][cg]);
                 }
             } else {
-                const f32x4 b = *reinterpret_cast<const f32x4*>(wt + 16 * s_ + 4 * g) * v[s_];
+                const int at = column_lane<KD>(tid, tid & 15);
+                const f32x4 w = *reinterpret_cast<const f32x4*>(wt + 16 * s_ + 4 * g);
+                f32x4 b[CG];
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) s[kt] = mfma(column_frag<KD>(kt_, at, s_, 64 * kt), b, s[kt]);
+                for (int cg = 0; cg < CG; ++cg) b[cg] = w * v[s_][cg];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    const f32x4 a = column_frag<KD>(kt_, at, s_, 64 * kt);
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg) s[kt][cg] = mfma(a, b[cg], s[kt][cg]);
+                }
             }
         }
     }
 };
 
-// The wave's 16 columns of v as operands, two blocks of tokens.
+// The wave's columns of v as operands, two blocks of tokens.
 template <typename T, int VD>
-__device__ __forceinline__ void value_frags(const char* tile, int tid, typename Shape<T>::frag* v) {
+__device__ __forceinline__ void value_frags(const char* tile, int tid, typename Shape<T>::frag (*v)[VD / 64]) {
+    constexpr int CG = VD / 64;
     const int p = tid & 15, w = tid >> 6;
-    int at;
-    if constexpr (sizeof(T) == 2) at = across_lane<VD>(tid, 16 * w + 4 * (p & 3));
-    else at = column_lane<VD>(tid, 16 * w + p);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        if constexpr (sizeof(T) == 2) v[s] = across_frag<VD>(tile, at, s, 0, 0);
-        else v[s] = column_frag<VD>(tile, at, s, 0);
+    for (int cg = 0; cg < CG; ++cg) {
+        const int col = 16 * (CG * w + cg);
+        if constexpr (sizeof(T) == 2) {
+            const int at = across_lane<VD>(tid, col + 4 * (p & 3));
+#pragma unroll
+            for (int s = 0; s < 2; ++s) v[s][cg] = across_frag<VD>(tile, at, s, 0, 0);
+        } else {
+            const int at = column_lane<VD>(tid, col + p);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) v[s][cg] = column_frag<VD>(tile, at, s, 0);
+        }
     }
 }
 
 // ------------------------------------------------------------------ kernels
-template <typename T, int KD, int VD>
-__global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um, LaJobs jobs) {
-    constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, NT = 4 * VD, WAVES = VD / 16;
+// Two workgroups a compute unit (77 KiB of LDS each for K = V = 128): the q
+// and v tiles are free for the next chunk once the scores are written and
+// q S and v are in registers, so only k has two tiles.
+// TERMS: bf16 terms of the decayed v that enters S
+template <typename T, int KD, int VD, int TERMS>
+__global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
+    constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, WAVES = NT / 64, CG = VD / 64;
     constexpr bool BF = sizeof(T) == 2;
-    constexpr int PB = C * C * sizeof(T);   // bytes of the scores; bf16: of each of their two terms
-    using PT = Tile<T, C>;
+    constexpr int KB = C * KD * sizeof(T), PB = Scores<T>::BYTES;
+    using SC = Scores<T>;
     using frag = typename Shape<T>::frag;
-    __shared__ __attribute__((aligned(32))) char qt[C * KD * sizeof(T)];
-    __shared__ __attribute__((aligned(32))) char kt[C * KD * sizeof(T)];
-    __shared__ __attribute__((aligned(32))) char vt[C * VD * sizeof(T)];
-    __shared__ __attribute__((aligned(32))) char pt[(BF ? 2 : 1) * PB];
+    __shared__ __attribute__((aligned(1024))) char qt[KB];
+    __shared__ __attribute__((aligned(1024))) char kt2[2 * KB];
+    __shared__ __attribute__((aligned(1024))) char vt[C * VD * sizeof(T)];
+    __shared__ __attribute__((aligned(1024))) char pt[(BF ? 2 : 1) * PB];
     __shared__ __attribute__((aligned(32))) float wt[C];
     __shared__ float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
 
@@ -416,32 +507,19 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
     const int seg0 = sg.index * um.seg_tokens;
     const int seg1 = min(sg.len, seg0 + um.seg_tokens);
     const int nch = seg1 > seg0 ? (seg1 - seg0 + C - 1) / C : 0;
-    const int last_shift = nch * C - max(0, seg1 - seg0);   // zero rows of the last chunk
+    const int last_shift = nch * C - max(0, seg1 - seg0);   // tile rows before the last chunk's first
 
-    Carrier<T, KD, C, NT> cq, ck;
-    Carrier<T, VD, C, NT> cv;
-    cq.init(jb.q, h, sg.start, sg.len, jb.rev, seg0);
-    ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
-    cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
+    Feeder<T, KD, C> fq, fk;
+    Feeder<T, VD, C> fv;
+    fq.init(jb.q, h, sg.start, sg.len, jb.rev, seg0);
+    fk.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
+    fv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
     auto shift_of = [&](int c) { return c + 1 < nch ? 0 : last_shift; };
-    // the data of a chunk lives from its fetch to its staging only, so that
-    // nothing but the staging waits for it
-    struct Data {
-        typename Carrier<T, KD, C, NT>::Data q, k;
-        typename Carrier<T, VD, C, NT>::Data v;
-    };
-    auto fetch = [&](Data& d, int c, int tid) {
-        cq.load(d.q, shift_of(c), tid);
-        ck.load(d.k, shift_of(c), tid);
-        cv.load(d.v, shift_of(c), tid);
-    };
-    auto stage = [&](Data& d, int c, int tid) {
-        cq.store(d.q, qt, shift_of(c), tid);
-        ck.store(d.k, kt, shift_of(c), tid);
-        cv.store(d.v, vt, shift_of(c), tid);
-    };
-    Data first;
-    if (nch > 0) fetch(first, 0, tid);
+    if (nch > 0) {
+        fk.load(kt2, shift_of(0), tid);
+        fq.load(qt, shift_of(0), tid);
+        fv.load(vt, shift_of(0), tid);
+    }
 
     State<T, KD, VD> st;
     {
@@ -456,20 +534,25 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
         else st.zero();
     }
     const double gd = um.decay[h];
-    for (int i = tid; i < 2 * C; i += NT) pw[i] = i < C ? 0.0f : (float)(jb.s_p * dpow(gd, i - C));
-    if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
-    if (tid < 2 * C) {
-        const int i = tid % C - (tid < C ? 0 : last_shift);
-        rf[tid / C][tid % C] = i < 0 ? 0.0f : (float)(jb.s_o * dpow(gd, i + jb.e));
+    if (tid < 4 * C) {   // four tables of C powers
+        const int i = tid % C, table = tid / C;
+        const int n = table == 0 ? i : table == 1 ? C - jb.e - i : table == 2 ? i + jb.e : i - last_shift + jb.e;
+        const float x = (table == 0 ? jb.s_p : table == 1 ? jb.s_w : jb.s_o) * (float)dpow(gd, max(n, 0));
+        if (table == 0) pw[C + i] = x;
+        if (table == 1) wt[i] = x;
+        if (table == 2) rf[0][i] = x;
+        if (table == 3) rf[1][i] = i < last_shift ? 0.0f : x;
+        if (table == 0) pw[i] = 0.0f;
     }
     const Factor full(dpow(gd, C)), last(dpow(gd, C - last_shift));
-    // score tiles above the diagonal that an operand reaches stay zero
+    // the parts of the diagonal's blocks that no score is written to
     for (int i = tid; i < (BF ? 2 : 1) * PB / 16; i += NT) reinterpret_cast<u32x4*>(pt)[i] = u32x4{0, 0, 0, 0};
-    if (nch > 0) stage(first, 0, tid);
-    // the state's loads end here: a wait for them inside the loop would also
-    // wait for the next chunk's
-    __builtin_amdgcn_s_waitcnt(0);
-    lds_barrier();
+    data_arrived<0>();
+    tile_barrier();
+    if (shift_of(0) && nch > 0) {
+        fv.clear(vt, shift_of(0), tid);
+        tile_barrier();
+    }
 
     // o: bytes from a row to the next, the lowest of the next 16 rows, the lane's part from there
     const int es = jb.o_f32 ? 4 : 2;
@@ -479,88 +562,135 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
 
     for (int c = 0; c < nch; ++c) {
         const int shift = shift_of(c);
+        const bool more = c + 1 < nch;
         const float* rfc = rf[shift ? 1 : 0];
-        Data next;
-        if (c + 1 < nch) fetch(next, c + 1, fresh(tid));
+        const char* kt = kt2 + (c & 1) * KB;
         const int t_ = fresh(tid), p = t_ & 15, g = (t_ & 63) >> 4;
         const int row_at = row_lane<T, KD>(t_);
+        if (more) fk.load(kt2 + (~c & 1) * KB, shift_of(c + 1), t_);
 
-        // scores of the lower triangle, transposed: tile n of the list for wave n % WAVES
-        constexpr int TILES = IT * (IT + 1) / 2;
+        // scores of the lower triangle, transposed: the wave's tiles of the list
+        // (row tiles of 1, 2, .. tiles); the last waves do the last tile again
+        // instead of waiting for the others
+        constexpr int TILES = IT * (IT + 1) / 2, MINE = (TILES + WAVES - 1) / WAVES;
+        int it_[MINE], jt_[MINE];
+        f32x4 sc[MINE];
 #pragma unroll
-        for (int n0 = 0; n0 < TILES; n0 += WAVES) {
-            const int n = n0 + wave;
-            if (n < TILES) {
-                const int it = BF ? (n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0) : (n >= 1 ? 1 : 0);
-                const int jt = n - it * (it + 1) / 2;
-                f32x4 acc = {0, 0, 0, 0};
+        for (int i = 0; i < MINE; ++i) {
+            const int n = min(wave + i * WAVES, TILES - 1);
+            it_[i] = BF ? (n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0) : (n >= 1 ? 1 : 0);
+            jt_[i] = n - it_[i] * (it_[i] + 1) / 2;
+            sc[i] = f32x4{0, 0, 0, 0};
+        }
 #pragma unroll
-                for (int t = 0; t < KD / KS; ++t)
-                    acc = mfma(row_frag<T, KD>(kt, row_at, jt, t), row_frag<T, KD>(qt, row_at, it, t), acc);
-                const float* pwl = pw + C + 16 * (it - jt) + p - 4 * g;
+        for (int t = 0; t < KD / KS; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] *= pwl[-r];
-                // row 16 it + p, columns 16 jt + 4 g ..
-                const int at = 16 * it * PT::RB + PT::at(p, (16 * jt + 4 * g) / PT::EPU) + (16 * jt + 4 * g) % PT::EPU * (int)sizeof(T);
-                if constexpr (BF) {
-                    *reinterpret_cast<bf16x4*>(pt + at) = split<4>(acc);
-                    *reinterpret_cast<bf16x4*>(pt + PB + at) = __builtin_convertvector(acc, bf16x4);
-                } else {
-                    *reinterpret_cast<f32x4*>(pt + at) = acc;
-                }
+            for (int i = 0; i < MINE; ++i)
+                sc[i] = mfma(row_frag<T, KD>(kt, row_at, jt_[i], t), row_frag<T, KD>(qt, row_at, it_[i], t), sc[i]);
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const float* pwl = pw + C + 16 * (it_[i] - jt_[i]) + p - 4 * g;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc[i][r] *= pwl[-r];
+            // row p of row tile it, columns 16 jt + 4 g ..: bf16 half a unit, fp32 a unit
+            const int u = BF ? 2 * (jt_[i] & 1) + (g >> 1) : g;
+            const int at = 1024 * SC::block(it_[i], BF ? jt_[i] >> 1 : jt_[i]) + SC::at(p, u) + (BF ? 8 * (g & 1) : 0);
+            if constexpr (BF) {
+                *reinterpret_cast<bf16x4*>(pt + at) = split<4>(sc[i]);
+                *reinterpret_cast<bf16x4*>(pt + PB + at) = __builtin_convertvector(sc[i], bf16x4);
+            } else {
+                *reinterpret_cast<f32x4*>(pt + at) = sc[i];
             }
         }
-
-        frag vf[2];
+        frag vf[2][CG];
         value_frags<T, VD>(vt, t_, vf);
-        lds_barrier();   // scores written
 
         // o^T = (q S)^T, rows scaled by their distance from the chunk's start
-        f32x4 o[IT];
+        f32x4 o[IT][CG];
 #pragma unroll
-        for (int it = 0; it < IT; ++it) o[it] = f32x4{0, 0, 0, 0};
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int cg = 0; cg < CG; ++cg) o[it][cg] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < KD / KS; ++t) {
             if constexpr (BF) {
-                f32x8 x = __builtin_shufflevector(st.s[2 * t], st.s[2 * t + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-                const bf16x8 hi = split<8>(x), lo = __builtin_convertvector(x, bf16x8);
+                bf16x8 hi[CG], lo[CG];
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg) {
+                    f32x8 x = __builtin_shufflevector(st.s[2 * t][cg], st.s[2 * t + 1][cg], 0, 1, 2, 3, 4, 5, 6, 7);
+                    hi[cg] = split<8>(x);
+                    lo[cg] = __builtin_convertvector(x, bf16x8);
+                }
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     const bf16x8 b = row_frag<T, KD>(qt, row_at, it, t);
-                    o[it] = mfma(hi, b, o[it]);
-                    o[it] = mfma(lo, b, o[it]);
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(hi[cg], b, o[it][cg]);
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(lo[cg], b, o[it][cg]);
                 }
             } else {
 #pragma unroll
-                for (int it = 0; it < IT; ++it) o[it] = mfma(st.s[t], row_frag<T, KD>(qt, row_at, it, t), o[it]);
+                for (int it = 0; it < IT; ++it) {
+                    const f32x4 b = row_frag<T, KD>(qt, row_at, it, t);
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(st.s[t][cg], b, o[it][cg]);
+                }
             }
         }
-#pragma unroll
-        for (int it = 0; it < IT; ++it) o[it] *= rfc[16 * it + p];
-
-        const int p_at = row_lane<T, C>(t_);
-        const uint32_t o_at = (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * VD * es) + (16 * wave + 4 * g) * es;
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
+            const float f = rfc[16 * it + p];
 #pragma unroll
-            for (int s = 0; s <= (it * 16) / KS; ++s) {
-                o[it] = mfma(vf[s], row_frag<T, C>(pt, p_at, it, s), o[it]);
-                if constexpr (BF) o[it] = mfma(vf[s], row_frag<T, C>(pt + PB, p_at, it, s), o[it]);
-            }
-            if (16 * it + p >= shift) {
-                char* to = op + (16 * it - shift) * orow + o_at;
-                if (jb.o_f32) *reinterpret_cast<f32x4*>(to) = o[it];
-                else *reinterpret_cast<bf16x4*>(to) = __builtin_convertvector(o[it], bf16x4);
-            }
+            for (int cg = 0; cg < CG; ++cg) o[it][cg] *= f;
+        }
+        tile_barrier();   // scores written, q and v read
+        if (more) {
+            fq.load(qt, shift_of(c + 1), t_);
+            fv.load(vt, shift_of(c + 1), t_);
+        }
+        st.scale(shift ? last : full);
+
+        const int p_at = SC::at(p, g);
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int s = 0; s <= (it * 16) / KS; ++s)
+#pragma unroll
+                for (int x = 0; x < (BF ? 2 : 1); ++x) {
+                    const frag b = lds_get<frag>(pt + x * PB + 1024 * SC::block(it, s), p_at);
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(vf[s][cg], b, o[it][cg]);
+                }
+        const uint32_t o_at =
+            (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * VD * es) + (16 * CG * wave + 4 * g) * es;
+        if (jb.o_f32) {
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+                if (16 * it + p >= shift)
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg)
+                        *reinterpret_cast<f32x4*>(op + (16 * it - shift) * orow + o_at + 64 * cg) = o[it][cg];
+        } else {
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+                if (16 * it + p >= shift)
+#pragma unroll
+                    for (int cg = 0; cg < CG; ++cg)
+                        *reinterpret_cast<bf16x4*>(op + (16 * it - shift) * orow + o_at + 32 * cg) =
+                            __builtin_convertvector(o[it][cg], bf16x4);
         }
         op += C * orow;
+        st.template add<TERMS>(kt, t_, vf, wt);
 
-        st.scale(shift ? last : full);
-        st.add(kt, fresh(tid), vf, wt);
-        if (c + 1 < nch) {
-            lds_barrier();   // scores and tiles read
-            stage(next, c + 1, fresh(tid));
-            lds_barrier();
+        // a chunk that is not the last has stored all its rows after the copies
+        if (more) {
+            data_arrived<IT * CG>();
+            tile_barrier();
+            if (shift_of(c + 1)) {
+                fv.clear(vt, shift_of(c + 1), t_);
+                tile_barrier();
+            }
         }
     }
 
@@ -572,11 +702,11 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_main(LaUnits um,
 
 // A segment's own contribution to the state after it, into the next slot of
 // its unit. The last segment of a unit has no next one.
-template <typename T, int KD, int VD>
-__global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_summary(LaUnits um, LaJobs jobs) {
-    constexpr int C = Shape<T>::C, NT = 4 * VD;
-    __shared__ __attribute__((aligned(32))) char kt[2][C * KD * sizeof(T)];
-    __shared__ __attribute__((aligned(32))) char vt[2][C * VD * sizeof(T)];
+template <typename T, int KD, int VD, int TERMS>
+__global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
+    constexpr int C = Shape<T>::C, KB = C * KD * sizeof(T), VB = C * VD * sizeof(T);
+    __shared__ __attribute__((aligned(1024))) char kt[2 * KB];
+    __shared__ __attribute__((aligned(1024))) char vt[2 * VB];
     __shared__ __attribute__((aligned(32))) float wt[C];
     const int tid = threadIdx.x;
     const int id = xcd_order(blockIdx.x, gridDim.x);
@@ -585,32 +715,29 @@ __global__ __launch_bounds__(4 * VD, VD == 128 ? 4 : 2) void la_summary(LaUnits 
     const Seg sg = find_seg(um, seg_id);
     if (sg.unit < 0 || sg.index == sg.count - 1 || seg_id + 1 >= um.n_segs) return;
     const int seg0 = sg.index * um.seg_tokens, nch = um.seg_tokens / C;
-    Carrier<T, KD, C, NT> ck;
-    Carrier<T, VD, C, NT> cv;
-    ck.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
-    cv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
-    typename decltype(ck)::Data dk;
-    typename decltype(cv)::Data dv;
-    ck.load(dk, 0, tid);
-    cv.load(dv, 0, tid);
+    Feeder<T, KD, C> fk;
+    Feeder<T, VD, C> fv;
+    fk.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
+    fv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
+    fk.load(kt, 0, tid);
+    fv.load(vt, 0, tid);
     const double gd = um.decay[h];
     if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
     const Factor full(dpow(gd, C));
     State<T, KD, VD> st;
     st.zero();
     for (int c = 0; c < nch; ++c) {
-        const int t_ = fresh(tid);
-        ck.store(dk, kt[c & 1], 0, t_);
-        cv.store(dv, vt[c & 1], 0, t_);
+        data_arrived<0>();
+        tile_barrier();
+        const int t_ = fresh(tid), b = c & 1;
         if (c + 1 < nch) {
-            ck.load(dk, 0, t_);
-            cv.load(dv, 0, t_);
+            fk.load(kt + (b ^ 1) * KB, 0, t_);
+            fv.load(vt + (b ^ 1) * VB, 0, t_);
         }
-        lds_barrier();
-        typename Shape<T>::frag vf[2];
-        value_frags<T, VD>(vt[c & 1], t_, vf);
+        typename Shape<T>::frag vf[2][VD / 64];
+        value_frags<T, VD>(vt + b * VB, t_, vf);
         st.scale(full);
-        st.add(kt[c & 1], fresh(tid), vf, wt);
+        st.template add<TERMS>(kt + b * KB, t_, vf, wt);
     }
     st.store(jb.slots + ((int64_t)(seg_id + 1) * um.H + h) * (KD * VD));
 }
@@ -677,34 +804,43 @@ __global__ __launch_bounds__(NT) void la_group(const float* x, T* out, int64_t n
     put4(out + 4 * i, s);
 }
 
-template <typename T>
+template <typename T, int TERMS>
 hipError_t main_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    if (K == 128 && V == 128) la_main<T, 128, 128><<<n, 512, 0, s>>>(u, j);
-    else if (K == 128) la_main<T, 128, 64><<<n, 256, 0, s>>>(u, j);
-    else if (V == 128) la_main<T, 64, 128><<<n, 512, 0, s>>>(u, j);
-    else la_main<T, 64, 64><<<n, 256, 0, s>>>(u, j);
+    if (K == 128 && V == 128) la_main<T, 128, 128, TERMS><<<n, NT, 0, s>>>(u, j);
+    else if (K == 128) la_main<T, 128, 64, TERMS><<<n, NT, 0, s>>>(u, j);
+    else if (V == 128) la_main<T, 64, 128, TERMS><<<n, NT, 0, s>>>(u, j);
+    else la_main<T, 64, 64, TERMS><<<n, NT, 0, s>>>(u, j);
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, int TERMS>
 hipError_t summary_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    if (K == 128 && V == 128) la_summary<T, 128, 128><<<n, 512, 0, s>>>(u, j);
-    else if (K == 128) la_summary<T, 128, 64><<<n, 256, 0, s>>>(u, j);
-    else if (V == 128) la_summary<T, 64, 128><<<n, 512, 0, s>>>(u, j);
-    else la_summary<T, 64, 64><<<n, 256, 0, s>>>(u, j);
+    if (K == 128 && V == 128) la_summary<T, 128, 128, TERMS><<<n, NT, 0, s>>>(u, j);
+    else if (K == 128) la_summary<T, 128, 64, TERMS><<<n, NT, 0, s>>>(u, j);
+    else if (V == 128) la_summary<T, 64, 128, TERMS><<<n, NT, 0, s>>>(u, j);
+    else la_summary<T, 64, 64, TERMS><<<n, NT, 0, s>>>(u, j);
     return hipGetLastError();
+}
+
+// a third term (24 bits) only where a state is returned; fp32 has no terms
+bool returns_state(const LaJobs& j) {
+    for (int i = 0; i < j.n; ++i)
+        if (j.job[i].s_out) return true;
+    return false;
 }
 
 }  // namespace
 
 hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s) {
-    return dtype == GDN_DTYPE_BF16 ? main_t<bf16>(u, j, K, V, s) : main_t<float>(u, j, K, V, s);
+    if (dtype == GDN_DTYPE_F32) return main_t<float, 1>(u, j, K, V, s);
+    return returns_state(j) ? main_t<bf16, 3>(u, j, K, V, s) : main_t<bf16, 2>(u, j, K, V, s);
 }
 
 hipError_t launch_la_summary(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s) {
-    return dtype == GDN_DTYPE_BF16 ? summary_t<bf16>(u, j, K, V, s) : summary_t<float>(u, j, K, V, s);
+    if (dtype == GDN_DTYPE_F32) return summary_t<float, 1>(u, j, K, V, s);
+    return returns_state(j) ? summary_t<bf16, 3>(u, j, K, V, s) : summary_t<bf16, 2>(u, j, K, V, s);
 }
 
 hipError_t launch_la_merge(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {

@@ -4,6 +4,7 @@
 // checks can be exercised without a GPU.
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "gdn_recurrent.h"
@@ -91,7 +92,7 @@ gdn_status check_prompt(const gdn_linattn_desc* d, Prompt* p) {
     }
     // Segments: enough of them to give every compute unit its two
     // workgroups, none shorter than four chunks.
-    const int64_t want = 512;
+    const int64_t want = getenv("LA_WANT") ? atoi(getenv("LA_WANT")) : 512;
     int64_t seg = (p->chunks * d->H + want - 1) / want;
     if (seg < 4) seg = 4;
     if (seg > p->longest / kChunk + 1) seg = p->longest / kChunk + 1;
