@@ -352,7 +352,8 @@ struct Scores {
 // ------------------------------------------------------------------ the state
 // A wave's part of S: CG groups of 16 value columns, KD / 16 tiles of 16 keys.
 // Two groups (V = 128) rather than eight waves of one: an operand read from
-// LDS then meets both.
+// LDS then meets both; their columns alternate by fours, so that a lane's rows
+// of o^T in both are eight consecutive values of o.
 // bf16: row m of tile 2 t + u is key 32 t + 8 (m / 4) + 4 u + m % 4, so that
 // tiles 2 t and 2 t + 1 hold, in each lane, the eight consecutive keys of an
 // operand; fp32: row m of tile t is key 16 t + m.
@@ -366,8 +367,9 @@ struct State {
         if constexpr (sizeof(T) == 2) return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1);
         return 16 * kt + 4 * g;
     }
-    __device__ static __forceinline__ int col(int cg) {
-        return (threadIdx.x >> 6) * 16 * CG + 16 * cg + (threadIdx.x & 15);
+    __device__ static __forceinline__ int col(int tid, int cg) {
+        const int p = tid & 15, w = tid >> 6;
+        return CG == 2 ? 32 * w + 8 * (p >> 2) + 4 * cg + (p & 3) : 16 * w + p;
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -376,30 +378,30 @@ struct State {
             for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f32x4{0, 0, 0, 0};
     }
     __device__ __forceinline__ void load(const float* p, int transposed) {
-        const int g = (threadIdx.x & 63) >> 4;
+        const int tid = threadIdx.x, g = (tid & 63) >> 4;
         if (transposed) {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int cg = 0; cg < CG; ++cg)
-                    s[kt][cg] = *reinterpret_cast<const f32x4*>(p + col(cg) * KD + key0(kt, g));
+                    s[kt][cg] = *reinterpret_cast<const f32x4*>(p + col(tid, cg) * KD + key0(kt, g));
         } else {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * VD + col(cg)];
+                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * VD + col(tid, cg)];
         }
     }
     __device__ __forceinline__ void store(float* p) const {
-        const int g = (threadIdx.x & 63) >> 4;
+        const int tid = threadIdx.x, g = (tid & 63) >> 4;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col(cg)] = s[kt][cg][r];
+                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col(tid, cg)] = s[kt][cg][r];
     }
     __device__ __forceinline__ void scale(const Factor& f) {
         if (f.near_one) {
@@ -459,20 +461,19 @@ struct State {
     }
 };
 
-// The wave's columns of v as operands, two blocks of tokens.
-template <typename T, int VD>
+// The wave's columns of v (State::col) as operands, two blocks of tokens.
+template <typename T, int KD, int VD>
 __device__ __forceinline__ void value_frags(const char* tile, int tid, typename Shape<T>::frag (*v)[VD / 64]) {
     constexpr int CG = VD / 64;
-    const int p = tid & 15, w = tid >> 6;
 #pragma unroll
     for (int cg = 0; cg < CG; ++cg) {
-        const int col = 16 * (CG * w + cg);
         if constexpr (sizeof(T) == 2) {
-            const int at = across_lane<VD>(tid, col + 4 * (p & 3));
+            // the group of four that lane p % 4 names: the columns of rows 4 (p % 4) ..
+            const int at = across_lane<VD>(tid, State<T, KD, VD>::col((tid & ~15) | 4 * (tid & 3), cg));
 #pragma unroll
             for (int s = 0; s < 2; ++s) v[s][cg] = across_frag<VD>(tile, at, s, 0, 0);
         } else {
-            const int at = column_lane<VD>(tid, col + p);
+            const int at = column_lane<VD>(tid, State<T, KD, VD>::col(tid, cg));
 #pragma unroll
             for (int s = 0; s < 2; ++s) v[s][cg] = column_frag<VD>(tile, at, s, 0);
         }
@@ -603,7 +604,7 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
             }
         }
         frag vf[2][CG];
-        value_frags<T, VD>(vt, t_, vf);
+        value_frags<T, KD, VD>(vt, t_, vf);
 
         // o^T = (q S)^T, rows scaled by their distance from the chunk's start
         f32x4 o[IT][CG];
@@ -662,30 +663,31 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
 #pragma unroll
                     for (int cg = 0; cg < CG; ++cg) o[it][cg] = mfma(vf[s][cg], b, o[it][cg]);
                 }
+        // a lane's rows of o^T: 4 CG consecutive values of row p of o
         const uint32_t o_at =
-            (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * VD * es) + (16 * CG * wave + 4 * g) * es;
-        if (jb.o_f32) {
+            (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * VD * es) + CG * (16 * wave + 4 * g) * es;
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
-                if (16 * it + p >= shift)
+        for (int it = 0; it < IT; ++it) {
+            char* to = op + (16 * it - shift) * orow + o_at;
+            if (16 * it + p < shift) continue;
+            if (jb.o_f32) {
 #pragma unroll
-                    for (int cg = 0; cg < CG; ++cg)
-                        *reinterpret_cast<f32x4*>(op + (16 * it - shift) * orow + o_at + 64 * cg) = o[it][cg];
-        } else {
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-                if (16 * it + p >= shift)
-#pragma unroll
-                    for (int cg = 0; cg < CG; ++cg)
-                        *reinterpret_cast<bf16x4*>(op + (16 * it - shift) * orow + o_at + 32 * cg) =
-                            __builtin_convertvector(o[it][cg], bf16x4);
+                for (int cg = 0; cg < CG; ++cg)
+                    __builtin_nontemporal_store(o[it][cg], reinterpret_cast<f32x4*>(to) + cg);
+            } else if constexpr (CG == 2) {
+                const f32x8 x = __builtin_shufflevector(o[it][0], o[it][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                __builtin_nontemporal_store(__builtin_convertvector(x, bf16x8), reinterpret_cast<bf16x8*>(to));
+            } else {
+                __builtin_nontemporal_store(__builtin_convertvector(o[it][0], bf16x4), reinterpret_cast<bf16x4*>(to));
+            }
         }
         op += C * orow;
         st.template add<TERMS>(kt, t_, vf, wt);
 
-        // a chunk that is not the last has stored all its rows after the copies
+        // a chunk that is not the last has stored all its rows after the
+        // copies, with at least one store for each it
         if (more) {
-            data_arrived<IT * CG>();
+            data_arrived<IT>();
             tile_barrier();
             if (shift_of(c + 1)) {
                 fv.clear(vt, shift_of(c + 1), t_);
@@ -735,7 +737,7 @@ __global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
             fv.load(vt + (b ^ 1) * VB, 0, t_);
         }
         typename Shape<T>::frag vf[2][VD / 64];
-        value_frags<T, VD>(vt + b * VB, t_, vf);
+        value_frags<T, KD, VD>(vt + b * VB, t_, vf);
         st.scale(full);
         st.template add<TERMS>(kt + b * KB, t_, vf, wt);
     }
