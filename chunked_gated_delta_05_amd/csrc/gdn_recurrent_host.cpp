@@ -4,7 +4,6 @@
 // checks can be exercised without a GPU.
 #include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include "gdn_recurrent.h"
@@ -90,11 +89,16 @@ gdn_status check_prompt(const gdn_linattn_desc* d, Prompt* p) {
         u.n_units = d->n_units;
         u.offsets = d->offsets_dev;
     }
-    // Segments: enough of them to give every compute unit its two
-    // workgroups, none shorter than four chunks.
-    const int64_t want = getenv("LA_WANT") ? atoi(getenv("LA_WANT")) : 512;
-    int64_t seg = (p->chunks * d->H + want - 1) / want;
-    if (seg < 4) seg = 4;
+    // Segments: as long as 256 workgroups' even share of the heads' chunks.
+    // Shorter ones give each compute unit its second workgroup but cost more
+    // states between them (B=4 T=4096 H=16 bf16: 114 us at 256 and at 512;
+    // its gradients 233 and 256 us; 20 packed documents, T=32768 H=32, which
+    // 512 cuts and 256 does not: 323 and 455 us). At least two chunks, or one
+    // where a chunk's products take fp32 MFMA's time (B=1 T=2048 H=8 at 1, 2
+    // and 4 chunks: bf16 40, 34 and 38 us, fp32 47, 55 and 85 us).
+    int64_t seg = (p->chunks * d->H + 255) / 256;
+    const int64_t least = d->dtype == GDN_DTYPE_F32 ? 1 : 2;
+    if (seg < least) seg = least;
     if (seg > p->longest / kChunk + 1) seg = p->longest / kChunk + 1;
     u.seg_tokens = (int32_t)(seg * kChunk);
     int64_t n = 0;
