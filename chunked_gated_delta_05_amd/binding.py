@@ -11,6 +11,7 @@ been built: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -18,6 +19,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
 
 GDN_OK, GDN_ERR_INVALID, GDN_ERR_UNSUPPORTED, GDN_ERR_DEVICE, GDN_ERR_CAPACITY = range(5)
 LAYOUT_BSND, LAYOUT_TND = 0, 1
@@ -799,134 +801,29 @@ def split_forward(q, k, v, g, beta, scale=None, *, seg, use_exp2=False, initial_
 
 
 # ------------------------------------------------------------------ recurrent-state operators
-# (include/gdn_recurrent.h)
-class LinattnDesc(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H", "Hq", "Hk", "Hv", "K", "V", "dtype", "o_dtype")] + [
-        ("scale", ctypes.c_float), ("n_units", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 2),
-        ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2), ("offsets_host", _i32p),
-        ("offsets_dev", ctypes.c_void_p)]
+# (include/gdn_recurrent.h). Their argument checks, allocations and calls are
+# native (csrc/gdn_torch.cpp): a decode step's kernel takes 4 us, its checks in
+# Python would take 14.
+_NATIVE = None
 
 
-class StepDesc(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "Hq", "Hk", "Hv", "K", "V", "dtype", "o_dtype")] + [
-        ("scale", ctypes.c_float), ("n_pages", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 2),
-        ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2)]
+def _native():
+    """The native marshalling module; raises if it has not been built."""
+    global _NATIVE
+    if _NATIVE is None:
+        lib()   # its own message when nothing is built
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(f"_native.so is not built ({NATIVE_PATH}); run "
+                               "`python -m chunked_gated_delta_05_amd.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._native", NATIVE_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _NATIVE = mod
+    return _NATIVE
 
 
-_RECURRENT = None
-
-
-def _recurrent():
-    """lib() with the argument types of the recurrent-state entry points."""
-    global _RECURRENT
-    if _RECURRENT is None:
-        L = lib()
-        vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-        sz = ctypes.POINTER(ctypes.c_size_t)
-        for name, args in {
-            "gdn_linattn_fwd": [ctypes.POINTER(LinattnDesc)] + [vp] * 8 + [i32, vp, vp, sz, vp],
-            "gdn_linattn_bwd": [ctypes.POINTER(LinattnDesc)] + [vp] * 12 + [sz, vp],
-            "gdn_linattn_step": [ctypes.POINTER(StepDesc)] + [vp] * 8,
-            "gdn_recurrent_step": [ctypes.POINTER(StepDesc), i32, i32] + [vp] * 8 + [i32, vp],
-            "gdn_pages_copy": [vp, i32, vp, i32, i32, i64, vp, vp, i32, vp],
-            "gdn_pages_fork": [vp, i32, i32, i64, vp, vp, i32, vp, i32, vp, vp, vp, vp],
-            "gdn_pages_compact": [vp, i32, i32, i64, vp, i32, vp, vp, vp, vp],
-        }.items():
-            getattr(L, name).restype = ctypes.c_int
-            getattr(L, name).argtypes = args
-        L.gdn_pages_workspace_ints.restype = ctypes.c_size_t
-        L.gdn_pages_workspace_ints.argtypes = [i32]
-        _RECURRENT = L
-    return _RECURRENT
-
-
-def _row_strides(name, t):
-    """(token stride, head stride) in elements of [B,T,h,D] or [tokens,h,D]
-    rows that are contiguous and 16-byte aligned, batch rows at T token
-    strides."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the values of a row must be contiguous")
-    es = t.element_size()
-    ts, hs = t.stride(-3), t.stride(-2)
-    # strides of axes of length one are not used
-    if t.shape[-2] == 1:
-        hs = t.shape[-1]
-    if t.dim() == 4:
-        B, T = t.shape[:2]
-        if B * T <= 1:
-            ts = t.shape[-2] * hs
-        elif T == 1:
-            ts = t.stride(0)
-        elif B > 1 and t.stride(0) != T * ts:
-            raise ValueError(f"{name}: batch rows must follow each other at the token stride")
-    elif t.shape[0] <= 1:
-        ts = t.shape[-2] * hs
-    if (ts * es) % 16 or (hs * es) % 16 or t.data_ptr() % 16 or ts < 0 or hs < 0:
-        raise ValueError(f"{name}: rows must be 16-byte aligned")
-    return ts, hs
-
-
-def _linattn_desc(q, k, v, decay, scale, meta, o_dtype):
-    """Checked descriptor of a prompt: every input against k's dtype, token
-    axes and device."""
-    if k is None or k.dim() not in (3, 4):
-        raise ValueError("linear attention inputs must have shape [B,T,h,K] or [T,h,K]")
-    if k.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"unsupported dtype {k.dtype}")
-    if k.dim() == 3 and meta is None:
-        raise ValueError("packed inputs [T,h,K] need meta")
-    if k.dim() == 4 and meta is not None:
-        raise ValueError("meta goes with packed inputs [T,h,K]")
-    if decay is None or decay.dim() != 1:
-        raise ValueError("decay must be fp32 [H]")
-    H, lead = decay.shape[0], tuple(k.shape[:-2])
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is None or t.dim() != k.dim() or tuple(t.shape[:-2]) != lead:
-            raise ValueError(f"{name} must have shape {lead} + (heads, width)")
-        if t.dtype != k.dtype:
-            raise ValueError(f"{name} must be {k.dtype}, got {t.dtype}")
-        if t.shape[-2] < 1 or H % t.shape[-2]:
-            raise ValueError(f"{name} has {t.shape[-2]} heads, which do not divide the {H} of decay")
-    if q.shape[-1] != k.shape[-1]:
-        raise ValueError(f"q must have k's width {k.shape[-1]}, got {q.shape[-1]}")
-    if o_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported output dtype {o_dtype}")
-    d = LinattnDesc()
-    d.B, d.T = (k.shape[0], k.shape[1]) if k.dim() == 4 else (1, k.shape[0])
-    d.H, d.Hq, d.Hk, d.Hv = H, q.shape[-2], k.shape[-2], v.shape[-2]
-    d.K, d.V = k.shape[-1], v.shape[-1]
-    d.dtype, d.o_dtype = _dtype_code(k.dtype), _dtype_code(o_dtype)
-    d.scale = float(k.shape[-1] ** -0.5 if scale is None else scale)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        getattr(d, name + "_stride")[:] = _row_strides(name, t)
-    if meta is not None:
-        d.n_units = len(meta.offsets) - 1
-        d.offsets_host = ctypes.cast(meta.host, _i32p)
-        d.offsets_dev = meta.offsets_dev.data_ptr()
-    dev = k.device
-    if dev.type != "cuda":
-        raise ValueError(f"inputs must be GPU tensors, got {dev}")
-    for name, t in (("q", q), ("v", v)):
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    _check_tensor("decay", decay, torch.float32, (H,), dev)
-    if meta is not None and meta.offsets_dev.device != dev:
-        raise ValueError(f"unit metadata must be on {dev}, got {meta.offsets_dev.device}")
-    return d
-
-
-def _check_pages(name, pages, n, device):
-    if pages is not None:
-        _check_tensor(name, pages, torch.int32, (n,), device)
-
-
-def _la_workspace(fn, desc, n_ptrs, tail, workspace, dev):
-    nb = ctypes.c_size_t(0)
-    check(fn(ctypes.byref(desc), *([None] * n_ptrs), *tail, None, ctypes.byref(nb), None), "workspace query")
-    ws = workspace if workspace is not None else torch.empty(nb.value, dtype=torch.uint8, device=dev)
-    if ws.dtype != torch.uint8 or ws.device != dev or ws.numel() < nb.value:
-        raise ValueError(f"workspace must be a uint8 tensor of at least {nb.value} bytes on {dev}")
-    return ws, ctypes.c_size_t(ws.numel())
+def _meta_args(meta):
+    return (None, 0, 0) if meta is None else (meta.offsets_dev, len(meta.offsets) - 1, ctypes.addressof(meta.host))
 
 
 def gdn_linattn_fwd(q, k, v, decay, scale=None, *, meta: UnitMeta | None = None, initial_state=None,
@@ -944,34 +841,8 @@ def gdn_linattn_fwd(q, k, v, decay, scale=None, *, meta: UnitMeta | None = None,
     state). final_out likewise with final_pages (-1: not written); it may be
     the pool that initial_state is. out: contiguous [..,H,V] in o_dtype (the
     inputs' dtype by default). Returns (o, final state or None)."""
-    o_dtype = o_dtype or (out.dtype if out is not None else k.dtype)
-    d = _linattn_desc(q, k, v, decay, scale, meta, o_dtype)
-    dev, units = k.device, n_units_of(k, meta)
-    oshape, sshape = (*k.shape[:-2], d.H, d.V), (d.H, d.K, d.V)
-    o = out if out is not None else torch.empty(oshape, dtype=o_dtype, device=dev)
-    _check_tensor("out", o, o_dtype, oshape, dev)
-    _check_pages("initial_pages", initial_pages, units, dev)
-    _check_pages("final_pages", final_pages, units, dev)
-    n_pages = None
-    for name, t, pages in (("initial_state", initial_state, initial_pages), ("final_out", final_out, final_pages)):
-        if pages is not None and (t is None or t.dim() != 4):
-            raise ValueError(f"{name} must be a pool [n_pages,H,K,V] when its pages are given")
-        if t is not None:
-            n = t.shape[0] if pages is not None else units
-            _check_tensor(name, t, torch.float32, (n, *sshape), dev)
-            if pages is not None:
-                if n_pages not in (None, n):
-                    raise ValueError(f"the pools have {n_pages} and {n} pages")
-                n_pages = n
-    fin = final_out
-    if fin is None and output_final_state:
-        fin = torch.empty((units, *sshape), dtype=torch.float32, device=dev)
-    L = _recurrent()
-    ws, nbytes = _la_workspace(L.gdn_linattn_fwd, d, 8, (0, None), workspace, dev)
-    check(L.gdn_linattn_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(initial_state),
-                            _ptr(initial_pages), _ptr(fin), _ptr(final_pages), n_pages or 0, _ptr(o), _ptr(ws),
-                            ctypes.byref(nbytes), _stream(dev)), "gdn_linattn_fwd")
-    return o, fin
+    return (_NATIVE or _native()).linattn_fwd(q, k, v, decay, scale, *_meta_args(meta), initial_state, initial_pages,
+                                              output_final_state, final_out, final_pages, o_dtype, out, workspace)
 
 
 def gdn_linattn_bwd(q, k, v, decay, dout, scale=None, *, meta: UnitMeta | None = None, initial_state=None, dht=None,
@@ -981,21 +852,8 @@ def gdn_linattn_bwd(q, k, v, decay, dout, scale=None, *, meta: UnitMeta | None =
     dk, dv shaped and typed like q, k, v (sums over the heads that share one)
     and dh0 = dL/d(initial state), fp32 [units,H,K,V], when wanted. decay is a
     constant."""
-    d = _linattn_desc(q, k, v, decay, scale, meta, k.dtype)
-    dev, sshape = k.device, (n_units_of(k, meta), d.H, d.K, d.V)
-    _check_tensor("dout", dout, k.dtype, (*k.shape[:-2], d.H, d.V), dev)
-    for name, t in (("initial_state", initial_state), ("dht", dht)):
-        if t is not None:
-            _check_tensor(name, t, torch.float32, sshape, dev)
-    r = {"d" + n: torch.empty(t.shape, dtype=t.dtype, device=dev) for n, t in (("q", q), ("k", k), ("v", v))}
-    if want_dh0:
-        r["dh0"] = torch.empty(sshape, dtype=torch.float32, device=dev)
-    L = _recurrent()
-    ws, nbytes = _la_workspace(L.gdn_linattn_bwd, d, 11, (), workspace, dev)
-    check(L.gdn_linattn_bwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(initial_state), _ptr(dout),
-                            _ptr(dht), _ptr(r["dq"]), _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r.get("dh0")), _ptr(ws),
-                            ctypes.byref(nbytes), _stream(dev)), "gdn_linattn_bwd")
-    return r
+    return (_NATIVE or _native()).linattn_bwd(q, k, v, decay, dout, scale, *_meta_args(meta), initial_state, dht,
+                                              want_dh0, workspace)
 
 
 class LinearAttention(torch.autograd.Function):
@@ -1021,63 +879,13 @@ class LinearAttention(torch.autograd.Function):
         return r["dq"], r["dk"], r["dv"], None, r.get("dh0"), None, None
 
 
-def _step_desc(q, k, v, H, state, scale, pages, o_dtype, out):
-    """Checked descriptor and output of a single-token step."""
-    if k is None or k.dim() != 3:
-        raise ValueError("step inputs must have shape [N, heads, width]")
-    if k.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"unsupported dtype {k.dtype}")
-    N = k.shape[0]
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is None or t.dim() != 3 or t.shape[0] != N:
-            raise ValueError(f"{name} must have shape ({N}, heads, width)")
-        if t.dtype != k.dtype:
-            raise ValueError(f"{name} must be {k.dtype}, got {t.dtype}")
-        if t.shape[1] < 1 or H < 1 or H % t.shape[1]:
-            raise ValueError(f"{name} has {t.shape[1]} heads, which do not divide {H}")
-    if q.shape[-1] != k.shape[-1]:
-        raise ValueError(f"q must have k's width {k.shape[-1]}, got {q.shape[-1]}")
-    K, V = k.shape[-1], v.shape[-1]
-    if state is None or state.dim() != 4:
-        raise ValueError("state must be [n_pages, H, K, V]")
-    o_dtype = o_dtype or (out.dtype if out is not None else k.dtype)
-    if o_dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"unsupported output dtype {o_dtype}")
-    dev = k.device
-    _check_tensor("state", state, torch.float32, (state.shape[0], H, K, V), None)
-    if pages is None and state.shape[0] < N:
-        raise ValueError(f"state has {state.shape[0]} pages for {N} rows")
-    _check_pages("pages", pages, N, None)
-    d = StepDesc()
-    d.N, d.H, d.Hq, d.Hk, d.Hv, d.K, d.V = N, H, q.shape[1], k.shape[1], v.shape[1], K, V
-    d.dtype, d.o_dtype = _dtype_code(k.dtype), _dtype_code(o_dtype)
-    d.scale = float(K ** -0.5 if scale is None else scale)
-    d.n_pages = state.shape[0]
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        getattr(d, name + "_stride")[:] = _row_strides(name, t)
-    if dev.type != "cuda":
-        raise ValueError(f"inputs must be GPU tensors, got {dev}")
-    for name, t in (("q", q), ("v", v), ("state", state), ("pages", pages)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    o = out if out is not None else torch.empty((N, H, V), dtype=o_dtype, device=dev)
-    _check_tensor("out", o, o_dtype, (N, H, V), dev)
-    return d, o
-
-
 def gdn_linattn_step(q, k, v, decay, state, scale=None, *, pages=None, o_dtype=None, out=None):
     """One token of linear attention for N sequences: S = e^decay[h] S + k
     v^T, o = scale S^T q, with S updated in place. q [N,Hq,K], k [N,Hk,K], v
     [N,Hv,V] (strides as in gdn_linattn_fwd); decay fp32 [H]; state: fp32 pool
     [n_pages,H,K,V]; pages: int32 [N], distinct (-1: no sequence, o = 0), or
     None (row n uses page n). Returns o [N,H,V]."""
-    if decay is None or decay.dim() != 1:
-        raise ValueError("decay must be fp32 [H]")
-    d, o = _step_desc(q, k, v, decay.shape[0], state, scale, pages, o_dtype, out)
-    _check_tensor("decay", decay, torch.float32, (d.H,), k.device)
-    check(_recurrent().gdn_linattn_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(pages),
-                                        _ptr(state), _ptr(o), _stream(k.device)), "gdn_linattn_step")
-    return o
+    return (_NATIVE or _native()).linattn_step(q, k, v, decay, state, scale, pages, o_dtype, out)
 
 
 def gdn_recurrent_step(q, k, v, g, beta, state, scale=None, *, pages=None, use_exp2=False, qk_l2norm=False,
@@ -1087,56 +895,18 @@ def gdn_recurrent_step(q, k, v, g, beta, state, scale=None, *, pages=None, use_e
     dividing H, v [N,H,128]; g fp32 [N,H] or [N,H,128] (per key); beta [N,H];
     state and pages as in gdn_linattn_step; use_exp2, qk_l2norm and
     beta_sigmoid as in gdn_chunk_fwd. Returns o [N,H,V]."""
-    if beta is None or beta.dim() != 2:
-        raise ValueError("beta must be [N, H]")
-    H = beta.shape[1]
-    if g is None or g.dim() not in (2, 3):
-        raise ValueError("g must be [N, H] (scalar gate) or [N, H, K] (per-key gate)")
-    d, o = _step_desc(q, k, v, H, state, scale, pages, o_dtype, out)
-    _check_tensor("g", g, torch.float32, (d.N, H) if g.dim() == 2 else (d.N, H, d.K), k.device)
-    _check_tensor("beta", beta, k.dtype, (d.N, H), k.device)
     flags = (FLAG_QK_L2NORM if qk_l2norm else 0) | (FLAG_BETA_SIGMOID if beta_sigmoid else 0)
-    check(_recurrent().gdn_recurrent_step(ctypes.byref(d), GATE_PER_KEY if g.dim() == 3 else GATE_SCALAR,
-                                          int(bool(use_exp2)), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                          _ptr(pages), _ptr(state), _ptr(o), flags, _stream(k.device)),
-          "gdn_recurrent_step")
-    return o
+    return (_NATIVE or _native()).recurrent_step(q, k, v, g, beta, state, scale, pages, use_exp2, flags, o_dtype, out)
 
 
 # ------------------------------------------------------------------ pages of a cache
-def _check_pool(name, pool):
-    """(layers, pages, bytes of a page) of a contiguous [layers, pages, ...] pool."""
-    if pool is None or pool.dim() < 3:
-        raise ValueError(f"{name} must be [n_layers, n_pages, ...]")
-    if not pool.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    nb = pool.element_size()
-    for x in pool.shape[2:]:
-        nb *= x
-    if nb == 0 or nb % 16 or pool.data_ptr() % 16:
-        raise ValueError(f"{name}: pages must be a multiple of 16 bytes and 16-byte aligned, got {nb} bytes")
-    if pool.device.type != "cuda":
-        raise ValueError(f"{name} must be a GPU tensor, got {pool.device}")
-    return pool.shape[0], pool.shape[1], nb
-
-
 def gdn_pages_copy(dst_pool, src_pool, dst_pages, src_pages):
     """Page dst_pages[i] of dst_pool = page src_pages[i] of src_pool, in every
     layer. Pools [n_layers, n_pages, ...] of one dtype, layer count and page
     shape (they may be one pool; the destinations must then be distinct and
     none a source); pages int32 on the GPU, pairs with a page out of range
     skipped."""
-    layers, dn, nb = _check_pool("dst_pool", dst_pool)
-    sl, sn, snb = _check_pool("src_pool", src_pool)
-    if src_pool.dtype != dst_pool.dtype or sl != layers or src_pool.shape[2:] != dst_pool.shape[2:]:
-        raise ValueError("the pools differ in dtype, layers or page shape")
-    if src_pool.device != dst_pool.device:
-        raise ValueError(f"src_pool must be on {dst_pool.device}, got {src_pool.device}")
-    n = dst_pages.numel()
-    _check_tensor("dst_pages", dst_pages, torch.int32, (n,), dst_pool.device)
-    _check_tensor("src_pages", src_pages, torch.int32, (n,), dst_pool.device)
-    check(_recurrent().gdn_pages_copy(_ptr(dst_pool), dn, _ptr(src_pool), sn, layers, nb, _ptr(dst_pages),
-                                      _ptr(src_pages), n, _stream(dst_pool.device)), "gdn_pages_copy")
+    (_NATIVE or _native()).pages_copy(dst_pool, src_pool, dst_pages, src_pages)
 
 
 def gdn_pages_fork(pool, table, parent, *, spare=None):
@@ -1145,33 +915,11 @@ def gdn_pages_fork(pool, table, parent, *, spare=None):
     keeps its page, the others get copies in the pages of childless slots
     (ascending), then in spare ones; a child that finds none gets -1. Returns
     (new table [n], free pages not taken [n + len(spare)], then -1)."""
-    layers, pages, nb = _check_pool("pool", pool)
-    dev, n = pool.device, table.numel()
-    _check_tensor("table", table, torch.int32, (n,), dev)
-    _check_tensor("parent", parent, torch.int32, (n,), dev)
-    m = 0 if spare is None else spare.numel()
-    if spare is not None:
-        _check_tensor("spare", spare, torch.int32, (m,), dev)
-    L = _recurrent()
-    new = torch.empty((n,), dtype=torch.int32, device=dev)
-    left = torch.empty((n + m,), dtype=torch.int32, device=dev)
-    ws = torch.empty((L.gdn_pages_workspace_ints(n),), dtype=torch.int32, device=dev)
-    check(L.gdn_pages_fork(_ptr(pool), layers, pages, nb, _ptr(table), _ptr(parent), n, _ptr(spare), m, _ptr(new),
-                           _ptr(left), _ptr(ws), _stream(dev)), "gdn_pages_fork")
-    return new, left
+    return (_NATIVE or _native()).pages_fork(pool, table, parent, spare)
 
 
 def gdn_pages_compact(pool, table):
     """Moves the pages that table (int32 [n]) names into the pool's first
     ones, in place: pages below their number stay, the others move, in order,
     into the holes. Returns (new table [n], the number of pages in use [1])."""
-    layers, pages, nb = _check_pool("pool", pool)
-    dev, n = pool.device, table.numel()
-    _check_tensor("table", table, torch.int32, (n,), dev)
-    L = _recurrent()
-    new = torch.empty((n,), dtype=torch.int32, device=dev)
-    count = torch.empty((1,), dtype=torch.int32, device=dev)
-    ws = torch.empty((L.gdn_pages_workspace_ints(pages),), dtype=torch.int32, device=dev)
-    check(L.gdn_pages_compact(_ptr(pool), layers, pages, nb, _ptr(table), n, _ptr(new), _ptr(count), _ptr(ws),
-                              _stream(dev)), "gdn_pages_compact")
-    return new, count
+    return (_NATIVE or _native()).pages_compact(pool, table)

@@ -3,18 +3,21 @@
     python -m chunked_gated_delta_05_amd.build [-v]
 
 hipcc compiles the kernels and the host API into one shared library next to
-this file. Packed FP32 instructions are disabled for all device code.
+this file, and g++ the torch marshalling of the recurrent-state operators
+(_native.so). Packed FP32 instructions are disabled for all device code.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn.so")
+NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_host.cpp"),
            os.path.join(CSRC, "gdn_noalloc.hip"), os.path.join(CSRC, "gdn_bwd.hip")]
 # the recurrent-state operators of include/gdn_recurrent.h
@@ -68,7 +71,25 @@ def build(verbose: bool = False) -> str:
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", kobj, hobj, nobj, bobj, *robjs, "-o", LIB + ".tmp"],
          verbose)
     os.replace(LIB + ".tmp", LIB)
+    _build_native(inc, verbose)
     return LIB
+
+
+def _build_native(inc, verbose):
+    """_native.so: torch marshalling of the recurrent-state operators (host
+    code; CPython's C API and torch's C++ headers)."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    tinc = [x for p in include_paths() for x in ("-isystem", p)]
+    tlib = [x for p in library_paths() for x in ("-L" + p, "-Wl,-rpath," + p)]
+    _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, *tinc,
+          "-isystem", sysconfig.get_path("include"), "-isystem", "/opt/rocm/include",
+          os.path.join(CSRC, "gdn_torch.cpp"), "-o", NATIVE + ".tmp",
+          "-L" + HERE, "-l:libgdn.so", "-Wl,-rpath,$ORIGIN", *tlib, "-lc10", "-lc10_hip", "-ltorch_cpu",
+          "-ltorch_python"], verbose)
+    os.replace(NATIVE + ".tmp", NATIVE)
 
 
 if __name__ == "__main__":

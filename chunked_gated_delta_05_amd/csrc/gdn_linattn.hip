@@ -181,7 +181,7 @@ __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t at, uint3
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(at), "s"(base)
-                 : "memory", "m0");
+                 : "memory");
 }
 // waits until at most the LATER youngest of this wave's memory accesses are
 // in flight
