@@ -385,7 +385,7 @@ extern "C" gdn_status gdn_pages_copy(void* dst_pool, int32_t dst_n_pages, const 
     if (n < 0 || (n > 0 && (!dst_pages || !src_pages))) return GDN_ERR_INVALID;
     const gdn::PoolArgs a{static_cast<char*>(dst_pool), static_cast<const char*>(src_pool), n_layers, dst_n_pages,
                           src_n_pages, page_bytes};
-    return run(gdn::launch_pages_copy(a, dst_pages, src_pages, n, nullptr, stream));
+    return run(gdn::launch_pages_copy(a, dst_pages, src_pages, n, nullptr, true, stream));
 }
 
 extern "C" gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes,
@@ -403,7 +403,7 @@ extern "C" gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pag
         return GDN_ERR_DEVICE;
     const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
                           page_bytes};
-    return run(gdn::launch_pages_copy(a, workspace + 1 + n_slots, workspace + 1, n_slots, workspace, stream));
+    return run(gdn::launch_pages_copy(a, workspace + 1 + n_slots, workspace + 1, n_slots, workspace, false, stream));
 }
 
 extern "C" gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes,
@@ -419,5 +419,5 @@ extern "C" gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_
         return GDN_ERR_DEVICE;
     const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
                           page_bytes};
-    return run(gdn::launch_pages_copy(a, workspace + 1 + n_pages, workspace + 1, n_pages, workspace, stream));
+    return run(gdn::launch_pages_copy(a, workspace + 1 + n_pages, workspace + 1, n_pages, workspace, true, stream));
 }

@@ -11,6 +11,10 @@
 
 namespace gdn {
 
+// Memory that a call walks through is read and written around the caches
+// where it exceeds the last-level cache, which it would only flush.
+constexpr int64_t LAST_LEVEL_BYTES = int64_t(256) << 20;
+
 // Rows of q, k or v: token / head distances in elements, and how many of the
 // H heads share one.
 struct RowsOf {
@@ -90,9 +94,10 @@ struct PoolArgs {
     int32_t n_layers, dst_pages, src_pages;
     int64_t page_bytes;
 };
-// pairs: n on the host, or *n_dev of at most n
+// pairs: n on the host, or *n_dev of at most n. read_once: no page is the
+// source of several
 hipError_t launch_pages_copy(const PoolArgs& pool, const int32_t* dst_pages, const int32_t* src_pages, int n,
-                             const int32_t* n_dev, hipStream_t s);
+                             const int32_t* n_dev, bool read_once, hipStream_t s);
 // The plans write their copies to the workspace: [0] the count, then sources
 // and destinations of n each.
 hipError_t launch_fork_plan(int n_pages, const int32_t* table, const int32_t* parent, int n, const int32_t* spare,

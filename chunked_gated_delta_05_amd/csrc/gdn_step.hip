@@ -35,8 +35,8 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 
 // KIND: 0 linear attention, 1 delta rule with a scalar gate, 2 with a
-// per-key gate
-template <typename T, int KD, int VD, int VS, int KIND>
+// per-key gate. AROUND: the states are read and written around the caches
+template <typename T, int KD, int VD, int VS, int KIND, bool AROUND>
 __global__ __launch_bounds__(NT) void step_kernel(StepArgs a) {
     constexpr int CL = VS / 4;          // lanes across the columns, 16 bytes each
     constexpr int RG = NT / CL;         // rows in flight per pass
@@ -60,7 +60,15 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs a) {
     float* S = a.state + ((int64_t)page * a.H + h) * (KD * VD) + sl * VS + 4 * cl;
     f32x4 s[RPT];
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) s[i] = *reinterpret_cast<const f32x4*>(S + (rg + RG * i) * VD);
+    for (int i = 0; i < RPT; ++i) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(S + (rg + RG * i) * VD);
+        s[i] = AROUND ? __builtin_nontemporal_load(p) : *p;
+    }
+    auto put = [&](int i) {
+        f32x4* p = reinterpret_cast<f32x4*>(S + (rg + RG * i) * VD);
+        if constexpr (AROUND) __builtin_nontemporal_store(s[i], p);
+        else *p = s[i];
+    };
 
     const T* q = static_cast<const T*>(a.q.p) + n * a.q.ts + (h / a.q.share) * a.q.hs;
     const T* k = static_cast<const T*>(a.k.p) + n * a.k.ts + (h / a.k.share) * a.k.hs;
@@ -136,7 +144,7 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs a) {
     }
     if constexpr (KIND == 0) {
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) *reinterpret_cast<f32x4*>(S + (rg + RG * i) * VD) = s[i];
+        for (int i = 0; i < RPT; ++i) put(i);
     }
     lds_barrier();
     sq = part[0][0][cl] + part[0][1][cl] + part[0][2][cl] + part[0][3][cl];
@@ -145,9 +153,8 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs a) {
         const f32x4 br = beta * (vv - sk);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            const int r = rg + RG * i;
-            s[i] += (ks[r] * rk) * br;
-            *reinterpret_cast<f32x4*>(S + r * VD) = s[i];
+            s[i] += (ks[rg + RG * i] * rk) * br;
+            put(i);
         }
         sq = sq * rq + kq * br;
     }
@@ -157,11 +164,18 @@ __global__ __launch_bounds__(NT) void step_kernel(StepArgs a) {
 template <typename T, int KD, int VD, int KIND>
 hipError_t launch(const StepArgs& a, hipStream_t s) {
     const int64_t states = (int64_t)a.N * a.H;
+    // Few states: 32 columns a workgroup, for four times the workgroups (16
+    // states: 3.6 us a kernel). Many: all columns, so that a workgroup's 64 KiB
+    // lie together (8192 states: 211 us against 216). Beyond the last-level
+    // cache around the caches (8192 states, 512 MB: 211 to 188 us), within it
+    // through them (4096 states, 256 MB: 80 us against 94).
     if (states < 512) {
         constexpr int VS = 32;
-        step_kernel<T, KD, VD, VS, KIND><<<(unsigned)(states * (VD / VS)), NT, 0, s>>>(a);
+        step_kernel<T, KD, VD, VS, KIND, false><<<(unsigned)(states * (VD / VS)), NT, 0, s>>>(a);
+    } else if (states * (KD * VD * 4) <= LAST_LEVEL_BYTES) {
+        step_kernel<T, KD, VD, VD, KIND, false><<<(unsigned)states, NT, 0, s>>>(a);
     } else {
-        step_kernel<T, KD, VD, VD, KIND><<<(unsigned)states, NT, 0, s>>>(a);
+        step_kernel<T, KD, VD, VD, KIND, true><<<(unsigned)states, NT, 0, s>>>(a);
     }
     return hipGetLastError();
 }
