@@ -1,7 +1,10 @@
 // The pages of a state cache: explicit copies, forking a batch of beams and
-// compacting. Fork and compaction are a plan (one workgroup: who keeps, who
-// copies, what is free, written to the caller's workspace) followed by the
-// copies, whose number only the device knows: a fixed grid walks the list.
+// compacting. Fork and compaction are a plan (who keeps, who copies, what is
+// free) and the copies it lists, whose number only the device knows: a fixed
+// grid walks the list. Few slots or pages: one kernel, in which every
+// workgroup makes the plan for itself in LDS and the first writes the new
+// table. Many: the plan is a kernel of one workgroup that leaves its list in
+// the caller's workspace.
 #include "gdn_device.h"
 #include "gdn_recurrent_internal.h"
 
@@ -11,20 +14,15 @@ namespace {
 
 constexpr int NT = 256;        // threads of the copy kernel
 constexpr int PIECE = 16384;   // bytes a workgroup copies at a time: 4 x 16 bytes a thread in flight
-constexpr int COPY_WGS = 1024; // 4 workgroups per compute unit
 constexpr int PT = 1024;       // threads of the plans
 
+// The first n pairs of the lists, every layer, spread over the grid.
 // NT_LOAD, NT_STORE: around the caches. Pools beyond the last-level cache
 // (1.6 GB forked, 1.1 GB compacted): stores around it take 316 to 304 us and
 // 203 to 196 us, loads as well 189 us where every page is read once, but 320
 // where beams share parents, whose pages the caches serve.
 template <bool NT_LOAD, bool NT_STORE>
-__global__ __launch_bounds__(NT) void copy_kernel(PoolArgs a, const int32_t* dst_pages, const int32_t* src_pages,
-                                                  int n, const int32_t* n_dev) {
-    if (n_dev) {
-        const int c = *n_dev;
-        n = c < 0 ? 0 : (c < n ? c : n);
-    }
+__device__ __forceinline__ void copy_pairs(const PoolArgs& a, const int32_t* dst_pages, const int32_t* src_pages, int n) {
     const int64_t pieces = (a.page_bytes + PIECE - 1) / PIECE;
     const int64_t per_pair = pieces * a.n_layers, items = per_pair * n;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -54,7 +52,18 @@ __global__ __launch_bounds__(NT) void copy_kernel(PoolArgs a, const int32_t* dst
     }
 }
 
+template <bool NT_LOAD, bool NT_STORE>
+__global__ __launch_bounds__(NT) void copy_kernel(PoolArgs a, const int32_t* dst_pages, const int32_t* src_pages,
+                                                  int n, const int32_t* n_dev) {
+    if (n_dev) {
+        const int c = *n_dev;
+        n = c < 0 ? 0 : (c < n ? c : n);
+    }
+    copy_pairs<NT_LOAD, NT_STORE>(a, dst_pages, src_pages, n);
+}
+
 // Exclusive sum of x over the workgroup's threads; total: the whole sum.
+template <int THREADS>
 __device__ __forceinline__ int block_scan(int x, int* total, int* waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int s = x;
@@ -67,7 +76,7 @@ __device__ __forceinline__ int block_scan(int x, int* total, int* waves) {
     if (lane == 63) waves[wave] = s;
     __syncthreads();
     int before = 0, all = 0;
-    for (int w = 0; w < PT / 64; ++w) {
+    for (int w = 0; w < THREADS / 64; ++w) {
         if (w < wave) before += waves[w];
         all += waves[w];
     }
@@ -80,26 +89,32 @@ __device__ __forceinline__ bool is_page(int p, int n_pages) { return p >= 0 && p
 // Every slot i: its source page is table[parent[i]]; the lowest child of a
 // slot keeps it, the e-th other child copies into the e-th free page. A slot
 // range of its own for each thread keeps the scans in slot order.
-__global__ __launch_bounds__(PT) void fork_plan_kernel(int n_pages, const int32_t* table, const int32_t* parent, int n,
-                                                       const int32_t* spare, int m, int32_t* new_table, int32_t* left,
-                                                       int32_t* ws) {
-    __shared__ int lowest[FORK_MAX];
-    __shared__ int waves[PT / 64];
-    const int tid = threadIdx.x;
-    for (int i = tid; i < n; i += PT) lowest[i] = n;
-    for (int i = tid; i < n + m; i += PT) left[i] = -1;
+struct ForkArgs {
+    int n_pages, n, m;
+    const int32_t *table, *parent, *spare;
+    int32_t *new_table, *left;
+};
+// Returns the number of copies, listed in src and dst; write: also the new
+// table and the pages left. lowest[n] and waves in LDS.
+template <int THREADS>
+__device__ int fork_plan(const ForkArgs& f, int32_t* src, int32_t* dst, bool write, int* lowest, int* waves) {
+    const int n = f.n, m = f.m, n_pages = f.n_pages, tid = threadIdx.x;
+    const int32_t *table = f.table, *parent = f.parent, *spare = f.spare;
+    for (int i = tid; i < n; i += THREADS) lowest[i] = n;
+    if (write)
+        for (int i = tid; i < n + m; i += THREADS) f.left[i] = -1;
     __syncthreads();
     auto source = [&](int i) {   // the slot that i continues, or -1
         const int p = parent[i];
         return p >= 0 && p < n && is_page(table[p], n_pages) ? p : -1;
     };
-    for (int i = tid; i < n; i += PT) {
+    for (int i = tid; i < n; i += THREADS) {
         const int p = source(i);
         if (p >= 0) atomicMin(&lowest[p], i);
     }
     __syncthreads();
-    const int per = (n + PT - 1) / PT, lo = min(tid * per, n), hi = min(lo + per, n);
-    const int mper = (m + PT - 1) / PT, mlo = min(tid * mper, m), mhi = min(mlo + mper, m);
+    const int per = (n + THREADS - 1) / THREADS, lo = min(tid * per, n), hi = min(lo + per, n);
+    const int mper = (m + THREADS - 1) / THREADS, mlo = min(tid * mper, m), mhi = min(mlo + mper, m);
     int extra = 0, dead = 0, spares = 0;
     for (int i = lo; i < hi; ++i) {
         const int p = source(i);
@@ -108,16 +123,14 @@ __global__ __launch_bounds__(PT) void fork_plan_kernel(int n_pages, const int32_
     }
     for (int i = mlo; i < mhi; ++i) spares += is_page(spare[i], n_pages);
     int n_extra, n_dead, n_spare;
-    int e = block_scan(extra, &n_extra, waves);
-    int d = block_scan(dead, &n_dead, waves);
-    int sp = n_dead + block_scan(spares, &n_spare, waves);
+    int e = block_scan<THREADS>(extra, &n_extra, waves);
+    int d = block_scan<THREADS>(dead, &n_dead, waves);
+    int sp = n_dead + block_scan<THREADS>(spares, &n_spare, waves);
     const int copies = min(n_extra, n_dead + n_spare);
-    int32_t* src = ws + 1;
-    int32_t* dst = ws + 1 + n;
     // the free pages in order: the first `copies` are destinations, the rest is left
     auto free_page = [&](int rank, int page) {
         if (rank < copies) dst[rank] = page;
-        else left[rank - copies] = page;
+        else if (write) f.left[rank - copies] = page;
     };
     for (int i = lo; i < hi; ++i)
         if (lowest[i] == n && is_page(table[i], n_pages)) free_page(d++, table[i]);
@@ -136,31 +149,57 @@ __global__ __launch_bounds__(PT) void fork_plan_kernel(int n_pages, const int32_
             }
             ++e;
         }
-        new_table[i] = page;
+        if (write) f.new_table[i] = page;
     }
-    if (tid == 0) ws[0] = copies;
+    return copies;
 }
+
+__global__ __launch_bounds__(PT) void fork_plan_kernel(ForkArgs f, int32_t* ws) {
+    __shared__ int lowest[FORK_MAX];
+    __shared__ int waves[PT / 64];
+    const int copies = fork_plan<PT>(f, ws + 1, ws + 1 + f.n, true, lowest, waves);
+    if (threadIdx.x == 0) ws[0] = copies;
+}
+
+// At most FORK_SMALL slots and spare pages: one kernel for two (8 slots, 8 MB:
+// 8.1 to 5.6 us)
+constexpr int FORK_SMALL = 256;
+template <bool NT_STORE>
+__global__ __launch_bounds__(NT) void fork_kernel(PoolArgs a, ForkArgs f) {
+    __shared__ int lowest[FORK_SMALL], src[FORK_SMALL], dst[FORK_SMALL];
+    __shared__ int waves[NT / 64];
+    const int copies = fork_plan<NT>(f, src, dst, blockIdx.x == 0, lowest, waves);
+    __syncthreads();
+    copy_pairs<false, NT_STORE>(a, dst, src, copies);
+}
+
 
 // A bit for each used page; a page's rank among the pages that move, and a
 // hole's rank among the holes, are counts of bits before it.
-__global__ __launch_bounds__(PT) void compact_plan_kernel(int n_pages, const int32_t* table, int n, int32_t* new_table,
-                                                          int32_t* count, int32_t* ws) {
-    constexpr int WORDS = COMPACT_MAX / 32;
-    __shared__ uint32_t used[WORDS];
-    __shared__ int movers_before[WORDS];
-    __shared__ int waves[PT / 64];
-    const int tid = threadIdx.x, words = (n_pages + 31) / 32;
-    for (int w = tid; w < words; w += PT) used[w] = 0;
+struct CompactArgs {
+    int n_pages, n;
+    const int32_t* table;
+    int32_t *new_table, *count;
+};
+// Returns the number of moves, listed in src and dst; write: also the new
+// table and the count. used[], movers_before[] (a word for 32 pages) and
+// waves in LDS.
+template <int THREADS>
+__device__ int compact_plan(const CompactArgs& f, int32_t* src, int32_t* dst, bool write, uint32_t* used,
+                            int* movers_before, int* waves) {
+    const int n_pages = f.n_pages, n = f.n, tid = threadIdx.x, words = (n_pages + 31) / 32;
+    const int32_t* table = f.table;
+    for (int w = tid; w < words; w += THREADS) used[w] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += PT) {
+    for (int i = tid; i < n; i += THREADS) {
         const int p = table[i];
         if (is_page(p, n_pages)) atomicOr(&used[p >> 5], 1u << (p & 31));
     }
     __syncthreads();
-    const int per = (words + PT - 1) / PT, lo = min(tid * per, words), hi = min(lo + per, words);
+    const int per = (words + THREADS - 1) / THREADS, lo = min(tid * per, words), hi = min(lo + per, words);
     int mine = 0, total;
     for (int w = lo; w < hi; ++w) mine += __popc(used[w]);
-    block_scan(mine, &total, waves);
+    block_scan<THREADS>(mine, &total, waves);
     // bits of word w that are pages below the count
     auto below = [&](int w) -> uint32_t {
         const int b = total - 32 * w;
@@ -171,56 +210,112 @@ __global__ __launch_bounds__(PT) void compact_plan_kernel(int n_pages, const int
         movers += __popc(used[w] & ~below(w));
         holes += __popc(~used[w] & below(w));
     }
-    int mv = block_scan(movers, &n_movers, waves);
-    int ho = block_scan(holes, &n_holes, waves);
-    int32_t* src = ws + 1;
-    int32_t* dst = ws + 1 + n_pages;
+    int mv = block_scan<THREADS>(movers, &n_movers, waves);
+    int ho = block_scan<THREADS>(holes, &n_holes, waves);
     for (int w = lo; w < hi; ++w) {
         movers_before[w] = mv;
         for (uint32_t b = used[w] & ~below(w); b; b &= b - 1) src[mv++] = 32 * w + __ffs(b) - 1;
         for (uint32_t b = ~used[w] & below(w); b; b &= b - 1) dst[ho++] = 32 * w + __ffs(b) - 1;
     }
     __syncthreads();
-    for (int i = tid; i < n; i += PT) {
-        int p = table[i];
-        if (!is_page(p, n_pages)) {
-            p = -1;
-        } else if (p >= total) {
-            const int w = p >> 5;
-            p = dst[movers_before[w] + __popc(used[w] & ~below(w) & ((1u << (p & 31)) - 1u))];
+    if (write) {
+        for (int i = tid; i < n; i += THREADS) {
+            int p = table[i];
+            if (!is_page(p, n_pages)) {
+                p = -1;
+            } else if (p >= total) {
+                const int w = p >> 5;
+                p = dst[movers_before[w] + __popc(used[w] & ~below(w) & ((1u << (p & 31)) - 1u))];
+            }
+            f.new_table[i] = p;
         }
-        new_table[i] = p;
+        if (tid == 0) *f.count = total;
     }
-    if (tid == 0) {
-        *count = total;
-        ws[0] = n_movers;
-    }
+    return n_movers;
+}
+
+__global__ __launch_bounds__(PT) void compact_plan_kernel(CompactArgs f, int32_t* ws) {
+    __shared__ uint32_t used[COMPACT_MAX / 32];
+    __shared__ int movers_before[COMPACT_MAX / 32];
+    __shared__ int waves[PT / 64];
+    const int moves = compact_plan<PT>(f, ws + 1, ws + 1 + f.n_pages, true, used, movers_before, waves);
+    if (threadIdx.x == 0) ws[0] = moves;
+}
+
+// At most COMPACT_SMALL pages and slots
+constexpr int COMPACT_SMALL = 1024;
+template <bool AROUND>
+__global__ __launch_bounds__(NT) void compact_kernel(PoolArgs a, CompactArgs f) {
+    __shared__ uint32_t used[COMPACT_SMALL / 32];
+    __shared__ int movers_before[COMPACT_SMALL / 32], src[COMPACT_SMALL], dst[COMPACT_SMALL];
+    __shared__ int waves[NT / 64];
+    const int moves = compact_plan<NT>(f, src, dst, blockIdx.x == 0, used, movers_before, waves);
+    __syncthreads();
+    copy_pairs<AROUND, AROUND>(a, dst, src, moves);
+}
+
+}  // namespace
+
+namespace {
+
+bool beyond_caches(const PoolArgs& pool) {
+    return (int64_t)pool.n_layers * pool.src_pages * pool.page_bytes > LAST_LEVEL_BYTES;
+}
+// Workgroups for at most n pairs: four a compute unit, each making the plan
+// once; beyond the caches, where copying takes far longer than a plan, four
+// times as many, which even out (3.2 GB, 128 slots: 284 to 259 us forked, 313
+// to 273 compacted; 80 MB, 20 slots: 8.0 us at 1024, 9.9 at 4096).
+unsigned copy_blocks(const PoolArgs& pool, int n) {
+    const int64_t items = (pool.page_bytes + PIECE - 1) / PIECE * pool.n_layers * n;
+    const int64_t most = beyond_caches(pool) ? 4096 : 1024;
+    return (unsigned)(items < most ? items : most);
+}
+
+// read_once: no page is the source of several
+hipError_t copy_listed(const PoolArgs& pool, const int32_t* dst_pages, const int32_t* src_pages, int n,
+                       const int32_t* n_dev, bool read_once, hipStream_t s) {
+    const unsigned blocks = copy_blocks(pool, n);
+    if (blocks == 0) return hipSuccess;
+    if (!beyond_caches(pool)) copy_kernel<false, false><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
+    else if (read_once) copy_kernel<true, true><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
+    else copy_kernel<false, true><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_pages_copy(const PoolArgs& pool, const int32_t* dst_pages, const int32_t* src_pages, int n,
-                             const int32_t* n_dev, bool read_once, hipStream_t s) {
-    const int64_t items = (pool.page_bytes + PIECE - 1) / PIECE * pool.n_layers * n;
-    if (items == 0) return hipSuccess;
-    const unsigned blocks = (unsigned)(items < COPY_WGS ? items : COPY_WGS);
-    const bool large = (int64_t)pool.n_layers * pool.src_pages * pool.page_bytes > LAST_LEVEL_BYTES;
-    if (large && read_once) copy_kernel<true, true><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
-    else if (large) copy_kernel<false, true><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
-    else copy_kernel<false, false><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
-    return hipGetLastError();
+                             hipStream_t s) {
+    return copy_listed(pool, dst_pages, src_pages, n, nullptr, true, s);
 }
 
-hipError_t launch_fork_plan(int n_pages, const int32_t* table, const int32_t* parent, int n, const int32_t* spare,
-                            int m, int32_t* new_table, int32_t* left, int32_t* ws, hipStream_t s) {
-    fork_plan_kernel<<<1, PT, 0, s>>>(n_pages, table, parent, n, spare, m, new_table, left, ws);
-    return hipGetLastError();
+hipError_t launch_fork(const PoolArgs& pool, const int32_t* table, const int32_t* parent, int n, const int32_t* spare,
+                       int m, int32_t* new_table, int32_t* left, int32_t* ws, hipStream_t s) {
+    const ForkArgs f{pool.src_pages, n, m, table, parent, spare, new_table, left};
+    if (n <= FORK_SMALL && m <= FORK_SMALL) {
+        const unsigned blocks = copy_blocks(pool, n);
+        if (beyond_caches(pool)) fork_kernel<true><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
+        else fork_kernel<false><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
+        return hipGetLastError();
+    }
+    fork_plan_kernel<<<1, PT, 0, s>>>(f, ws);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : copy_listed(pool, ws + 1 + n, ws + 1, n, ws, false, s);
 }
 
-hipError_t launch_compact_plan(int n_pages, const int32_t* table, int n, int32_t* new_table, int32_t* count,
-                               int32_t* ws, hipStream_t s) {
-    compact_plan_kernel<<<1, PT, 0, s>>>(n_pages, table, n, new_table, count, ws);
-    return hipGetLastError();
+hipError_t launch_compact(const PoolArgs& pool, const int32_t* table, int n, int32_t* new_table, int32_t* count,
+                          int32_t* ws, hipStream_t s) {
+    const int n_pages = pool.src_pages;
+    const CompactArgs f{n_pages, n, table, new_table, count};
+    if (n_pages <= COMPACT_SMALL && n <= COMPACT_SMALL) {
+        const unsigned blocks = copy_blocks(pool, n_pages);
+        if (beyond_caches(pool)) compact_kernel<true><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
+        else compact_kernel<false><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
+        return hipGetLastError();
+    }
+    compact_plan_kernel<<<1, PT, 0, s>>>(f, ws);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : copy_listed(pool, ws + 1 + n_pages, ws + 1, n_pages, ws, true, s);
 }
 
 }  // namespace gdn

@@ -385,7 +385,7 @@ extern "C" gdn_status gdn_pages_copy(void* dst_pool, int32_t dst_n_pages, const 
     if (n < 0 || (n > 0 && (!dst_pages || !src_pages))) return GDN_ERR_INVALID;
     const gdn::PoolArgs a{static_cast<char*>(dst_pool), static_cast<const char*>(src_pool), n_layers, dst_n_pages,
                           src_n_pages, page_bytes};
-    return run(gdn::launch_pages_copy(a, dst_pages, src_pages, n, nullptr, true, stream));
+    return run(gdn::launch_pages_copy(a, dst_pages, src_pages, n, stream));
 }
 
 extern "C" gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes,
@@ -398,12 +398,9 @@ extern "C" gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pag
     if (n_slots > gdn::FORK_MAX || n_spare > gdn::FORK_MAX) return GDN_ERR_UNSUPPORTED;
     if (n_slots > 0 && (!table || !parent || !new_table || new_table == table)) return GDN_ERR_INVALID;
     if ((n_spare > 0 && !spare) || (n_slots + n_spare > 0 && !left) || !workspace) return GDN_ERR_INVALID;
-    if (gdn::launch_fork_plan(n_pages, table, parent, n_slots, spare, n_spare, new_table, left, workspace, stream) !=
-        hipSuccess)
-        return GDN_ERR_DEVICE;
     const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
                           page_bytes};
-    return run(gdn::launch_pages_copy(a, workspace + 1 + n_slots, workspace + 1, n_slots, workspace, false, stream));
+    return run(gdn::launch_fork(a, table, parent, n_slots, spare, n_spare, new_table, left, workspace, stream));
 }
 
 extern "C" gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes,
@@ -415,9 +412,7 @@ extern "C" gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_
     if (n_pages > gdn::COMPACT_MAX) return GDN_ERR_UNSUPPORTED;
     if (n_slots > 0 && (!table || !new_table || new_table == table)) return GDN_ERR_INVALID;
     if (!count || !workspace) return GDN_ERR_INVALID;
-    if (gdn::launch_compact_plan(n_pages, table, n_slots, new_table, count, workspace, stream) != hipSuccess)
-        return GDN_ERR_DEVICE;
     const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
                           page_bytes};
-    return run(gdn::launch_pages_copy(a, workspace + 1 + n_pages, workspace + 1, n_pages, workspace, true, stream));
+    return run(gdn::launch_compact(a, table, n_slots, new_table, count, workspace, stream));
 }

@@ -94,15 +94,13 @@ struct PoolArgs {
     int32_t n_layers, dst_pages, src_pages;
     int64_t page_bytes;
 };
-// pairs: n on the host, or *n_dev of at most n. read_once: no page is the
-// source of several
 hipError_t launch_pages_copy(const PoolArgs& pool, const int32_t* dst_pages, const int32_t* src_pages, int n,
-                             const int32_t* n_dev, bool read_once, hipStream_t s);
-// The plans write their copies to the workspace: [0] the count, then sources
-// and destinations of n each.
-hipError_t launch_fork_plan(int n_pages, const int32_t* table, const int32_t* parent, int n, const int32_t* spare,
-                            int m, int32_t* new_table, int32_t* left, int32_t* ws, hipStream_t s);
-hipError_t launch_compact_plan(int n_pages, const int32_t* table, int n, int32_t* new_table, int32_t* count,
-                               int32_t* ws, hipStream_t s);
+                             hipStream_t s);
+// ws: where many slots or pages make a plan of its own, the count of copies,
+// then sources and destinations of n each
+hipError_t launch_fork(const PoolArgs& pool, const int32_t* table, const int32_t* parent, int n, const int32_t* spare,
+                       int m, int32_t* new_table, int32_t* left, int32_t* ws, hipStream_t s);
+hipError_t launch_compact(const PoolArgs& pool, const int32_t* table, int n, int32_t* new_table, int32_t* count,
+                          int32_t* ws, hipStream_t s);
 
 }  // namespace gdn
