@@ -377,7 +377,8 @@ struct State {
 #pragma unroll
             for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f32x4{0, 0, 0, 0};
     }
-    __device__ __forceinline__ void load(const float* p, int transposed) {
+    // p: from the slice's first column (transposed: row) on, rows of W values
+    __device__ __forceinline__ void load(const float* p, int W, int transposed) {
         const int tid = threadIdx.x, g = (tid & 63) >> 4;
         if (transposed) {
 #pragma unroll
@@ -391,17 +392,17 @@ struct State {
 #pragma unroll
                 for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * VD + col(tid, cg)];
+                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * W + col(tid, cg)];
         }
     }
-    __device__ __forceinline__ void store(float* p) const {
+    __device__ __forceinline__ void store(float* p, int W) const {
         const int tid = threadIdx.x, g = (tid & 63) >> 4;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int cg = 0; cg < CG; ++cg)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * VD + col(tid, cg)] = s[kt][cg][r];
+                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * W + col(tid, cg)] = s[kt][cg][r];
     }
     __device__ __forceinline__ void scale(const Factor& f) {
         if (f.near_one) {
@@ -486,7 +487,7 @@ __device__ __forceinline__ void value_frags(const char* tile, int tid, typename 
 // q S and v are in registers, so only k has two tiles.
 // TERMS: bf16 terms of the decayed v that enters S
 template <typename T, int KD, int VD, int TERMS>
-__global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
+__global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs, int slices) {
     constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, WAVES = NT / 64, CG = VD / 64;
     constexpr bool BF = sizeof(T) == 2;
     constexpr int KB = C * KD * sizeof(T), PB = Scores<T>::BYTES;
@@ -500,7 +501,9 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
     __shared__ float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int id = xcd_order(blockIdx.x, gridDim.x);
+    int id = xcd_order(blockIdx.x, gridDim.x);
+    const int V = VD * slices, v0 = VD * (id % slices);   // o's row, this workgroup's first column
+    id /= slices;
     const LaJob& jb = jobs.job[id % jobs.n];
     const int h = (id / jobs.n) % um.H, seg_id = id / jobs.n / um.H;
     const Seg sg = find_seg(um, seg_id);
@@ -515,6 +518,7 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
     fq.init(jb.q, h, sg.start, sg.len, jb.rev, seg0);
     fk.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     fv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
+    fv.p += v0 * (int)sizeof(T);
     auto shift_of = [&](int c) { return c + 1 < nch ? 0 : last_shift; };
     if (nch > 0) {
         fk.load(kt2, shift_of(0), tid);
@@ -526,12 +530,12 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
     {
         const float* from = nullptr;
         if (jb.slots) {
-            from = jb.slots + ((int64_t)seg_id * um.H + h) * (KD * VD);
+            from = jb.slots + ((int64_t)seg_id * um.H + h) * (KD * V);
         } else if (jb.s_in) {
             const int page = page_of(jb.in_pages, sg.unit, um.n_pages);
-            if (page >= 0) from = jb.s_in + ((int64_t)page * um.H + h) * (KD * VD);
+            if (page >= 0) from = jb.s_in + ((int64_t)page * um.H + h) * (KD * V);
         }
-        if (from) st.load(from, jb.transposed);
+        if (from) st.load(from + v0 * (jb.transposed ? KD : 1), V, jb.transposed);
         else st.zero();
     }
     const double gd = um.decay[h];
@@ -557,9 +561,9 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
 
     // o: bytes from a row to the next, the lowest of the next 16 rows, the lane's part from there
     const int es = jb.o_f32 ? 4 : 2;
-    const int64_t orow = (jb.rev ? -1 : 1) * (int64_t)um.H * VD * es;
+    const int64_t orow = (jb.rev ? -1 : 1) * (int64_t)um.H * V * es;
     char* op = static_cast<char*>(jb.o) +
-               ((jb.rev ? sg.start + sg.len - seg0 - 16 : sg.start + seg0) * um.H + h) * (VD * es);
+               ((jb.rev ? sg.start + sg.len - seg0 - 16 : sg.start + seg0) * um.H + h) * (V * es) + v0 * es;
 
     for (int c = 0; c < nch; ++c) {
         const int shift = shift_of(c);
@@ -665,7 +669,7 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
                 }
         // a lane's rows of o^T: 4 CG consecutive values of row p of o
         const uint32_t o_at =
-            (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * VD * es) + CG * (16 * wave + 4 * g) * es;
+            (uint32_t)(jb.rev ? 15 - p : p) * (uint32_t)(um.H * V * es) + CG * (16 * wave + 4 * g) * es;
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
             char* to = op + (16 * it - shift) * orow + o_at;
@@ -698,7 +702,7 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs) {
 
     if (jb.s_out && sg.index == sg.count - 1) {
         const int page = page_of(jb.out_pages, sg.unit, um.n_pages);
-        if (page >= 0) st.store(jb.s_out + ((int64_t)page * um.H + h) * (KD * VD));
+        if (page >= 0) st.store(jb.s_out + ((int64_t)page * um.H + h) * (KD * V) + v0, V);
     }
 }
 
@@ -741,7 +745,7 @@ __global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
         st.scale(full);
         st.template add<TERMS>(kt + b * KB, t_, vf, wt);
     }
-    st.store(jb.slots + ((int64_t)(seg_id + 1) * um.H + h) * (KD * VD));
+    st.store(jb.slots + ((int64_t)(seg_id + 1) * um.H + h) * (KD * VD), VD);
 }
 
 // Slot s of a unit: from the contribution of segment s - 1 alone to the state
@@ -809,10 +813,17 @@ __global__ __launch_bounds__(NT) void la_group(const float* x, T* out, int64_t n
 template <typename T, int TERMS>
 hipError_t main_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    if (K == 128 && V == 128) la_main<T, 128, 128, TERMS><<<n, NT, 0, s>>>(u, j);
-    else if (K == 128) la_main<T, 128, 64, TERMS><<<n, NT, 0, s>>>(u, j);
-    else if (V == 128) la_main<T, 64, 128, TERMS><<<n, NT, 0, s>>>(u, j);
-    else la_main<T, 64, 64, TERMS><<<n, NT, 0, s>>>(u, j);
+    // With at most half a compute unit's share of workgroups, two of them take
+    // 64 value columns each (B=1 T=97 H=8 bf16: 15.1 to 11.9 us a call, T=512
+    // H=8: 25 to 23); beyond it that only repeats the scores (T=8192 H=32: 106
+    // to 120).
+    if (V == 128 && n <= 128) {
+        if (K == 128) la_main<T, 128, 64, TERMS><<<2 * n, NT, 0, s>>>(u, j, 2);
+        else la_main<T, 64, 64, TERMS><<<2 * n, NT, 0, s>>>(u, j, 2);
+    } else if (K == 128 && V == 128) la_main<T, 128, 128, TERMS><<<n, NT, 0, s>>>(u, j, 1);
+    else if (K == 128) la_main<T, 128, 64, TERMS><<<n, NT, 0, s>>>(u, j, 1);
+    else if (V == 128) la_main<T, 64, 128, TERMS><<<n, NT, 0, s>>>(u, j, 1);
+    else la_main<T, 64, 64, TERMS><<<n, NT, 0, s>>>(u, j, 1);
     return hipGetLastError();
 }
 
