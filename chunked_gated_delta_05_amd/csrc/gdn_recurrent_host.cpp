@@ -34,7 +34,7 @@ int64_t elem_bytes(int32_t d) { return d == GDN_DTYPE_BF16 ? 2 : 4; }
 bool strides_ok(const int64_t* s, int64_t rows, int64_t heads, int32_t dtype) {
     const int64_t lim = int64_t(1) << 60;
     for (int i = 0; i < 2; ++i) {
-        if (s[i] < 0 || s[i] * elem_bytes(dtype) % 16 != 0) return false;
+        if (s[i] < 0 || s[i] > lim || s[i] * elem_bytes(dtype) % 16 != 0) return false;
         const int64_t n = i == 0 ? rows : heads;
         if (n > 0 && s[i] > lim / n) return false;
     }

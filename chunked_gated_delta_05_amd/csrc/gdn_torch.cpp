@@ -85,6 +85,7 @@ struct Arguments {
     }
     // an output's dtype: given, else the given buffer's, else the inputs'
     ScalarType o_dtype(int i, const Tensor& out, ScalarType in) const {
+        dtype_code(in);
         ScalarType t = in;
         if (!none(i)) {
             if (!THPDtype_Check(a[i])) invalid("o_dtype must be a torch dtype");
@@ -151,8 +152,6 @@ void row_strides(const char* name, const Tensor& t, int64_t* out) {
 
 // q, k, v of one dtype and leading shape, with heads that divide H
 void check_qkv(const Tensor& q, const Tensor& k, const Tensor& v, int64_t H, const char* lead_text) {
-    if (k.scalar_type() != ScalarType::BFloat16 && k.scalar_type() != ScalarType::Float)
-        invalid("unsupported dtype " + dtype_text(k.scalar_type()));
     const int64_t d = k.dim();
     const std::pair<const char*, const Tensor*> all[] = {{"q", &q}, {"k", &k}, {"v", &v}};
     for (const auto& [name, t] : all) {
@@ -304,8 +303,8 @@ PyObject* linattn_bwd(const Arguments& a) {
                  dout = a.tensor(4, "dout"), offsets = a.tensor(6, "meta"), s_in = a.tensor(9, "initial_state"),
                  dht = a.tensor(10, "dht"), given = a.tensor(12, "workspace");
     if (!k.defined()) invalid("linear attention inputs must have shape [B,T,h,K] or [T,h,K]");
-    Prompt p = prompt(q, k, v, decay, offsets, a.integer(7), a.integer(8),
-                      k.scalar_type() == ScalarType::BFloat16 ? ScalarType::BFloat16 : ScalarType::Float);
+    dtype_code(k.scalar_type());
+    Prompt p = prompt(q, k, v, decay, offsets, a.integer(7), a.integer(8), k.scalar_type());
     p.d.scale = a.scale(5, p.d.K);
     if (!dout.defined()) invalid("dout is required");
     check_tensor("dout", dout, k.scalar_type(), p.tokens({p.d.H, p.d.V}));
