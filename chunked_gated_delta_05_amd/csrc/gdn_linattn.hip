@@ -197,12 +197,12 @@ __device__ __forceinline__ void tile_barrier() {
 }
 
 // One tensor's chunks on their way from memory to a tile. A wave's i-th copy
-// brings the rows ROWS (4 i + wave) .. of the tile, 64 / UNITS of them.
-template <typename T, int W, int C>
+// brings the rows ROWS (WAVES i + wave) .. of the tile, 64 / UNITS of them.
+template <typename T, int W, int C, int WAVES>
 struct Feeder {
     using TL = Tile<T, W>;
     static constexpr int ROWS = 64 / TL::UNITS;     // rows of a copy
-    static constexpr int N = C / (4 * ROWS);        // copies of a wave
+    static constexpr int N = C / (WAVES * ROWS);    // copies of a wave
     static_assert(N >= 1, "");
     const char* p;   // the next chunk's lowest token (wave-uniform)
     int64_t row;     // bytes from a tile row to the next (negative in reversed time)
@@ -223,15 +223,15 @@ struct Feeder {
         const char* q = p - shift * row;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int r = max(row0 + 4 * ROWS * i, shift);
-            const int u = unit ^ TL::swizzle(row0 + 4 * ROWS * i);
-            copy_to_lds(q, (uint32_t)(row < 0 ? C - 1 - r : r) * len + 16 * u, to + 4096 * i);
+            const int r = max(row0 + WAVES * ROWS * i, shift);
+            const int u = unit ^ TL::swizzle(row0 + WAVES * ROWS * i);
+            copy_to_lds(q, (uint32_t)(row < 0 ? C - 1 - r : r) * len + 16 * u, to + 1024 * WAVES * i);
         }
         p += C * row;
     }
     // clears the rows before `shift`
     __device__ static __forceinline__ void clear(char* tile, int shift, int tid) {
-        for (int i = tid; i < shift * TL::UNITS; i += NT) reinterpret_cast<u32x4*>(tile)[i] = u32x4{0, 0, 0, 0};
+        for (int i = tid; i < shift * TL::UNITS; i += 64 * WAVES) reinterpret_cast<u32x4*>(tile)[i] = u32x4{0, 0, 0, 0};
     }
 };
 
@@ -351,15 +351,14 @@ struct Scores {
 
 // ------------------------------------------------------------------ the state
 // A wave's part of S: CG groups of 16 value columns, KD / 16 tiles of 16 keys.
-// Two groups (V = 128) rather than eight waves of one: an operand read from
-// LDS then meets both; their columns alternate by fours, so that a lane's rows
-// of o^T in both are eight consecutive values of o.
+// The columns of two groups alternate by fours, so that a lane's rows of o^T in
+// both are eight consecutive values of o.
 // bf16: row m of tile 2 t + u is key 32 t + 8 (m / 4) + 4 u + m % 4, so that
 // tiles 2 t and 2 t + 1 hold, in each lane, the eight consecutive keys of an
 // operand; fp32: row m of tile t is key 16 t + m.
-template <typename T, int KD, int VD>
+template <typename T, int KD, int CG>
 struct State {
-    static constexpr int KT = KD / 16, CG = VD / 64;
+    static constexpr int KT = KD / 16;
     using frag = typename Shape<T>::frag;
     f32x4 s[KT][CG];
 
@@ -463,18 +462,18 @@ struct State {
 };
 
 // The wave's columns of v (State::col) as operands, two blocks of tokens.
-template <typename T, int KD, int VD>
-__device__ __forceinline__ void value_frags(const char* tile, int tid, typename Shape<T>::frag (*v)[VD / 64]) {
-    constexpr int CG = VD / 64;
+template <typename T, int VD, int CG>
+__device__ __forceinline__ void value_frags(const char* tile, int tid, typename Shape<T>::frag (*v)[CG]) {
+    using ST = State<T, 128, CG>;   // its columns, whatever the keys
 #pragma unroll
     for (int cg = 0; cg < CG; ++cg) {
         if constexpr (sizeof(T) == 2) {
             // the group of four that lane p % 4 names: the columns of rows 4 (p % 4) ..
-            const int at = across_lane<VD>(tid, State<T, KD, VD>::col((tid & ~15) | 4 * (tid & 3), cg));
+            const int at = across_lane<VD>(tid, ST::col((tid & ~15) | 4 * (tid & 3), cg));
 #pragma unroll
             for (int s = 0; s < 2; ++s) v[s][cg] = across_frag<VD>(tile, at, s, 0, 0);
         } else {
-            const int at = column_lane<VD>(tid, State<T, KD, VD>::col(tid, cg));
+            const int at = column_lane<VD>(tid, ST::col(tid, cg));
 #pragma unroll
             for (int s = 0; s < 2; ++s) v[s][cg] = column_frag<VD>(tile, at, s, 0);
         }
@@ -485,10 +484,14 @@ __device__ __forceinline__ void value_frags(const char* tile, int tid, typename 
 // Two workgroups a compute unit (77 KiB of LDS each for K = V = 128): the q
 // and v tiles are free for the next chunk once the scores are written and
 // q S and v are in registers, so only k has two tiles.
+// Four waves of two column groups rather than eight of one (V = 128): an
+// operand read from LDS then meets both groups (20 ragged prompts of 32768
+// tokens, 32 heads: 321 us against 387).
 // TERMS: bf16 terms of the decayed v that enters S
 template <typename T, int KD, int VD, int TERMS>
-__global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs, int slices) {
-    constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, WAVES = NT / 64, CG = VD / 64;
+__global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int slices) {
+    constexpr int WAVES = 4, NT = 64 * WAVES;
+    constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, CG = VD / (16 * WAVES);
     constexpr bool BF = sizeof(T) == 2;
     constexpr int KB = C * KD * sizeof(T), PB = Scores<T>::BYTES;
     using SC = Scores<T>;
@@ -513,8 +516,8 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs, int sl
     const int nch = seg1 > seg0 ? (seg1 - seg0 + C - 1) / C : 0;
     const int last_shift = nch * C - max(0, seg1 - seg0);   // tile rows before the last chunk's first
 
-    Feeder<T, KD, C> fq, fk;
-    Feeder<T, VD, C> fv;
+    Feeder<T, KD, C, WAVES> fq, fk;
+    Feeder<T, VD, C, WAVES> fv;
     fq.init(jb.q, h, sg.start, sg.len, jb.rev, seg0);
     fk.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     fv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs, int sl
         fv.load(vt, shift_of(0), tid);
     }
 
-    State<T, KD, VD> st;
+    State<T, KD, CG> st;
     {
         const float* from = nullptr;
         if (jb.slots) {
@@ -608,7 +611,7 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs, int sl
             }
         }
         frag vf[2][CG];
-        value_frags<T, KD, VD>(vt, t_, vf);
+        value_frags<T, VD, CG>(vt, t_, vf);
 
         // o^T = (q S)^T, rows scaled by their distance from the chunk's start
         f32x4 o[IT][CG];
@@ -707,10 +710,12 @@ __global__ __launch_bounds__(NT, 2) void la_main(LaUnits um, LaJobs jobs, int sl
 }
 
 // A segment's own contribution to the state after it, into the next slot of
-// its unit. The last segment of a unit has no next one.
-template <typename T, int KD, int VD, int TERMS>
-__global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
-    constexpr int C = Shape<T>::C, KB = C * KD * sizeof(T), VB = C * VD * sizeof(T);
+// its unit. The last segment of a unit has no next one. Here eight waves of
+// one group are ahead (B=1 T=2048 H=8 30 us against 32 in all): there is no
+// q S and no score to read operands for, and two waves a SIMD overlap.
+template <typename T, int KD, int VD, int TERMS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void la_summary(LaUnits um, LaJobs jobs) {
+    constexpr int C = Shape<T>::C, KB = C * KD * sizeof(T), VB = C * VD * sizeof(T), CG = VD / (16 * WAVES);
     __shared__ __attribute__((aligned(1024))) char kt[2 * KB];
     __shared__ __attribute__((aligned(1024))) char vt[2 * VB];
     __shared__ __attribute__((aligned(32))) float wt[C];
@@ -721,8 +726,8 @@ __global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
     const Seg sg = find_seg(um, seg_id);
     if (sg.unit < 0 || sg.index == sg.count - 1 || seg_id + 1 >= um.n_segs) return;
     const int seg0 = sg.index * um.seg_tokens, nch = um.seg_tokens / C;
-    Feeder<T, KD, C> fk;
-    Feeder<T, VD, C> fv;
+    Feeder<T, KD, C, WAVES> fk;
+    Feeder<T, VD, C, WAVES> fv;
     fk.init(jb.k, h, sg.start, sg.len, jb.rev, seg0);
     fv.init(jb.v, h, sg.start, sg.len, jb.rev, seg0);
     fk.load(kt, 0, tid);
@@ -730,7 +735,7 @@ __global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
     const double gd = um.decay[h];
     if (tid < C) wt[tid] = (float)(jb.s_w * dpow(gd, C - jb.e - tid));
     const Factor full(dpow(gd, C));
-    State<T, KD, VD> st;
+    State<T, KD, CG> st;
     st.zero();
     for (int c = 0; c < nch; ++c) {
         data_arrived<0>();
@@ -740,8 +745,8 @@ __global__ __launch_bounds__(NT, 2) void la_summary(LaUnits um, LaJobs jobs) {
             fk.load(kt + (b ^ 1) * KB, 0, t_);
             fv.load(vt + (b ^ 1) * VB, 0, t_);
         }
-        typename Shape<T>::frag vf[2][VD / 64];
-        value_frags<T, KD, VD>(vt + b * VB, t_, vf);
+        typename Shape<T>::frag vf[2][CG];
+        value_frags<T, VD, CG>(vt + b * VB, t_, vf);
         st.scale(full);
         st.template add<TERMS>(kt + b * KB, t_, vf, wt);
     }
@@ -817,23 +822,21 @@ hipError_t main_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s
     // 64 value columns each (B=1 T=97 H=8 bf16: 15.1 to 11.9 us a call, T=512
     // H=8: 25 to 23); beyond it that only repeats the scores (T=8192 H=32: 106
     // to 120).
-    if (V == 128 && n <= 128) {
-        if (K == 128) la_main<T, 128, 64, TERMS><<<2 * n, NT, 0, s>>>(u, j, 2);
-        else la_main<T, 64, 64, TERMS><<<2 * n, NT, 0, s>>>(u, j, 2);
-    } else if (K == 128 && V == 128) la_main<T, 128, 128, TERMS><<<n, NT, 0, s>>>(u, j, 1);
-    else if (K == 128) la_main<T, 128, 64, TERMS><<<n, NT, 0, s>>>(u, j, 1);
-    else if (V == 128) la_main<T, 64, 128, TERMS><<<n, NT, 0, s>>>(u, j, 1);
-    else la_main<T, 64, 64, TERMS><<<n, NT, 0, s>>>(u, j, 1);
+    const int slices = V == 128 && n <= 128 ? 2 : 1, VS = V / slices;
+    if (K == 128 && VS == 128) la_main<T, 128, 128, TERMS><<<n, 256, 0, s>>>(u, j, 1);
+    else if (K == 128) la_main<T, 128, 64, TERMS><<<n * slices, 256, 0, s>>>(u, j, slices);
+    else if (VS == 128) la_main<T, 64, 128, TERMS><<<n, 256, 0, s>>>(u, j, 1);
+    else la_main<T, 64, 64, TERMS><<<n * slices, 256, 0, s>>>(u, j, slices);
     return hipGetLastError();
 }
 
 template <typename T, int TERMS>
 hipError_t summary_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    if (K == 128 && V == 128) la_summary<T, 128, 128, TERMS><<<n, NT, 0, s>>>(u, j);
-    else if (K == 128) la_summary<T, 128, 64, TERMS><<<n, NT, 0, s>>>(u, j);
-    else if (V == 128) la_summary<T, 64, 128, TERMS><<<n, NT, 0, s>>>(u, j);
-    else la_summary<T, 64, 64, TERMS><<<n, NT, 0, s>>>(u, j);
+    if (K == 128 && V == 128) la_summary<T, 128, 128, TERMS, 8><<<n, 512, 0, s>>>(u, j);
+    else if (K == 128) la_summary<T, 128, 64, TERMS, 4><<<n, 256, 0, s>>>(u, j);
+    else if (V == 128) la_summary<T, 64, 128, TERMS, 8><<<n, 512, 0, s>>>(u, j);
+    else la_summary<T, 64, 64, TERMS, 4><<<n, 256, 0, s>>>(u, j);
     return hipGetLastError();
 }
 
