@@ -68,8 +68,18 @@ __device__ __forceinline__ int xcd_order(int b, int n) {
     return x * per + (x < rem ? x : rem) + i;
 }
 
+// The same for work that comes longest first: each XCD gets `each` neighbours
+// of every 8 `each` in turn, so that all of them take the long ones first.
+__device__ __forceinline__ int xcd_deal(int b, int n, int each) {
+    const int round = NXCD * each, whole = n / round * round;
+    if (b >= whole) return whole + xcd_order(b - whole, n - whole);
+    const int r = b % round;
+    return b - r + r % NXCD * each + r / NXCD;
+}
+
 struct Seg {
     int unit, index, count;   // the segment's place in its unit
+    int id;                   // its place among all, units in order
     int64_t start;            // the unit's first token
     int len;                  // the unit's tokens
 };
@@ -86,14 +96,21 @@ __device__ __forceinline__ void unit_range(const LaUnits& um, int u, int64_t& st
     len = (int)(b - a);
 }
 
-// The segment of a flat index: units in order, each with its segments. unit
-// is -1 beyond the last.
+// The segment that is id-th to be worked on; unit is -1 beyond the last.
+// Packed units are of any lengths, and the last workgroups to start decide
+// when a launch ends: of each 64 units first the segments of the full length,
+// then the rest of each unit by falling length, in sixteenths of a full one
+// (in order: 20 prompts of 32768 tokens and 32 heads 329 us, like this 285;
+// gradients of 12 documents, T=16384 H=16, 336 and 283; only where many short
+// ones fill the chip often over is it behind, T=32768 H=16 in 200 prompts 215
+// and 227: equal lengths at once store their states at once).
 __device__ Seg find_seg(const LaUnits& um, int id) {
     Seg s;
     if (um.dense) {
         s.count = segs_of(um.T, um.seg_tokens);
         s.unit = id / s.count;
         s.index = id - s.unit * s.count;
+        s.id = id;
         s.start = (int64_t)s.unit * um.T;
         s.len = um.T;
         if (s.unit >= um.n_units) s.unit = -1;
@@ -109,25 +126,42 @@ __device__ Seg find_seg(const LaUnits& um, int id) {
             unit_range(um, u0 + lane, start, len);
             ns = segs_of(len, um.seg_tokens);
         }
-        int inc = ns;
+        const int full = len / um.seg_tokens;
+        int inc = ns, finc = full;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
-            const int y = __shfl_up(inc, m);
-            if (lane >= m) inc += y;
+            const int y = __shfl_up(inc, m), z = __shfl_up(finc, m);
+            if (lane >= m) inc += y, finc += z;
         }
-        const uint64_t after = __ballot(id < base + inc);
-        if (after) {
-            const int at = __ffsll((unsigned long long)after) - 1;
-            s.unit = u0 + at;
-            s.count = __builtin_amdgcn_readfirstlane(__shfl(ns, at));
-            s.index = __builtin_amdgcn_readfirstlane(id - base - __shfl(inc - ns, at));
-            s.len = __builtin_amdgcn_readfirstlane(__shfl(len, at));
-            const uint32_t lo = __builtin_amdgcn_readfirstlane(__shfl((uint32_t)start, at));
-            const uint32_t hi = __builtin_amdgcn_readfirstlane(__shfl((uint32_t)(start >> 32), at));
+        const int total = __builtin_amdgcn_readlane(inc, 63), fulls = __builtin_amdgcn_readlane(finc, 63);
+        if (id < base + total) {
+            const int x = id - base;
+            uint64_t here;
+            if (x < fulls) {
+                here = __ballot(x < finc);
+            } else {
+                const int key = ns > full ? (int)((int64_t)(len - full * um.seg_tokens) * 16 / um.seg_tokens) : -1;
+                int before = fulls, k = 16;
+                uint64_t mask = 0;
+                do {
+                    before += __popcll(mask);
+                    mask = __ballot(key == --k);
+                } while (k > 0 && x >= before + __popcll(mask));
+                here = __ballot(key == k && x - before == (int)__popcll(mask & ((1ull << lane) - 1)));
+            }
+            const int at = __ffsll((unsigned long long)here) - 1;
+            s.count = __builtin_amdgcn_readlane(ns, at);
+            s.index = x < fulls ? x - __builtin_amdgcn_readlane(finc - full, at) : __builtin_amdgcn_readlane(full, at);
+            s.id = base + __builtin_amdgcn_readlane(inc - ns, at) + s.index;
+            // offsets that are not the host's end here rather than beyond the slots
+            if (s.id < um.n_segs) s.unit = u0 + at;
+            s.len = __builtin_amdgcn_readlane(len, at);
+            const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)start, at);
+            const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(start >> 32), at);
             s.start = (int64_t)(((uint64_t)hi << 32) | lo);
             return s;
         }
-        base += __shfl(inc, 63);
+        base += total;
     }
     return s;
 }
@@ -504,12 +538,13 @@ __global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int s
     __shared__ float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int id = xcd_order(blockIdx.x, gridDim.x);
+    int id = um.dense ? xcd_order(blockIdx.x, gridDim.x)
+                      : xcd_deal(blockIdx.x, gridDim.x, max(1, um.H * jobs.n * slices / NXCD));
     const int V = VD * slices, v0 = VD * (id % slices);   // o's row, this workgroup's first column
     id /= slices;
     const LaJob& jb = jobs.job[id % jobs.n];
-    const int h = (id / jobs.n) % um.H, seg_id = id / jobs.n / um.H;
-    const Seg sg = find_seg(um, seg_id);
+    const int h = (id / jobs.n) % um.H;
+    const Seg sg = find_seg(um, id / jobs.n / um.H);
     if (sg.unit < 0) return;
     const int seg0 = sg.index * um.seg_tokens;
     const int seg1 = min(sg.len, seg0 + um.seg_tokens);
@@ -533,7 +568,7 @@ __global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int s
     {
         const float* from = nullptr;
         if (jb.slots) {
-            from = jb.slots + ((int64_t)seg_id * um.H + h) * (KD * V);
+            from = jb.slots + ((int64_t)sg.id * um.H + h) * (KD * V);
         } else if (jb.s_in) {
             const int page = page_of(jb.in_pages, sg.unit, um.n_pages);
             if (page >= 0) from = jb.s_in + ((int64_t)page * um.H + h) * (KD * V);
@@ -720,11 +755,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void la_summary(LaUnits um, LaJobs j
     __shared__ __attribute__((aligned(1024))) char vt[2 * VB];
     __shared__ __attribute__((aligned(32))) float wt[C];
     const int tid = threadIdx.x;
-    const int id = xcd_order(blockIdx.x, gridDim.x);
+    const int id = um.dense ? xcd_order(blockIdx.x, gridDim.x)
+                            : xcd_deal(blockIdx.x, gridDim.x, max(1, um.H * jobs.n / NXCD));
     const LaJob& jb = jobs.job[id % jobs.n];
-    const int h = (id / jobs.n) % um.H, seg_id = id / jobs.n / um.H;
-    const Seg sg = find_seg(um, seg_id);
-    if (sg.unit < 0 || sg.index == sg.count - 1 || seg_id + 1 >= um.n_segs) return;
+    const int h = (id / jobs.n) % um.H;
+    const Seg sg = find_seg(um, id / jobs.n / um.H);
+    if (sg.unit < 0 || sg.index == sg.count - 1 || sg.id + 1 >= um.n_segs) return;
     const int seg0 = sg.index * um.seg_tokens, nch = um.seg_tokens / C;
     Feeder<T, KD, C, WAVES> fk;
     Feeder<T, VD, C, WAVES> fv;
@@ -750,7 +786,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void la_summary(LaUnits um, LaJobs j
         st.scale(full);
         st.template add<TERMS>(kt + b * KB, t_, vf, wt);
     }
-    st.store(jb.slots + ((int64_t)(seg_id + 1) * um.H + h) * (KD * VD), VD);
+    st.store(jb.slots + ((int64_t)(sg.id + 1) * um.H + h) * (KD * VD), VD);
 }
 
 // Slot s of a unit: from the contribution of segment s - 1 alone to the state

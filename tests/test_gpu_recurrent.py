@@ -100,6 +100,32 @@ def test_linattn_forward_without_states_and_with_fp32_output(dtype):
     within(o, ref.linattn(*args)[0], ref.linattn(*args, absolute=True)[0], 2.0 ** -14, o.dtype, "o")
 
 
+@pytest.mark.parametrize("lens", [
+    [2, 1, 64, 128, 129, 300, 63, 65] * 17,                      # 136 sequences, three groups of 64
+    [5] * 64 + [1] * 65,                                         # groups without a full segment
+    [1000] + [3] * 63 + [400, 256, 1, 255] + [128] * 40,         # the long ones at a group's ends
+])
+def test_linattn_many_sequences(lens):
+    # whatever order they are worked on in, each sequence gets its own result
+    case = ("", lens, True, 2, 2, 1, 2)
+    x = prompt(case, "bf16", 64, 64, "spread")
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], x["scale"], meta=x["meta"],
+                                initial_state=x["S0"], output_final_state=True)
+    args = (x["q"], x["k"], x["v"], x["decay"], x["scale"], x["offs"], x["S0"])
+    want, wfin = ref.linattn(*args)
+    A, Afin = ref.linattn(*args, absolute=True)
+    within(o, want, A, 2.0 ** -14, o.dtype, "o")
+    within(fin, wfin, Afin, 2.0 ** -17, fin.dtype, "final state")
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], meta=x["meta"],
+                           initial_state=x["S0"], dht=x["dht"])
+    args += (x["dout"], x["dht"])
+    want, A = ref.linattn_grads(*args), ref.linattn_grads(*args, absolute=True)
+    for i, (n, t) in enumerate((("dq", "q"), ("dk", "k"), ("dv", "v"))):
+        h = x[t].shape[-2]
+        within(r[n], ref.shared(want[i], h), ref.shared(A[i], h), 2.0 ** -14, r[n].dtype, n)
+    within(r["dh0"], want[3], A[3], 2.0 ** -17, torch.float32, "dh0")
+
+
 def test_linattn_no_tokens():
     q = torch.empty(2, 0, 3, 128, dtype=torch.bfloat16, device=DEV)
     S0 = torch.randn(2, 3, 128, 128, device=DEV)
