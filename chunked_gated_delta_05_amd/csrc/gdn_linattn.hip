@@ -521,31 +521,33 @@ __device__ __forceinline__ void value_frags(const char* tile, int tid, typename 
 // Four waves of two column groups rather than eight of one (V = 128): an
 // operand read from LDS then meets both groups (20 ragged prompts of 32768
 // tokens, 32 heads: 321 us against 387).
+template <typename T, int KD, int VD>
+struct Tiles {
+    static constexpr int C = Shape<T>::C, KB = C * KD * sizeof(T), VB = C * VD * sizeof(T);
+    static constexpr int PB = (sizeof(T) == 2 ? 2 : 1) * Scores<T>::BYTES;
+    alignas(1024) char qt[KB];
+    char kt2[2 * KB];
+    char vt[VB];
+    char pt[PB];
+    alignas(32) float wt[C];
+    float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
+};
+
+// V: o's row, v0: this workgroup's first column of it
 // TERMS: bf16 terms of the decayed v that enters S
 template <typename T, int KD, int VD, int TERMS>
-__global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int slices) {
+__device__ __forceinline__ void walk(const LaUnits& um, const LaJob& jb, const Seg& sg, int h, int V, int v0,
+                                     Tiles<T, KD, VD>& tiles) {
     constexpr int WAVES = 4, NT = 64 * WAVES;
     constexpr int C = Shape<T>::C, KS = Shape<T>::KS, IT = C / 16, CG = VD / (16 * WAVES);
     constexpr bool BF = sizeof(T) == 2;
     constexpr int KB = C * KD * sizeof(T), PB = Scores<T>::BYTES;
     using SC = Scores<T>;
     using frag = typename Shape<T>::frag;
-    __shared__ __attribute__((aligned(1024))) char qt[KB];
-    __shared__ __attribute__((aligned(1024))) char kt2[2 * KB];
-    __shared__ __attribute__((aligned(1024))) char vt[C * VD * sizeof(T)];
-    __shared__ __attribute__((aligned(1024))) char pt[(BF ? 2 : 1) * PB];
-    __shared__ __attribute__((aligned(32))) float wt[C];
-    __shared__ float pw[2 * C], rf[2][C];   // rf[1]: of a partial last chunk
-
+    char *const qt = tiles.qt, *const kt2 = tiles.kt2, *const vt = tiles.vt, *const pt = tiles.pt;
+    float *const wt = tiles.wt, *const pw = tiles.pw;
+    float (*const rf)[C] = tiles.rf;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int id = um.dense ? xcd_order(blockIdx.x, gridDim.x)
-                      : xcd_deal(blockIdx.x, gridDim.x, max(1, um.H * jobs.n * slices / NXCD));
-    const int V = VD * slices, v0 = VD * (id % slices);   // o's row, this workgroup's first column
-    id /= slices;
-    const LaJob& jb = jobs.job[id % jobs.n];
-    const int h = (id / jobs.n) % um.H;
-    const Seg sg = find_seg(um, id / jobs.n / um.H);
-    if (sg.unit < 0) return;
     const int seg0 = sg.index * um.seg_tokens;
     const int seg1 = min(sg.len, seg0 + um.seg_tokens);
     const int nch = seg1 > seg0 ? (seg1 - seg0 + C - 1) / C : 0;
@@ -744,6 +746,47 @@ __global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int s
     }
 }
 
+// Three terms (24 bits) for a segment whose state is returned, two elsewhere.
+template <typename T, int KD, int VD, bool STATES>
+__device__ __forceinline__ void walk_job(const LaUnits& um, const LaJob& jb, const Seg& sg, int h, int V, int v0,
+                                         Tiles<T, KD, VD>& tiles) {
+    if constexpr (sizeof(T) == 4) walk<T, KD, VD, 1>(um, jb, sg, h, V, v0, tiles);
+    else if (STATES && jb.s_out && sg.index == sg.count - 1) walk<T, KD, VD, 3>(um, jb, sg, h, V, v0, tiles);
+    else walk<T, KD, VD, 2>(um, jb, sg, h, V, v0, tiles);
+}
+
+template <typename T, int KD, int VD, bool STATES>
+__global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int slices) {
+    __shared__ Tiles<T, KD, VD> tiles;
+    int id = um.dense ? xcd_order(blockIdx.x, gridDim.x)
+                      : xcd_deal(blockIdx.x, gridDim.x, max(1, um.H * jobs.n * slices / NXCD));
+    const int slice = id % slices;
+    id /= slices;
+    const LaJob& jb = jobs.job[id % jobs.n];
+    const Seg sg = find_seg(um, id / jobs.n / um.H);
+    if (sg.unit < 0) return;
+    walk_job<T, KD, VD, STATES>(um, jb, sg, (id / jobs.n) % um.H, VD * slices, VD * slice, tiles);
+}
+
+// Jobs of both K = 64, V = 128 and K = 128, V = 64: the gradients where q and
+// v differ in width. One launch, since either alone leaves room (fp32, T=3001
+// in 7 documents, H=8).
+template <typename T, bool STATES>
+__global__ __launch_bounds__(256, 2) void la_main_mixed(LaUnits um, LaJobs jobs) {
+    __shared__ union {
+        Tiles<T, 64, 128> a;
+        Tiles<T, 128, 64> b;
+    } tiles;
+    const int id = um.dense ? xcd_order(blockIdx.x, gridDim.x)
+                            : xcd_deal(blockIdx.x, gridDim.x, max(1, um.H * jobs.n / NXCD));
+    const LaJob& jb = jobs.job[id % jobs.n];
+    const int h = (id / jobs.n) % um.H;
+    const Seg sg = find_seg(um, id / jobs.n / um.H);
+    if (sg.unit < 0) return;
+    if (jb.K == 64) walk_job<T, 64, 128, STATES>(um, jb, sg, h, 128, 0, tiles.a);
+    else walk_job<T, 128, 64, STATES>(um, jb, sg, h, 64, 0, tiles.b);
+}
+
 // A segment's own contribution to the state after it, into the next slot of
 // its unit. The last segment of a unit has no next one. Here eight waves of
 // one group are ahead (B=1 T=2048 H=8 30 us against 32 in all): there is no
@@ -851,18 +894,24 @@ __global__ __launch_bounds__(NT) void la_group(const float* x, T* out, int64_t n
     put4(out + 4 * i, s);
 }
 
-template <typename T, int TERMS>
-hipError_t main_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
+template <typename T, bool STATES>
+hipError_t main_t(const LaUnits& u, const LaJobs& j, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
+    const int K = j.job[0].K, V = j.job[0].V;
+    for (int i = 1; i < j.n; ++i)
+        if (j.job[i].K != K) {
+            la_main_mixed<T, STATES><<<n, 256, 0, s>>>(u, j);
+            return hipGetLastError();
+        }
     // With at most half a compute unit's share of workgroups, two of them take
     // 64 value columns each (B=1 T=97 H=8 bf16: 15.1 to 11.9 us a call, T=512
     // H=8: 25 to 23); beyond it that only repeats the scores (T=8192 H=32: 106
     // to 120).
     const int slices = V == 128 && n <= 128 ? 2 : 1, VS = V / slices;
-    if (K == 128 && VS == 128) la_main<T, 128, 128, TERMS><<<n, 256, 0, s>>>(u, j, 1);
-    else if (K == 128) la_main<T, 128, 64, TERMS><<<n * slices, 256, 0, s>>>(u, j, slices);
-    else if (VS == 128) la_main<T, 64, 128, TERMS><<<n, 256, 0, s>>>(u, j, 1);
-    else la_main<T, 64, 64, TERMS><<<n * slices, 256, 0, s>>>(u, j, slices);
+    if (K == 128 && VS == 128) la_main<T, 128, 128, STATES><<<n, 256, 0, s>>>(u, j, 1);
+    else if (K == 128) la_main<T, 128, 64, STATES><<<n * slices, 256, 0, s>>>(u, j, slices);
+    else if (VS == 128) la_main<T, 64, 128, STATES><<<n, 256, 0, s>>>(u, j, 1);
+    else la_main<T, 64, 64, STATES><<<n * slices, 256, 0, s>>>(u, j, slices);
     return hipGetLastError();
 }
 
@@ -885,9 +934,9 @@ bool returns_state(const LaJobs& j) {
 
 }  // namespace
 
-hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s) {
-    if (dtype == GDN_DTYPE_F32) return main_t<float, 1>(u, j, K, V, s);
-    return returns_state(j) ? main_t<bf16, 3>(u, j, K, V, s) : main_t<bf16, 2>(u, j, K, V, s);
+hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, hipStream_t s) {
+    if (dtype == GDN_DTYPE_F32) return main_t<float, false>(u, j, s);
+    return returns_state(j) ? main_t<bf16, true>(u, j, s) : main_t<bf16, false>(u, j, s);
 }
 
 hipError_t launch_la_summary(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s) {
