@@ -48,7 +48,8 @@ struct Prompt {
     bool cut;      // some sequence has more than one segment
 };
 
-gdn_status check_prompt(const gdn_linattn_desc* d, Prompt* p) {
+// walks: of every sequence, in one launch
+gdn_status check_prompt(const gdn_linattn_desc* d, int walks, Prompt* p) {
     if (d == nullptr) return GDN_ERR_INVALID;
     if (!width_ok(d->K) || !width_ok(d->V)) return GDN_ERR_UNSUPPORTED;
     if (d->B < 1 || d->T < 0 || d->H < 1 || d->Hq < 1 || d->Hk < 1 || d->Hv < 1) return GDN_ERR_INVALID;
@@ -89,17 +90,34 @@ gdn_status check_prompt(const gdn_linattn_desc* d, Prompt* p) {
         u.n_units = d->n_units;
         u.offsets = d->offsets_dev;
     }
-    // Segments: as long as 256 workgroups' even share of the heads' chunks.
-    // Shorter ones give each compute unit its second workgroup but cost more
-    // states between them (B=4 T=4096 H=16 bf16: 114 us at 256 and at 512;
-    // its gradients 233 and 256 us; 20 packed documents, T=32768 H=32, which
-    // 512 cuts and 256 does not: 323 and 455 us). At least two chunks, or one
-    // where a chunk's products take fp32 MFMA's time (B=1 T=2048 H=8 at 1, 2
-    // and 4 chunks: bf16 40, 34 and 38 us, fp32 47, 55 and 85 us).
-    int64_t seg = (p->chunks * d->H + 255) / 256;
+    // Segments, in chunks. A workgroup alone on its compute unit walks nearly
+    // as fast as two together, and every cut costs states between the parts.
+    // Rows of one length: as many equal parts as 256 workgroups have room for
+    // (B=4 T=4096 H=16 bf16: 114 us at 256 and 111 at 512; T=4096 H=16 45 and
+    // 52, its gradients 81 and 100; fp32 T=1000 H=32 60 and 66; T=3000, B=3
+    // H=16, 288 workgroups 94 and 240 of them 78).
+    // Packed sequences run longest first, and the work of all walks of a launch
+    // levels itself unless one sequence is longer than about a compute unit's
+    // share: then none is cut (20 prompts, T=32768 H=16, longest 1.35 shares:
+    // 204 us whole, 229 and 219 with 256 and 512 parts; gradients of 12
+    // documents, T=16384 H=16, 0.84: 222, 266 and 272). Beyond that parts of
+    // half a share, which fill both places of a unit (5 prompts, T=32768 H=16:
+    // 213, in parts of a share 225; 3 prompts, T=9000 H=32: 116 and 126; 12,
+    // T=4096 H=8: 43 and 40; fp32 gradients of 7 documents, T=3001 H=8: 105,
+    // at a third of a share 116).
+    // At least two chunks, or one where a chunk's products take fp32 MFMA's
+    // time (B=1 T=2048 H=8 at 1, 2 and 4 chunks: bf16 40, 34 and 38 us, fp32
+    // 47, 55 and 85 us).
+    const int64_t longest = (p->longest + kChunk - 1) / kChunk, work = p->chunks * d->H * walks;
     const int64_t least = d->dtype == GDN_DTYPE_F32 ? 1 : 2;
+    int64_t seg = longest;
+    if (u.dense) {
+        const int64_t parts = 256 / (int64_t(u.n_units) * d->H);
+        if (parts > 1) seg = (longest + parts - 1) / parts;
+    } else if (longest * 256 * 5 > work * 7) {
+        seg = (work + 511) / 512;
+    }
     if (seg < least) seg = least;
-    if (seg > p->longest / kChunk + 1) seg = p->longest / kChunk + 1;
     u.seg_tokens = (int32_t)(seg * kChunk);
     int64_t n = 0;
     for (int32_t i = 0; i < u.n_units; ++i) {
@@ -148,7 +166,7 @@ extern "C" gdn_status gdn_linattn_fwd(const gdn_linattn_desc* d, const void* q, 
                                       const int32_t* out_pages, int32_t n_pages, void* o, void* workspace,
                                       size_t* workspace_bytes, hipStream_t stream) {
     Prompt p;
-    gdn_status st = check_prompt(d, &p);
+    gdn_status st = check_prompt(d, 1, &p);
     if (st != GDN_OK) return st;
     bool query = false;
     st = check_workspace(slot_bytes(p, d), workspace, workspace_bytes, &query);
@@ -190,7 +208,7 @@ extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, 
                                       void* dq, void* dk, void* dv, float* dh0, void* workspace,
                                       size_t* workspace_bytes, hipStream_t stream) {
     Prompt p;
-    gdn_status st = check_prompt(d, &p);
+    gdn_status st = check_prompt(d, 3, &p);
     if (st != GDN_OK) return st;
     // slots of S and of its gradient, then the per-head gradients of shared heads
     const int64_t slots = slot_bytes(p, d);
