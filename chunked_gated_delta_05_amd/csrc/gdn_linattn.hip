@@ -905,10 +905,9 @@ __global__ __launch_bounds__(NT) void la_group(const float* x, T* out, int64_t n
 }
 
 template <typename T, bool STATES>
-hipError_t main_t(const LaUnits& u, const LaJobs& j, hipStream_t s) {
+hipError_t main_t(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s) {
     const unsigned n = (unsigned)((int64_t)u.n_segs * u.H * j.n);
-    const int K = j.job[0].K, V = j.job[0].V;
-    for (int i = 1; i < j.n; ++i)
+    for (int i = 0; i < j.n; ++i)
         if (j.job[i].K != K) {
             la_main_mixed<T, STATES><<<n, 256, 0, s>>>(u, j);
             return hipGetLastError();
@@ -944,9 +943,9 @@ bool returns_state(const LaJobs& j) {
 
 }  // namespace
 
-hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, hipStream_t s) {
-    if (dtype == GDN_DTYPE_F32) return main_t<float, false>(u, j, s);
-    return returns_state(j) ? main_t<bf16, true>(u, j, s) : main_t<bf16, false>(u, j, s);
+hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s) {
+    if (dtype == GDN_DTYPE_F32) return main_t<float, false>(u, j, K, V, s);
+    return returns_state(j) ? main_t<bf16, true>(u, j, K, V, s) : main_t<bf16, false>(u, j, K, V, s);
 }
 
 hipError_t launch_la_summary(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s) {

@@ -189,7 +189,6 @@ extern "C" gdn_status gdn_linattn_fwd(const gdn_linattn_desc* d, const void* q, 
     j.s_out = s_out;
     j.out_pages = out_pages;
     j.K = d->K;
-    j.V = d->V;
     j.e = 1;
     j.o_f32 = d->o_dtype == GDN_DTYPE_F32;
     j.o = o;
@@ -200,7 +199,7 @@ extern "C" gdn_status gdn_linattn_fwd(const gdn_linattn_desc* d, const void* q, 
         if (gdn::launch_la_summary(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
         if (gdn::launch_la_merge(p.u, jobs, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
     }
-    return run(gdn::launch_la_main(p.u, jobs, d->dtype, stream));
+    return run(gdn::launch_la_main(p.u, jobs, d->dtype, d->K, d->V, stream));
 }
 
 extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, const void* k, const void* v,
@@ -293,13 +292,13 @@ extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, 
         if (gdn::launch_la_summary(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
         if (gdn::launch_la_merge(p.u, jobs, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
     }
-    jq.K = jk.K = jv.V = d->V;
-    jq.V = jk.V = jv.K = d->K;
+    jq.K = jk.K = d->V;
+    jv.K = d->K;
     jobs.job[0] = jq;
     jobs.job[1] = jk;
     jobs.job[2] = jv;
     jobs.n = 3;
-    if (gdn::launch_la_main(p.u, jobs, d->dtype, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    if (gdn::launch_la_main(p.u, jobs, d->dtype, d->V, d->K, stream) != hipSuccess) return GDN_ERR_DEVICE;
     if (pq && gdn::launch_la_group(pq, dq, p.tokens, d->H, d->Hq, d->K, d->dtype, stream) != hipSuccess)
         return GDN_ERR_DEVICE;
     if (pk && gdn::launch_la_group(pk, dk, p.tokens, d->H, d->Hk, d->K, d->dtype, stream) != hipSuccess)

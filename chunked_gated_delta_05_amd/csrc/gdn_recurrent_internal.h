@@ -50,7 +50,7 @@ struct LaJob {
     float* s_out;              // states after the units, by unit or by out_pages; or NULL
     const int32_t* out_pages;
     float* slots;              // [n_segs][H]: the states entering the segments, or NULL
-    int32_t K, V;              // the walk's widths: of q and k, of v and o
+    int32_t K;                 // width of its q and k
     int32_t transposed;        // s_in and slots are read as V x K
     int32_t rev, e, o_f32;
     void* o;                   // [tokens][H][V]
@@ -65,8 +65,8 @@ struct LaJobs {
 hipError_t launch_la_summary(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s);
 // the slots' running states, from s_in
 hipError_t launch_la_merge(const LaUnits& u, const LaJobs& j, int K, int V, hipStream_t s);
-// jobs of one K and V, or of (64, 128) and (128, 64)
-hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, hipStream_t s);
+// K, V: of every job, or of some where the others have them exchanged
+hipError_t launch_la_main(const LaUnits& u, const LaJobs& j, int dtype, int K, int V, hipStream_t s);
 // out [tokens][h][D] = sums of the H / h heads of x [tokens][H][D] that share one
 hipError_t launch_la_group(const float* x, void* out, int64_t tokens, int H, int h, int D, int dtype, hipStream_t s);
 
