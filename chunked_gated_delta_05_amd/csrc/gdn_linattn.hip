@@ -80,8 +80,9 @@ __device__ __forceinline__ int xcd_deal(int b, int n, int each) {
 // The work of this workgroup. Where packed segments give some compute units a
 // second workgroup, which is dealt to them in the order of the first, the
 // longest ones come last of the first, so that they stay alone and the second
-// ones meet the shorter ones: one workgroup alone is as fast as two together
-// (3.2 us a chunk of K = V = 128 against 6.9 each).
+// ones meet the shorter ones: a chunk of K = V = 128 takes a workgroup alone
+// 4.6 us (3.1 with a quarter of the chip at work), one of two 6.9 (T=32768
+// H=16 in 20 prompts: longest first throughout 218 us, like this 204).
 __device__ __forceinline__ int work_of_block(const LaUnits& um, int each) {
     int b = blockIdx.x;
     const int n = gridDim.x;
@@ -528,6 +529,16 @@ __device__ __forceinline__ void value_frags(const char* tile, int tid, typename 
 }
 
 // ------------------------------------------------------------------ kernels
+// The walk: 4 KV + 2 C (K + V) flops a token and head, of which q S and the
+// update of S run on two or three bf16 terms, so a chunk of K = V = 128 is 164
+// to 196 MFMA of 16 cycles a wave next to about 800 vector instructions that
+// split, scale and store. With full-length work on all units memory bounds it
+// (B=16 T=4096 H=32: 485 us, 4.4 TB/s), with less the latency of one chunk's
+// chain - scores, S's two terms, q S, P v, k v^T - which two workgroups a unit
+// overlap: B=4 T=4096 H=16 78 us of 113 (the rest is the segments' states),
+// 20 prompts of 32768 tokens and 32 heads 277 us, 2.7 TB/s. fp32 MFMA bounds
+// fp32 (T=4096 H=16: 93 us). Eight waves a workgroup, deeper double buffers,
+// fewer address instructions and other orders of the products gain nothing.
 // Two workgroups a compute unit (77 KiB of LDS each for K = V = 128): the q
 // and v tiles are free for the next chunk once the scores are written and
 // q S and v are in registers, so only k has two tiles.
@@ -782,7 +793,7 @@ __global__ __launch_bounds__(256, 2) void la_main(LaUnits um, LaJobs jobs, int s
 
 // Jobs of both K = 64, V = 128 and K = 128, V = 64: the gradients where q and
 // v differ in width. One launch, since either alone leaves room (fp32, T=3001
-// in 7 documents, H=8).
+// in 7 documents, H=8, K=128 V=64: 35.7 + 23.6 us apart, 54.7 together).
 template <typename T, bool STATES>
 __global__ __launch_bounds__(256, 2) void la_main_mixed(LaUnits um, LaJobs jobs) {
     __shared__ union {
@@ -801,7 +812,9 @@ __global__ __launch_bounds__(256, 2) void la_main_mixed(LaUnits um, LaJobs jobs)
 // A segment's own contribution to the state after it, into the next slot of
 // its unit. The last segment of a unit has no next one. Here eight waves of
 // one group are ahead (B=1 T=2048 H=8 30 us against 32 in all): there is no
-// q S and no score to read operands for, and two waves a SIMD overlap.
+// q S and no score to read operands for, and two waves a SIMD overlap. Of B=4
+// T=4096 H=16 29 us: three quarters of k and v read once more (100 MB, 3.4
+// TB/s), the rest the first chunk's latency and the states' stores.
 template <typename T, int KD, int VD, int TERMS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void la_summary(LaUnits um, LaJobs jobs) {
     constexpr int C = Shape<T>::C, KB = C * KD * sizeof(T), VB = C * VD * sizeof(T), CG = VD / (16 * WAVES);
@@ -843,7 +856,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void la_summary(LaUnits um, LaJobs j
 }
 
 // Slot s of a unit: from the contribution of segment s - 1 alone to the state
-// entering segment s.
+// entering segment s. Memory bounds it (256 segments and heads, 17 MB read and
+// written, from the caches: 6.5 us).
 __global__ __launch_bounds__(NT) void la_merge(LaUnits um, LaJobs jobs, int kv) {
     const LaJob& jb = jobs.job[blockIdx.y];
     const int blocks = kv / (4 * NT);
@@ -891,7 +905,9 @@ __device__ __forceinline__ void put4(bf16* o, f32x4 x) {
     *reinterpret_cast<bf16x4*>(o) = __builtin_convertvector(x, bf16x4);
 }
 
-// Sums of the heads that share one, in head order; four values a thread.
+// Sums of the heads that share one, in head order; four values a thread: no
+// atomics, so the result is the same on every run. Memory bounds it (T=3001,
+// 8 heads to 2, 128 wide, from the caches: 5 us).
 template <typename T>
 __global__ __launch_bounds__(NT) void la_group(const float* x, T* out, int64_t n4, int group, int D4) {
     const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
