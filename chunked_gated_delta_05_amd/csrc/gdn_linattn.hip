@@ -410,10 +410,10 @@ struct State {
     using frag = typename Shape<T>::frag;
     f32x4 s[KT][CG];
 
-    __device__ static __forceinline__ int key0(int kt, int g) {   // of the lane's four rows
-        if constexpr (sizeof(T) == 2) return 32 * (kt >> 1) + 8 * g + 4 * (kt & 1);
-        return 16 * kt + 4 * g;
-    }
+    // the first of the lane's four rows: a part of the tile, a part of the lane
+    __device__ static constexpr int key0(int kt) { return sizeof(T) == 2 ? 32 * (kt >> 1) + 4 * (kt & 1) : 16 * kt; }
+    __device__ static __forceinline__ int lane_key(int g) { return sizeof(T) == 2 ? 8 * g : 4 * g; }
+    static constexpr int COL_STEP = CG == 2 ? 4 : 0;   // from a group's column to the next group's
     __device__ static __forceinline__ int col(int tid, int cg) {
         const int p = tid & 15, w = tid >> 6;
         return CG == 2 ? 32 * w + 8 * (p >> 2) + 4 * cg + (p & 3) : 16 * w + p;
@@ -424,32 +424,47 @@ struct State {
 #pragma unroll
             for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f32x4{0, 0, 0, 0};
     }
-    // p: from the slice's first column (transposed: row) on, rows of W values
+    // p: from the slice's first column (transposed: row) on, rows of W values.
+    // A lane's part of the address is 32 bits, the rest the same in all lanes.
     __device__ __forceinline__ void load(const float* p, int W, int transposed) {
-        const int tid = threadIdx.x, g = (tid & 63) >> 4;
+        const int tid = threadIdx.x, key = lane_key((tid & 63) >> 4), c = col(tid, 0);
+        const char* q = reinterpret_cast<const char*>(p);
+        const uint32_t lane = 4 * (transposed ? c * KD + key : key * W + c);
         if (transposed) {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int cg = 0; cg < CG; ++cg)
-                    s[kt][cg] = *reinterpret_cast<const f32x4*>(p + col(tid, cg) * KD + key0(kt, g));
+                    s[kt][cg] = *reinterpret_cast<const f32x4*>(q + 4 * (cg * COL_STEP * KD + key0(kt)) + lane);
         } else {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int cg = 0; cg < CG; ++cg)
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) s[kt][cg][r] = p[(key0(kt, g) + r) * W + col(tid, cg)];
+                    for (int cg = 0; cg < CG; ++cg)
+                        s[kt][cg][r] =
+                            *reinterpret_cast<const float*>(q + 4 * ((key0(kt) + r) * W + cg * COL_STEP) + lane);
         }
     }
-    __device__ __forceinline__ void store(float* p, int W) const {
-        const int tid = threadIdx.x, g = (tid & 63) >> 4;
+    // S <- f S + x
+    __device__ __forceinline__ void join(const Factor& f, const State& x) {
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int cg = 0; cg < CG; ++cg)
+            for (int cg = 0; cg < CG; ++cg) s[kt][cg] = f * s[kt][cg] + x.s[kt][cg];
+    }
+    __device__ __forceinline__ void store(float* p, int W) const {
+        const int tid = threadIdx.x, key = lane_key((tid & 63) >> 4), c = col(tid, 0);
+        char* q = reinterpret_cast<char*>(p);
+        const uint32_t lane = 4 * (key * W + c);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[(key0(kt, g) + r) * W + col(tid, cg)] = s[kt][cg][r];
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int cg = 0; cg < CG; ++cg)
+                    *reinterpret_cast<float*>(q + 4 * ((key0(kt) + r) * W + cg * COL_STEP) + lane) = s[kt][cg][r];
     }
     __device__ __forceinline__ void scale(const Factor& f) {
         if (f.near_one) {
@@ -590,19 +605,30 @@ __device__ __forceinline__ void walk(const LaUnits& um, const LaJob& jb, const S
         fv.load(vt, shift_of(0), tid);
     }
 
+    const double gd = um.decay[h];
     State<T, KD, CG> st;
     {
-        const float* from = nullptr;
-        if (jb.slots) {
-            from = jb.slots + ((int64_t)sg.id * um.H + h) * (KD * V);
-        } else if (jb.s_in) {
+        const int at = v0 * (jb.transposed ? KD : 1);
+        const float* slot = jb.slots ? jb.slots + ((int64_t)sg.id * um.H + h) * (KD * V) + at : nullptr;
+        const float* from = slot;
+        if (jb.s_in && (!slot || um.join)) {
             const int page = page_of(jb.in_pages, sg.unit, um.n_pages);
-            if (page >= 0) from = jb.s_in + ((int64_t)page * um.H + h) * (KD * V);
+            from = page >= 0 ? jb.s_in + ((int64_t)page * um.H + h) * (KD * V) + at : nullptr;
+        } else if (um.join) {
+            from = nullptr;
         }
-        if (from) st.load(from + v0 * (jb.transposed ? KD : 1), V, jb.transposed);
+        if (from) st.load(from, V, jb.transposed);
         else st.zero();
+        if (slot && um.join) {   // the segments before: each its own contribution
+            const Factor f(dpow(gd, um.seg_tokens));
+            const int64_t pitch = (int64_t)um.H * (KD * V);
+            for (int i = sg.index - 1; i >= 0; --i) {
+                State<T, KD, CG> x;
+                x.load(slot - i * pitch, V, jb.transposed);
+                st.join(f, x);
+            }
+        }
     }
-    const double gd = um.decay[h];
     if (tid < 4 * C) {   // four tables of C powers
         const int i = tid % C, table = tid / C;
         const int n = table == 0 ? i : table == 1 ? C - jb.e - i : table == 2 ? i + jb.e : i - last_shift + jb.e;

@@ -34,6 +34,7 @@ struct LaUnits {
     const int32_t* offsets;   // packed: device [n_units + 1]
     int32_t seg_tokens;       // a multiple of 64
     int32_t n_segs;           // over all units
+    int32_t join;             // the walk adds the slots up itself, no merge
     int32_t n_pages;
     const float* decay;       // [H]
 };

@@ -126,6 +126,29 @@ def test_linattn_many_sequences(lens):
     within(r["dh0"], want[3], A[3], 2.0 ** -17, torch.float32, "dh0")
 
 
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,packed", [([250, 250], False), ([256, 70, 1, 190], True), ([129], False)])
+def test_linattn_few_segments(lens, packed, dtype, K, V):
+    # two to four parts of a sequence: the walk adds up the parts before its own
+    x = prompt(("", lens, packed, 2, 2, 1, 2), dtype, K, V, "mixed", seed=2)
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], x["scale"], meta=x["meta"],
+                                initial_state=x["S0"], output_final_state=True)
+    args = (x["q"], x["k"], x["v"], x["decay"], x["scale"], x["offs"], x["S0"])
+    want, wfin = ref.linattn(*args)
+    A, Afin = ref.linattn(*args, absolute=True)
+    within(o, want, A, 2.0 ** -14, o.dtype, "o")
+    within(fin, wfin, Afin, 2.0 ** -17, fin.dtype, "final state")
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], meta=x["meta"],
+                           initial_state=x["S0"], dht=x["dht"])
+    args += (x["dout"], x["dht"])
+    want, A = ref.linattn_grads(*args), ref.linattn_grads(*args, absolute=True)
+    for i, (n, t) in enumerate((("dq", "q"), ("dk", "k"), ("dv", "v"))):
+        h = x[t].shape[-2]
+        within(r[n], ref.shared(want[i], h), ref.shared(A[i], h), 2.0 ** -14, r[n].dtype, n)
+    within(r["dh0"], want[3], A[3], 2.0 ** -17, torch.float32, "dh0")
+
+
 def test_linattn_no_tokens():
     q = torch.empty(2, 0, 3, 128, dtype=torch.bfloat16, device=DEV)
     S0 = torch.randn(2, 3, 128, 128, device=DEV)
