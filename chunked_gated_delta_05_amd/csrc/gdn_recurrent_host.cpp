@@ -110,13 +110,18 @@ gdn_status check_prompt(const gdn_linattn_desc* d, int walks, Prompt* p) {
     // 213, in parts of a share 225; 3 prompts, T=9000 H=32: 116 and 126; 12,
     // T=4096 H=8: 43 and 40; fp32 gradients of 7 documents, T=3001 H=8: 105,
     // at a third of a share 116).
+    // A few chunks are walked before a second launch has begun (bf16 H=8, 2.9
+    // us a chunk: T=192 13.2 whole and 16.8 cut, T=320 19.2 and 18.7, with H=32
+    // 19.3 and 22.3; fp32 H=8 T=128 19.4 and 22.2).
     // At least two chunks, or one where a chunk's products take fp32 MFMA's
     // time (B=1 T=2048 H=8 at 1, 2 and 4 chunks: bf16 40, 34 and 38 us, fp32
     // 47, 55 and 85 us).
     const int64_t longest = (p->longest + kChunk - 1) / kChunk, work = p->chunks * d->H * walks;
     const int64_t least = d->dtype == GDN_DTYPE_F32 ? 1 : 2;
+    const int64_t whole = d->dtype == GDN_DTYPE_F32 ? 2 : 5;
     int64_t seg = longest;
-    if (u.dense) {
+    if (longest <= whole) {
+    } else if (u.dense) {
         const int64_t parts = 256 / (int64_t(u.n_units) * d->H);
         if (parts > 1) seg = (longest + parts - 1) / parts;
     } else if (longest * 256 * 5 > work * 7) {

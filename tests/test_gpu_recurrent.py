@@ -128,7 +128,8 @@ def test_linattn_many_sequences(lens):
 
 @pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64), (64, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("lens,packed", [([250, 250], False), ([256, 70, 1, 190], True), ([129], False)])
+@pytest.mark.parametrize("lens,packed", [([250, 250], False), ([256, 70, 1, 190], True), ([129], False),
+                                         ([400, 400], False), ([380, 70, 1, 450], True)])
 def test_linattn_few_segments(lens, packed, dtype, K, V):
     # two to four parts of a sequence: the walk adds up the parts before its own
     x = prompt(("", lens, packed, 2, 2, 1, 2), dtype, K, V, "mixed", seed=2)
