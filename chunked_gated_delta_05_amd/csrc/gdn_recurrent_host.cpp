@@ -53,6 +53,40 @@ struct Prompt {
     bool cut;      // some sequence has more than one segment
 };
 
+// segments of at most seg chunks
+int64_t segments(const gdn_linattn_desc* d, const LaUnits& u, int64_t seg) {
+    const int64_t tokens = seg * kChunk;
+    auto of = [&](int64_t len) { return len > 0 ? (len + tokens - 1) / tokens : 1; };
+    if (u.dense) return of(d->T) * u.n_units;
+    int64_t n = 0;
+    for (int32_t i = 0; i < u.n_units; ++i) n += of(int64_t(d->offsets_host[i + 1]) - d->offsets_host[i]);
+    return n;
+}
+
+// About how long n segments of at most seg chunks take. One workgroup's chunk
+// is 2.9 us (fp32 7) and its sum of k v^T 1.5 (2.5); all units together do a
+// chunk in a 200th of that. The last segments to start leave units idle for
+// about 0.6 of a segment. A cut costs a launch of 5 us, 4 more for a merge,
+// and its states, 64 KiB each for K = V = 128, about 6 TB/s. Whether to cut at
+// all is decided by it, which matters where a few chunks are walked before a
+// second launch has begun (measured whole and cut: bf16 H=8 T=192 13.2 and
+// 16.8 us, fp32 T=128 19.4 and 22.2, 12 prompts T=4096 37 and 44; gradients,
+// bf16 H=32 T=320 19 and 34, B=4 T=512 H=16 39 and 54; forward T=512 H=8 about
+// 28 and 21).
+double micros(const gdn_linattn_desc* d, const LaUnits& u, int walks, int64_t work, int64_t seg, int64_t n) {
+    const bool f32 = d->dtype == GDN_DTYPE_F32;
+    const double walk = f32 ? 7.0 : 2.9, sum = f32 ? 2.5 : 1.5;
+    const int sums = walks > 1 ? 2 : 1;   // states of the forward, and of its gradients
+    double t = fmax(seg * walk, work * walk / 200 + 0.6 * seg * walk);
+    if (n > u.n_units) {
+        const double parts = double(n) / u.n_units;
+        const bool join = parts <= kJoin;
+        t += (join ? 5 : 9) + fmax(seg * sum, double(n - u.n_units) * seg * d->H * sums * sum / 200);
+        t += double(n) * d->H * d->K * d->V * 4 * (sums + (join ? walks * (parts - 1) / 2 : 2 * sums + walks)) / 6e6;
+    }
+    return t;
+}
+
 // walks: of every sequence, in one launch
 gdn_status check_prompt(const gdn_linattn_desc* d, int walks, Prompt* p) {
     if (d == nullptr) return GDN_ERR_INVALID;
@@ -107,39 +141,28 @@ gdn_status check_prompt(const gdn_linattn_desc* d, int walks, Prompt* p) {
     // 204 us whole, 229 and 219 with 256 and 512 parts; gradients of 12
     // documents, T=16384 H=16, 0.84: 222, 266 and 272). Beyond that parts of
     // half a share, which fill both places of a unit (5 prompts, T=32768 H=16:
-    // 213, in parts of a share 225; 3 prompts, T=9000 H=32: 116 and 126; 12,
-    // T=4096 H=8: 43 and 40; fp32 gradients of 7 documents, T=3001 H=8: 105,
-    // at a third of a share 116).
-    // A few chunks are walked before a second launch has begun (bf16 H=8, 2.9
-    // us a chunk: T=192 13.2 whole and 16.8 cut, T=320 19.2 and 18.7, with H=32
-    // 19.3 and 22.3; fp32 H=8 T=128 19.4 and 22.2).
+    // 213, in parts of a share 225; 3 prompts, T=9000 H=32: 116 and 126; fp32 gradients
+    // of 7 documents, T=3001 H=8: 105, at a third of a share 116).
     // At least two chunks, or one where a chunk's products take fp32 MFMA's
     // time (B=1 T=2048 H=8 at 1, 2 and 4 chunks: bf16 40, 34 and 38 us, fp32
     // 47, 55 and 85 us).
     const int64_t longest = (p->longest + kChunk - 1) / kChunk, work = p->chunks * d->H * walks;
     const int64_t least = d->dtype == GDN_DTYPE_F32 ? 1 : 2;
-    const int64_t whole = d->dtype == GDN_DTYPE_F32 ? 2 : 5;
     int64_t seg = longest;
-    if (longest <= whole) {
-    } else if (u.dense) {
+    if (u.dense) {
         const int64_t parts = 256 / (int64_t(u.n_units) * d->H);
         if (parts > 1) seg = (longest + parts - 1) / parts;
     } else if (longest * 256 * 5 > work * 7) {
         seg = (work + 511) / 512;
     }
     if (seg < least) seg = least;
-    u.seg_tokens = (int32_t)(seg * kChunk);
-    int64_t n = 0;
-    for (int32_t i = 0; i < u.n_units; ++i) {
-        const int64_t len = u.dense ? d->T : int64_t(d->offsets_host[i + 1]) - d->offsets_host[i];
-        const int64_t k = len > 0 ? (len + u.seg_tokens - 1) / u.seg_tokens : 1;
-        n += k;
-        if (k > 1) p->cut = true;
-        if (u.dense) {
-            n = k * u.n_units;
-            break;
-        }
+    int64_t n = segments(d, u, seg);
+    if (n > u.n_units && micros(d, u, walks, work, longest, u.n_units) <= micros(d, u, walks, work, seg, n)) {
+        seg = longest;
+        n = u.n_units;
     }
+    u.seg_tokens = (int32_t)(seg * kChunk);
+    p->cut = n > u.n_units;
     u.join = p->cut && (longest + seg - 1) / seg <= kJoin;
     if (n * d->H * gdn::LA_MAX_JOBS > kMaxBlocks || int64_t(u.n_units) * d->H * 16 > kMaxBlocks) return GDN_ERR_INVALID;
     u.n_segs = (int32_t)n;
