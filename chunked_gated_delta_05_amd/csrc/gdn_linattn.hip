@@ -550,8 +550,8 @@ __device__ __forceinline__ void value_frags(const char* tile, int tid, typename 
 // split, scale and store. With full-length work on all units memory bounds it
 // (B=16 T=4096 H=32: 485 us, 4.4 TB/s), with less the latency of one chunk's
 // chain - scores, S's two terms, q S, P v, k v^T - which two workgroups a unit
-// overlap: B=4 T=4096 H=16 78 us of 113 (the rest is the segments' states),
-// 20 prompts of 32768 tokens and 32 heads 277 us, 2.7 TB/s. fp32 MFMA bounds
+// overlap: B=4 T=4096 H=16 81 us of 110 (the rest is the segments' states),
+// 20 prompts of 32768 tokens and 32 heads 280 us, 2.7 TB/s. fp32 MFMA bounds
 // fp32 (T=4096 H=16: 93 us). Eight waves a workgroup, deeper double buffers,
 // fewer address instructions and other orders of the products gain nothing.
 // Two workgroups a compute unit (77 KiB of LDS each for K = V = 128): the q
