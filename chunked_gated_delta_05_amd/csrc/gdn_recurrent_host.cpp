@@ -162,6 +162,7 @@ gdn_status check_prompt(const gdn_linattn_desc* d, int walks, Prompt* p) {
         n = u.n_units;
     }
     u.seg_tokens = (int32_t)(seg * kChunk);
+    if (seg * kChunk + p->longest > INT32_MAX) return GDN_ERR_UNSUPPORTED;   // a segment's end is an int
     p->cut = n > u.n_units;
     u.join = p->cut && (longest + seg - 1) / seg <= kJoin;
     if (n * d->H * gdn::LA_MAX_JOBS > kMaxBlocks || int64_t(u.n_units) * d->H * 16 > kMaxBlocks) return GDN_ERR_INVALID;

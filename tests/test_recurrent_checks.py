@@ -241,3 +241,11 @@ def test_workspace_is_the_states_between_segments():
     assert query(T=64)[1] == 256
     st, nb = query(T=4096)
     assert st == gb.GDN_OK and nb % (2 * 4 * 128 * 64 * 4) == 0 and nb > 256
+
+
+@pytest.mark.parametrize("T,status", [(2 ** 31 - 1 - 2 ** 26, gb.GDN_OK), (2 ** 31 - 1, gb.GDN_ERR_UNSUPPORTED)])
+def test_a_segments_end_is_an_int(T, status):
+    one = (64, 64)
+    kw = dict(B=1, T=T, H=1, Hq=1, Hk=1, Hv=1, K=64, V=64, q_stride=one, k_stride=one, v_stride=one)
+    assert query(**kw)[0] == status
+    assert query(n_units=1, offsets=[0, T], **kw)[0] == status
