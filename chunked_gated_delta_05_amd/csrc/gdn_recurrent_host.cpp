@@ -229,6 +229,14 @@ extern "C" gdn_status gdn_linattn_fwd(const gdn_linattn_desc* d, const void* q, 
     j.o = o;
     j.s_p = j.s_o = d->scale;
     j.s_w = 1.0f;
+    // a sequence's last segment may replace the state before its others have
+    // read it: where the two share memory the merge reads it in front of all
+    if (s_in && s_out) {
+        const int64_t page = int64_t(d->H) * d->K * d->V;
+        const float *in_end = s_in + page * (in_pages ? n_pages : p.u.n_units),
+                    *out_end = s_out + page * (out_pages ? n_pages : p.u.n_units);
+        if (s_in < out_end && s_out < in_end) p.u.join = 0;
+    }
     if (p.cut) {
         j.slots = static_cast<float*>(workspace);
         if (gdn::launch_la_summary(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;

@@ -219,6 +219,22 @@ def test_linattn_states_in_pages(lens):
         assert torch.equal(pool[p], before[p])
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("dtype,T", [("bf16", 500), ("fp32", 250)])
+@pytest.mark.parametrize("H", [2, 16])
+def test_linattn_state_in_place_over_few_segments(dtype, T, paged, H):
+    # the state is replaced only after every segment of its sequence has read it
+    K, n = 128, 4
+    x = prompt(("", [T] * n, False, H, H, H, H), dtype, K, K, "spread")
+    want, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], initial_state=x["S0"], output_final_state=True)
+    for _ in range(5):
+        state = x["S0"].clone()
+        pages = dict(initial_pages=torch.arange(n, dtype=torch.int32, device=DEV),
+                     final_pages=torch.arange(n, dtype=torch.int32, device=DEV)) if paged else {}
+        o, _ = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], initial_state=state, final_out=state, **pages)
+        assert torch.equal(o, want) and torch.equal(state, fin)
+
+
 @pytest.mark.parametrize("K,V", [(128, 128), (64, 128), (128, 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("case", PROMPTS, ids=lambda c: c[0])
