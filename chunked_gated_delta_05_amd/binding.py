@@ -16,6 +16,7 @@ import os
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -858,7 +859,9 @@ def gdn_linattn_bwd(q, k, v, decay, dout, scale=None, *, meta: UnitMeta | None =
 
 class LinearAttention(torch.autograd.Function):
     """gdn_linattn_fwd and gdn_linattn_bwd as one autograd op: (q, k, v,
-    decay, initial_state, scale, meta) -> (o, final state)."""
+    decay, initial_state, scale, meta) -> (o, final state). Its gradients come
+    from a native call without a graph of its own: differentiating them once
+    more raises."""
 
     @staticmethod
     def forward(ctx, q, k, v, decay, initial_state=None, scale=None, meta=None):
@@ -870,6 +873,7 @@ class LinearAttention(torch.autograd.Function):
         return o, fin
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dfin):
         q, k, v, decay, s0 = ctx.saved_tensors
         if do is None:
