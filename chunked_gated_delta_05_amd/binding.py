@@ -861,7 +861,7 @@ class LinearAttention(torch.autograd.Function):
     """gdn_linattn_fwd and gdn_linattn_bwd as one autograd op: (q, k, v,
     decay, initial_state, scale, meta) -> (o, final state). Its gradients come
     from a native call without a graph of its own: differentiating them once
-    more raises."""
+    more raises, and so does a decay that requires grad (a constant here)."""
 
     @staticmethod
     def forward(ctx, q, k, v, decay, initial_state=None, scale=None, meta=None):
@@ -875,6 +875,8 @@ class LinearAttention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do, dfin):
+        if ctx.needs_input_grad[3]:
+            raise NotImplementedError("LinearAttention has no gradient for decay: detach it")
         q, k, v, decay, s0 = ctx.saved_tensors
         if do is None:
             do = torch.zeros((*k.shape[:-2], decay.shape[0], v.shape[-1]), dtype=k.dtype, device=k.device)

@@ -54,3 +54,15 @@ def test_a_second_order_gradient_is_refused(inputs):
     dk, = torch.autograd.grad(o.square().sum(), k, create_graph=True)   # a gradient penalty
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (o.sum() + dk.square().sum()).backward()
+
+
+def test_a_gradient_of_decay_is_refused(inputs):
+    q, k, v, decay = inputs
+    learnt = decay.clone().requires_grad_()
+    with torch.no_grad():   # evaluating with a parameter is fine
+        o, _ = gb.LinearAttention.apply(q, k, v, learnt)
+    assert torch.equal(o, gb.LinearAttention.apply(q, k, v, decay)[0])
+    o, _ = gb.LinearAttention.apply(q, k, v, learnt)
+    with pytest.raises(NotImplementedError, match="decay"):
+        o.sum().backward()
+    assert learnt.grad is None
