@@ -17,7 +17,7 @@ using gdn::LaUnits;
 using gdn::RowsOf;
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;   // sanity bound on any tensor
-constexpr int64_t kMaxBlocks = int64_t(1) << 30;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of a launch, along x
 constexpr int kChunk = 64;
 // With at most this many segments in a sequence each walk adds up those before
 // its own instead of a merge in front of all (B=4 T=4096 H=16 in 4: 117 to 108
@@ -165,7 +165,11 @@ gdn_status check_prompt(const gdn_linattn_desc* d, int walks, Prompt* p) {
     if (seg * kChunk + p->longest > INT32_MAX) return GDN_ERR_UNSUPPORTED;   // a segment's end is an int
     p->cut = n > u.n_units;
     u.join = p->cut && (longest + seg - 1) / seg <= kJoin;
-    if (n * d->H * gdn::LA_MAX_JOBS > kMaxBlocks || int64_t(u.n_units) * d->H * 16 > kMaxBlocks) return GDN_ERR_INVALID;
+    // threads for a segment's head: la_main 256 for each walk, la_summary up to 512 for each kind of
+    // state; la_merge one for four values of a sequence's state
+    const int64_t each = walks > 1 ? (p->cut ? 1024 : 768) : (p->cut ? 512 : 256);
+    if (n * d->H * each > kMaxThreads) return GDN_ERR_UNSUPPORTED;
+    if (p->cut && int64_t(u.n_units) * d->H * (d->K * d->V / 4) > kMaxThreads) return GDN_ERR_UNSUPPORTED;
     u.n_segs = (int32_t)n;
     return GDN_OK;
 }
@@ -252,6 +256,11 @@ extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, 
     Prompt p;
     gdn_status st = check_prompt(d, 3, &p);
     if (st != GDN_OK) return st;
+    // la_group has a thread for four values of a shared head
+    if ((d->Hq < d->H && p.tokens * d->Hq * (d->K / 4) > kMaxThreads) ||
+        (d->Hk < d->H && p.tokens * d->Hk * (d->K / 4) > kMaxThreads) ||
+        (d->Hv < d->H && p.tokens * d->Hv * (d->V / 4) > kMaxThreads))
+        return GDN_ERR_UNSUPPORTED;
     // slots of S and of its gradient, then the per-head gradients of shared heads
     const int64_t slots = slot_bytes(p, d);
     auto part_bytes = [&](int32_t h, int32_t W) {
@@ -361,7 +370,7 @@ gdn_status check_step(const gdn_step_desc* d, const void* q, const void* k, cons
     if (d->N < 0 || d->H < 1 || d->Hq < 1 || d->Hk < 1 || d->Hv < 1 || d->n_pages < 0) return GDN_ERR_INVALID;
     if (d->H % d->Hq || d->H % d->Hk || d->H % d->Hv) return GDN_ERR_INVALID;
     if (!dtype_ok(d->dtype) || !dtype_ok(d->o_dtype) || !isfinite(d->scale)) return GDN_ERR_INVALID;
-    if (int64_t(d->N) * d->H * 4 > kMaxBlocks) return GDN_ERR_INVALID;
+    if (int64_t(d->N) * d->H * 256 > kMaxThreads) return GDN_ERR_UNSUPPORTED;   // a workgroup a state
     if (int64_t(d->n_pages) * d->H > kMaxElems / (128 * 128)) return GDN_ERR_INVALID;
     if (!strides_ok(d->q_stride, d->N, d->Hq, d->dtype) || !strides_ok(d->k_stride, d->N, d->Hk, d->dtype) ||
         !strides_ok(d->v_stride, d->N, d->Hv, d->dtype))

@@ -48,7 +48,9 @@ extern "C" {
  * reads head h / (H / Hx). Rows (the K or V values of one token and head) are
  * contiguous; tokens and heads may lie at any distance that keeps every row
  * 16-byte aligned (strides in elements); a token stride of 32 MiB or more,
- * or 65536 heads, is GDN_ERR_UNSUPPORTED.
+ * or 65536 heads, is GDN_ERR_UNSUPPORTED. So is work that a launch cannot
+ * hold, 2^32 threads: 256 for each head of each segment of a sequence (1024
+ * in the backward), and a quarter of the values of gradients of shared heads.
  *
  * Sequences are the B rows of T tokens (n_units = 0) or packed documents of
  * one row, offsets as in gdn_desc (a sequence's tokens are contiguous).
@@ -114,6 +116,7 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_desc* desc, const void* q, const vo
  * Single tokens: N sequences, one token each. Row n of q, k, v belongs to
  * page pages[n] of the pool (pages NULL: page n), whose states are advanced
  * in place. Rows without a page get o = 0. No two rows may name one page.
+ * N * H >= 2^24 is GDN_ERR_UNSUPPORTED.
  */
 typedef struct {
     int32_t N, H, Hq, Hk, Hv;

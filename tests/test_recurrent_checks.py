@@ -249,3 +249,69 @@ def test_a_segments_end_is_an_int(T, status):
     kw = dict(B=1, T=T, H=1, Hq=1, Hk=1, Hv=1, K=64, V=64, q_stride=one, k_stride=one, v_stride=one)
     assert query(**kw)[0] == status
     assert query(n_units=1, offsets=[0, T], **kw)[0] == status
+
+
+# ------------------------------------------------------------------ launch sizes
+def status_of(f, *args):
+    fn = getattr(gb.lib(), f)
+    fn.restype = ctypes.c_int
+    return fn(*args)
+
+
+NONE = ctypes.c_void_p(None)
+
+
+def bwd_query(**kw):
+    d = LinattnDesc(B=1, T=4, H=1, Hq=1, Hk=1, Hv=1, K=64, V=64, dtype=1, o_dtype=1, scale=0.1)
+    for n, x in kw.items():
+        setattr(d, n, x)
+    for n, h, w in (("q", d.Hq, d.K), ("k", d.Hk, d.K), ("v", d.Hv, d.V)):
+        getattr(d, n + "_stride")[:] = (h * w, w)
+    nb = ctypes.c_size_t(0)
+    return status_of("gdn_linattn_bwd", ctypes.byref(d), *[NONE] * 12, ctypes.byref(nb), NONE)
+
+
+# a launch has fewer than 2^32 threads along x: 256 for a row's head, in the
+# backward for each of three passes; a quarter of the values where shared heads are summed
+def test_forward_launches_of_2_to_the_32_threads_are_refused():
+    one = dict(T=1, H=32, Hq=1, Hk=1, Hv=1, K=64, V=64, q_stride=(64, 64), k_stride=(64, 64), v_stride=(64, 64))
+    assert query(B=2 ** 19 - 1, **one)[0] == gb.GDN_OK
+    assert query(B=2 ** 19, **one)[0] == gb.GDN_ERR_UNSUPPORTED
+
+
+def test_backward_launches_of_2_to_the_32_threads_are_refused():
+    most = (2 ** 32 - 1) // (3 * 256 * 32)
+    assert bwd_query(B=most, H=32, Hq=32, Hk=32, Hv=32) == gb.GDN_OK
+    assert bwd_query(B=most + 1, H=32, Hq=32, Hk=32, Hv=32) == gb.GDN_ERR_UNSUPPORTED
+    # tokens x shared heads x width / 4
+    for n in ("Hq", "Hk", "Hv"):
+        kw = {"Hq": 64, "Hk": 64, "Hv": 64, n: 32}
+        assert bwd_query(B=1, T=2 ** 23 - 1, H=64, **kw) == gb.GDN_OK
+        assert bwd_query(B=1, T=2 ** 23, H=64, **kw) == gb.GDN_ERR_UNSUPPORTED
+
+
+def test_merges_of_2_to_the_32_threads_are_refused():
+    # one long document among many of one token is cut; the merge has K V / 4 threads a document and head
+    one = dict(B=1, H=16, Hq=16, Hk=16, Hv=16, K=128, V=128, q_stride=(2048, 128), k_stride=(2048, 128),
+               v_stride=(2048, 128))
+    for docs, status in ((2 ** 16 - 1, gb.GDN_OK), (2 ** 16, gb.GDN_ERR_UNSUPPORTED)):
+        offs = [*range(docs), docs - 1 + 2 ** 22]
+        st, need = query(T=offs[-1], n_units=docs, offsets=offs, **one)
+        assert st == status
+        if st == gb.GDN_OK:   # cut: a state for each segment
+            assert need // (16 * 128 * 128 * 4) > docs + 4
+
+
+class StepDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "Hq", "Hk", "Hv", "K", "V", "dtype", "o_dtype")] + [
+        ("scale", ctypes.c_float), ("n_pages", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2)]
+
+
+def test_step_launches_of_2_to_the_32_threads_are_refused():
+    for N, status in ((2 ** 19 - 1, gb.GDN_ERR_INVALID), (2 ** 19, gb.GDN_ERR_UNSUPPORTED)):   # INVALID: no pointers given
+        d = StepDesc(N=N, H=32, Hq=32, Hk=32, Hv=32, K=128, V=128, dtype=1, o_dtype=1, scale=0.1, n_pages=1)
+        for s in (d.q_stride, d.k_stride, d.v_stride):
+            s[:] = (32 * 128, 128)
+        assert status_of("gdn_linattn_step", ctypes.byref(d), *[NONE] * 8) == status
+        assert status_of("gdn_recurrent_step", ctypes.byref(d), 0, 0, *[NONE] * 7, 0, NONE) == status
