@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "gdn_recurrent.h"
 #include "gdn_recurrent_internal.h"
 
@@ -28,6 +30,27 @@ constexpr int kJoin = 4;
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+struct Range {
+    const void* p;
+    int64_t bytes;
+};
+
+bool overlap(const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes);
+}
+
+// whether what a call writes is apart from what it reads and else writes
+bool apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+    for (const Range* w = written.begin(); w != written.end(); ++w) {
+        for (const Range& r : read)
+            if (overlap(*w, r)) return false;
+        for (const Range* x = w + 1; x != written.end(); ++x)
+            if (overlap(*w, *x)) return false;
+    }
+    return true;
+}
 
 bool width_ok(int32_t w) { return w == 64 || w == 128; }
 
@@ -441,6 +464,11 @@ gdn_status check_pool(const void* pool, int32_t n_layers, int32_t n_pages, int64
 
 extern "C" size_t gdn_pages_workspace_ints(int32_t n) { return 1 + 2 * (size_t)(n > 0 ? n : 0); }
 
+// Every workgroup of a small fork or compaction makes its own plan from the
+// inputs while the first one writes the outputs, so none of these may be an
+// input.
+static Range ints(const int32_t* p, int64_t n) { return Range{p, 4 * n}; }
+
 extern "C" gdn_status gdn_pages_copy(void* dst_pool, int32_t dst_n_pages, const void* src_pool, int32_t src_n_pages,
                                      int32_t n_layers, int64_t page_bytes, const int32_t* dst_pages,
                                      const int32_t* src_pages, int32_t n, hipStream_t stream) {
@@ -461,8 +489,12 @@ extern "C" gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pag
     if (st != GDN_OK) return st;
     if (n_slots < 0 || n_spare < 0) return GDN_ERR_INVALID;
     if (n_slots > gdn::FORK_MAX || n_spare > gdn::FORK_MAX) return GDN_ERR_UNSUPPORTED;
-    if (n_slots > 0 && (!table || !parent || !new_table || new_table == table)) return GDN_ERR_INVALID;
+    if (n_slots > 0 && (!table || !parent || !new_table)) return GDN_ERR_INVALID;
     if ((n_spare > 0 && !spare) || (n_slots + n_spare > 0 && !left) || !workspace) return GDN_ERR_INVALID;
+    if (!apart({ints(new_table, n_slots), ints(left, n_slots + n_spare),
+                ints(workspace, (int64_t)gdn_pages_workspace_ints(n_slots))},
+               {ints(table, n_slots), ints(parent, n_slots), ints(spare, n_spare)}))
+        return GDN_ERR_INVALID;
     const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
                           page_bytes};
     return run(gdn::launch_fork(a, table, parent, n_slots, spare, n_spare, new_table, left, workspace, stream));
@@ -475,8 +507,12 @@ extern "C" gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_
     if (st != GDN_OK) return st;
     if (n_slots < 0) return GDN_ERR_INVALID;
     if (n_pages > gdn::COMPACT_MAX) return GDN_ERR_UNSUPPORTED;
-    if (n_slots > 0 && (!table || !new_table || new_table == table)) return GDN_ERR_INVALID;
+    if (n_slots > 0 && (!table || !new_table)) return GDN_ERR_INVALID;
     if (!count || !workspace) return GDN_ERR_INVALID;
+    if (!apart({ints(new_table, n_slots), ints(count, 1),
+                ints(workspace, (int64_t)gdn_pages_workspace_ints(n_pages))},
+               {ints(table, n_slots)}))
+        return GDN_ERR_INVALID;
     const gdn::PoolArgs a{static_cast<char*>(pool), static_cast<const char*>(pool), n_layers, n_pages, n_pages,
                           page_bytes};
     return run(gdn::launch_compact(a, table, n_slots, new_table, count, workspace, stream));

@@ -172,8 +172,9 @@ gdn_status gdn_pages_copy(void* dst_pool, int32_t dst_n_pages, const void* src_p
  *   left       device int32 [n_slots + n_spare]: the free pages not taken, in
  *              order, then -1
  *   workspace  device int32 [gdn_pages_workspace_ints(n_slots)]
- * table is not changed; new_table must be another buffer. n_slots <= 8192,
- * n_spare <= 8192 (GDN_ERR_UNSUPPORTED beyond).
+ * The inputs are not changed: new_table, left and workspace that overlap one
+ * of them or each other are GDN_ERR_INVALID. n_slots <= 8192, n_spare <= 8192
+ * (GDN_ERR_UNSUPPORTED beyond).
  */
 gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes, const int32_t* table,
                           const int32_t* parent, int32_t n_slots, const int32_t* spare, int32_t n_spare,
@@ -184,9 +185,10 @@ gdn_status gdn_pages_fork(void* pool, int32_t n_layers, int32_t n_pages, int64_t
  * [0, count), count being their number: pages below count stay, the others
  * move, in ascending order, into the holes in ascending order. Slots may
  * share a page; entries out of range stay -1.
- *   new_table  device int32 [n_slots] (another buffer than table)
+ *   new_table  device int32 [n_slots]
  *   count      device int32 [1]
  *   workspace  device int32 [gdn_pages_workspace_ints(n_pages)]
+ * These three may not overlap table or each other (GDN_ERR_INVALID).
  * n_pages <= 2^17 (GDN_ERR_UNSUPPORTED beyond).
  */
 gdn_status gdn_pages_compact(void* pool, int32_t n_layers, int32_t n_pages, int64_t page_bytes, const int32_t* table,

@@ -315,3 +315,40 @@ def test_step_launches_of_2_to_the_32_threads_are_refused():
             s[:] = (32 * 128, 128)
         assert status_of("gdn_linattn_step", ctypes.byref(d), *[NONE] * 8) == status
         assert status_of("gdn_recurrent_step", ctypes.byref(d), 0, 0, *[NONE] * 7, 0, NONE) == status
+
+
+# ------------------------------------------------------------------ outputs that are inputs
+I64 = ctypes.c_int64
+AT = 1 << 30      # addresses that nothing may touch: a refused call enqueues nothing
+
+
+def fork_status(n, m, **at):
+    """The plan's buffers lie 1 MiB apart unless placed elsewhere."""
+    p = {b: AT + (i << 20) for i, b in enumerate(("table", "parent", "spare", "new_table", "left", "workspace"))}
+    p.update({b: p[x] + d for b, (x, d) in at.items()})
+    p = {b: ctypes.c_void_p(x) for b, x in p.items()}
+    return status_of("gdn_pages_fork", ctypes.c_void_p(AT << 4), 1, 600, I64(1024), p["table"], p["parent"], n, p["spare"],
+                     m, p["new_table"], p["left"], p["workspace"], NONE)
+
+
+@pytest.mark.parametrize("n,m", [(8, 4), (300, 260)])
+@pytest.mark.parametrize("out,at", [
+    ("left", ("spare", 0)),            # an in-place list of free pages
+    ("new_table", ("parent", 0)), ("new_table", ("table", 4)), ("new_table", ("table", -4)),
+    ("left", ("parent", -16)), ("left", ("table", 28)), ("left", ("new_table", 12)),
+    ("workspace", ("spare", 8)), ("workspace", ("new_table", -8)), ("workspace", ("left", 0)),
+])
+def test_a_fork_refuses_outputs_over_its_inputs(out, at, n, m):
+    assert fork_status(n, m, **{out: at}) == gb.GDN_ERR_INVALID
+
+
+@pytest.mark.parametrize("out,at", [
+    ("new_table", ("table", 0)), ("new_table", ("table", 4)), ("count", ("table", 28)), ("count", ("new_table", 0)),
+    ("workspace", ("table", 0)), ("workspace", ("new_table", -8)), ("workspace", ("count", -400)),
+])
+def test_a_compaction_refuses_outputs_over_its_inputs(out, at):
+    p = {b: AT + (i << 20) for i, b in enumerate(("table", "new_table", "count", "workspace"))}
+    p[out] = p[at[0]] + at[1]
+    p = {b: ctypes.c_void_p(x) for b, x in p.items()}
+    assert status_of("gdn_pages_compact", ctypes.c_void_p(AT << 4), 1, 60, I64(1024), p["table"], 8, p["new_table"],
+                     p["count"], p["workspace"], NONE) == gb.GDN_ERR_INVALID
