@@ -19,7 +19,7 @@ using gdn::LaUnits;
 using gdn::RowsOf;
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;   // sanity bound on any tensor
-constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;   // of a launch, along x
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 256;   // of a launch along x, in workgroups of 256
 constexpr int kChunk = 64;
 // With at most this many segments in a sequence each walk adds up those before
 // its own instead of a merge in front of all (B=4 T=4096 H=16 in 4: 117 to 108

@@ -290,6 +290,11 @@ def test_backward_launches_of_2_to_the_32_threads_are_refused():
         assert bwd_query(B=1, T=2 ** 23, H=64, **kw) == gb.GDN_ERR_UNSUPPORTED
 
 
+def test_whole_workgroups_of_sums_of_shared_heads_count():
+    # 2^32 - 16 values in fours fill the 2^24th workgroup of 256 in part
+    assert bwd_query(B=1, T=2 ** 28 - 1, H=2, Hq=1, Hk=2, Hv=2) == gb.GDN_ERR_UNSUPPORTED
+
+
 def test_merges_of_2_to_the_32_threads_are_refused():
     # one long document among many of one token is cut; the merge has K V / 4 threads a document and head
     one = dict(B=1, H=16, Hq=16, Hk=16, Hv=16, K=128, V=128, q_stride=(2048, 128), k_stride=(2048, 128),
