@@ -33,12 +33,12 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 struct Range {
     const void* p;
-    int64_t bytes;
+    uint64_t bytes;
 };
 
 bool overlap(const Range& a, const Range& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes);
+    return a.p && b.p && a.bytes && b.bytes && (x < y ? y - x < a.bytes : x - y < b.bytes);
 }
 
 // whether what a call writes is apart from what it reads and else writes
@@ -297,6 +297,13 @@ extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(s_in) || !aligned16(dht) ||
         !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(dh0))
         return GDN_ERR_INVALID;
+    // dh0 may be dht or s_in, which the other walks of its launch read: then a
+    // merge reads them in front of all, or dh0's walk comes after the others
+    const uint64_t states = uint64_t(p.u.n_units) * d->H * d->K * d->V * 4;
+    const bool over_dht = overlap({dh0, states}, {dht, states}), over_s_in = overlap({dh0, states}, {s_in, states});
+    if ((over_dht && dh0 != dht) || (over_s_in && dh0 != s_in)) return GDN_ERR_INVALID;
+    const bool last = (over_dht || over_s_in) && !p.cut;
+    if (over_dht || over_s_in) p.u.join = 0;
     p.u.decay = decay;
     char* base = static_cast<char*>(workspace);
     float* s_slots = p.cut ? reinterpret_cast<float*>(base) : nullptr;
@@ -372,8 +379,13 @@ extern "C" gdn_status gdn_linattn_bwd(const gdn_linattn_desc* d, const void* q, 
     jobs.job[0] = jq;
     jobs.job[1] = jk;
     jobs.job[2] = jv;
-    jobs.n = 3;
+    jobs.n = last ? 2 : 3;
     if (gdn::launch_la_main(p.u, jobs, d->dtype, d->V, d->K, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    if (last) {
+        jobs.job[0] = jv;
+        jobs.n = 1;
+        if (gdn::launch_la_main(p.u, jobs, d->dtype, d->K, d->V, stream) != hipSuccess) return GDN_ERR_DEVICE;
+    }
     if (pq && gdn::launch_la_group(pq, dq, p.tokens, d->H, d->Hq, d->K, d->dtype, stream) != hipSuccess)
         return GDN_ERR_DEVICE;
     if (pk && gdn::launch_la_group(pk, dk, p.tokens, d->H, d->Hk, d->K, d->dtype, stream) != hipSuccess)
@@ -467,7 +479,7 @@ extern "C" size_t gdn_pages_workspace_ints(int32_t n) { return 1 + 2 * (size_t)(
 // Every workgroup of a small fork or compaction makes its own plan from the
 // inputs while the first one writes the outputs, so none of these may be an
 // input.
-static Range ints(const int32_t* p, int64_t n) { return Range{p, 4 * n}; }
+static Range ints(const int32_t* p, int64_t n) { return Range{p, 4 * (uint64_t)n}; }
 
 extern "C" gdn_status gdn_pages_copy(void* dst_pool, int32_t dst_n_pages, const void* src_pool, int32_t src_n_pages,
                                      int32_t n_layers, int64_t page_bytes, const int32_t* dst_pages,

@@ -104,7 +104,9 @@ gdn_status gdn_linattn_fwd(const gdn_linattn_desc* desc, const void* q, const vo
  *   dq, dk, dv  device, contiguous [tokens][Hq][K], [tokens][Hk][K],
  *               [tokens][Hv][V] in desc->dtype: sums over the heads that share
  *               one, each rounded once
- *   dh0         device fp32 [units][H][K][V] or NULL
+ *   dh0         device fp32 [units][H][K][V] or NULL; may be dht or s_in
+ *               (each sequence's state is replaced), but not overlap them
+ *               otherwise (GDN_ERR_INVALID)
  * decay is a constant: it has no gradient. desc->o_dtype is not used.
  */
 gdn_status gdn_linattn_bwd(const gdn_linattn_desc* desc, const void* q, const void* k, const void* v,

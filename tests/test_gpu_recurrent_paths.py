@@ -1,0 +1,54 @@
+"""Paths of the recurrent-state operators that only some sizes take, on the
+GPU against 64-bit references (the bounds are those of test_gpu_recurrent.py,
+where they are derived)."""
+import ctypes
+
+import pytest
+import torch
+
+from chunked_gated_delta_05_amd import binding as gb
+from test_gpu_recurrent import DEV, prompt
+from test_recurrent_checks import LinattnDesc, status_of
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ dh0 in place of dht or the entry states
+def bwd(x, dh0, s_in, dht):
+    """gdn_linattn_bwd with the caller's dh0, through the C ABI."""
+    B, T, H, K = x["q"].shape
+    V = x["v"].shape[-1]
+    code = 1 if x["q"].dtype == torch.bfloat16 else 0
+    d = LinattnDesc(B=B, T=T, H=H, Hq=H, Hk=H, Hv=H, K=K, V=V, dtype=code, o_dtype=code, scale=x["scale"])
+    for n, w in (("q", K), ("k", K), ("v", V)):
+        getattr(d, n + "_stride")[:] = (H * w, w)
+    grads = [torch.empty_like(x[n]) for n in "qkv"]
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    nb = ctypes.c_size_t(0)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def call(ws):
+        return status_of("gdn_linattn_bwd", ctypes.byref(d), p(x["q"]), p(x["k"]), p(x["v"]), p(x["decay"]), p(s_in),
+                         p(x["dout"]), p(dht), *(p(g) for g in grads), p(dh0), ws, ctypes.byref(nb), stream)
+
+    assert call(ctypes.c_void_p(None)) == gb.GDN_OK
+    ws = torch.empty(nb.value, dtype=torch.uint8, device=DEV)
+    assert call(p(ws)) == gb.GDN_OK
+    torch.cuda.synchronize()
+    return grads
+
+
+@pytest.mark.parametrize("over", ["dht", "S0"])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128)])
+@pytest.mark.parametrize("dtype,B,T", [("bf16", 3, 90), ("bf16", 2, 500), ("fp32", 2, 250), ("bf16", 1, 1500)])
+def test_an_entry_state_gradient_in_place(dtype, B, T, K, V, over):
+    # uncut, in few segments, in many: the same bits as with a buffer of its own
+    x = prompt(("", [T] * B, False, 2, 2, 2, 2), dtype, K, V, "spread")
+    want = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], initial_state=x["S0"],
+                              dht=x["dht"])
+    for _ in range(3):
+        state = {"dht": x["dht"].clone(), "S0": x["S0"].clone()}
+        got = bwd(x, state[over], state["S0"], state["dht"])
+        assert torch.equal(state[over], want["dh0"])
+        for g, n in zip(got, ("dq", "dk", "dv")):
+            assert torch.equal(g, want[n]), n

@@ -357,3 +357,18 @@ def test_a_compaction_refuses_outputs_over_its_inputs(out, at):
     p = {b: ctypes.c_void_p(x) for b, x in p.items()}
     assert status_of("gdn_pages_compact", ctypes.c_void_p(AT << 4), 1, 60, I64(1024), p["table"], 8, p["new_table"],
                      p["count"], p["workspace"], NONE) == gb.GDN_ERR_INVALID
+
+
+# shifted against a state that another walk reads: no order of the sequences would do
+@pytest.mark.parametrize("over", ["dht", "s_in"])
+@pytest.mark.parametrize("shift", [16, -16, 1 << 18])
+@pytest.mark.parametrize("T", [40, 2000])      # uncut, cut
+def test_a_gradient_shifted_against_its_states_is_refused(over, shift, T):
+    d = LinattnDesc(B=2, T=T, H=4, Hq=4, Hk=4, Hv=4, K=128, V=128, dtype=1, o_dtype=1, scale=0.1)
+    for s in (d.q_stride, d.k_stride, d.v_stride):
+        s[:] = (512, 128)
+    at = {n: AT + (i << 26) for i, n in enumerate(("q", "k", "v", "decay", "s_in", "dout", "dht", "dq", "dk", "dv"))}
+    at["dh0"] = at[over] + shift
+    nb = ctypes.c_size_t(1 << 30)
+    assert status_of("gdn_linattn_bwd", ctypes.byref(d), *(ctypes.c_void_p(x) for x in at.values()),
+                     ctypes.c_void_p(AT << 4), ctypes.byref(nb), NONE) == gb.GDN_ERR_INVALID
