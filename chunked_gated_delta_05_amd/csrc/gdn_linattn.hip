@@ -224,13 +224,18 @@ __device__ __forceinline__ V lds_get(const char* base, int at) {
 // `lds`, straight from memory: no register is written, so nothing the
 // compiler knows of is outstanding and it waits for nothing; data_arrived and
 // a barrier come before the first read. Written in assembly because the
-// builtin makes the compiler wait for every copy before any LDS read.
+// builtin makes the compiler wait for every copy before any LDS read. m0 is a
+// register that the compiler reserves, so it warns of the clobber; it has to
+// know of it all the same, since it merges its own writes of m0.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t at, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(at), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // waits until at most the LATER youngest of this wave's memory accesses are
 // in flight
 template <int LATER>
