@@ -52,3 +52,46 @@ def test_an_entry_state_gradient_in_place(dtype, B, T, K, V, over):
         assert torch.equal(state[over], want["dh0"])
         for g, n in zip(got, ("dq", "dk", "dv")):
             assert torch.equal(g, want[n]), n
+
+
+# ------------------------------------------------------------------ decays over many tokens
+def awkward(n, lo=-1e-3, hi=-1e-4):
+    """n log decays whose e^g lies almost half a step beside the nearest fp32 number."""
+    g = torch.linspace(lo, hi, 20001)
+    d = torch.exp(g.double())
+    off = (d.float().double() - d).abs() / d
+    return g[off.argsort(descending=True)[:n]].sort().values
+
+
+def remaining(S0, S, g, n, exp2=False):
+    """How far S is from b^{g n} S0, relative to it, over its bound. Every step
+    rounds an element once, by at most 2^-24, here or there by chance: 8
+    standard deviations of n such errors, 2^-24 / sqrt(3) each, hold for all
+    elements; b^g - 1 to 2^-22 adds n |g| 2^-22."""
+    g = g.detach().cpu().double()
+    want = S0.cpu().double() * (torch.exp2(g * n) if exp2 else torch.exp(g * n))
+    bound = 8 * 2.0 ** -24 * (n / 3) ** 0.5 + n * g.abs() * 2.0 ** -22
+    return (((S.cpu().double() - want) / want).abs() / bound).max().item()
+
+
+def test_a_weak_decay_does_not_drift_over_linear_steps():
+    n, H = 4096, 4
+    decay = awkward(H).to(DEV)
+    S0 = torch.randn(1, H, 128, 64, generator=torch.Generator().manual_seed(1)).to(DEV)
+    S, zero, v = S0.clone(), torch.zeros(1, H, 128, device=DEV), torch.ones(1, H, 64, device=DEV)
+    for _ in range(n):
+        gb.gdn_linattn_step(zero, zero, v, decay, S)
+    assert remaining(S0, S, decay.view(1, H, 1, 1), n) <= 1
+
+
+@pytest.mark.parametrize("per_key,exp2", [(False, False), (False, True), (True, False), (True, True)])
+def test_a_weak_decay_does_not_drift_over_delta_steps(per_key, exp2):
+    n, H = 4096, 4
+    g = awkward(H * 128 if per_key else H).view(1, H, -1)
+    g = (g if per_key else g[..., 0]).contiguous().to(DEV)
+    S0 = torch.randn(1, H, 128, 128, generator=torch.Generator().manual_seed(2)).to(DEV)
+    S, zero, v = S0.clone(), torch.zeros(1, H, 128, device=DEV), torch.ones(1, H, 128, device=DEV)
+    beta = torch.ones(1, H, device=DEV)
+    for _ in range(n):
+        gb.gdn_recurrent_step(zero, zero, v, g, beta, S, use_exp2=exp2)
+    assert remaining(S0, S, g.view(1, H, -1, 1), n, exp2) <= 1
