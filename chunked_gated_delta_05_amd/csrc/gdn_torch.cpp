@@ -125,6 +125,14 @@ P* ptr(const Tensor& t) {
     return t.defined() ? static_cast<P*>(t.data_ptr()) : nullptr;
 }
 
+// What a call has written in place of what the caller's tensors held: autograd
+// then refuses a gradient that needs the old values. Tensors made in inference
+// mode have no version.
+void written(std::initializer_list<const Tensor*> tensors) {
+    for (const Tensor* t : tensors)
+        if (t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 hipStream_t stream_of(c10::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
 // (token, head) strides in elements of [B,T,h,D] or [tokens,h,D] rows that
@@ -289,6 +297,7 @@ PyObject* linattn_fwd(const Arguments& a) {
                           ptr<float>(fin), ptr<int32_t>(out_pages), narrow(n_pages < 0 ? 0 : n_pages, "n_pages"),
                           ptr(o), ptr(ws), &bytes, stream_of(p.dev)),
           "gdn_linattn_fwd");
+    written({&out, &final_out});
     PyObject* po = THPVariable_Wrap(o);
     PyObject* pf = fin.defined() ? THPVariable_Wrap(fin) : Py_NewRef(Py_None);
     PyObject* r = PyTuple_Pack(2, po, pf);
@@ -387,6 +396,7 @@ PyObject* linattn_step(const Arguments& a) {
     check(gdn_linattn_step(&d, ptr(q), ptr(k), ptr(v), ptr<float>(decay), ptr<int32_t>(pages), ptr<float>(state),
                            ptr(o), stream_of(k.device())),
           "gdn_linattn_step");
+    written({&state, &out});
     return THPVariable_Wrap(o);
 }
 
@@ -411,6 +421,7 @@ PyObject* recurrent_step(const Arguments& a) {
                              ptr<float>(g), ptr(beta), ptr<int32_t>(pages), ptr<float>(state), ptr(o),
                              narrow(a.integer(9), "flags"), stream_of(k.device())),
           "gdn_recurrent_step");
+    written({&state, &out});
     return THPVariable_Wrap(o);
 }
 
@@ -464,6 +475,7 @@ PyObject* pages_copy(const Arguments& a) {
     check(gdn_pages_copy(ptr(dst), d.pages, ptr(src), s.pages, d.layers, d.bytes, ptr<int32_t>(dp), ptr<int32_t>(sp), n,
                          stream_of(dst.device())),
           "gdn_pages_copy");
+    written({&dst});
     Py_RETURN_NONE;
 }
 
@@ -486,6 +498,7 @@ PyObject* pages_fork(const Arguments& a) {
                          ptr<int32_t>(spare), m, ptr<int32_t>(made), ptr<int32_t>(left), ptr<int32_t>(ws),
                          stream_of(pool.device())),
           "gdn_pages_fork");
+    written({&pool});
     return pair(made, left);
 }
 
@@ -500,6 +513,7 @@ PyObject* pages_compact(const Arguments& a) {
     check(gdn_pages_compact(ptr(pool), p.layers, p.pages, p.bytes, ptr<int32_t>(table), n, ptr<int32_t>(made),
                             ptr<int32_t>(count), ptr<int32_t>(ws), stream_of(pool.device())),
           "gdn_pages_compact");
+    written({&pool});
     return pair(made, count);
 }
 

@@ -95,3 +95,41 @@ def test_a_weak_decay_does_not_drift_over_delta_steps(per_key, exp2):
     for _ in range(n):
         gb.gdn_recurrent_step(zero, zero, v, g, beta, S, use_exp2=exp2)
     assert remaining(S0, S, g.view(1, H, -1, 1), n, exp2) <= 1
+
+
+# ------------------------------------------------------------------ autograd sees what is written in place
+def writers():
+    """name, the tensors it writes, the call."""
+    H, N = 2, 2
+    z = lambda *s: torch.zeros(*s, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    q, decay, pool = z(N, H, 128), z(H), z(3, H, 128, 128)
+    out, p4 = z(N, H, 128), z(1, 4, 2, 8)
+    yield "linear step", (pool, out), lambda: gb.gdn_linattn_step(q, q, q, decay, pool, out=out)
+    yield "delta step", (pool, out), lambda: gb.gdn_recurrent_step(q, q, q, z(N, H), z(N, H), pool, out=out)
+    x, o, fin = z(1, 5, H, 128), z(1, 5, H, 128), z(1, H, 128, 128)
+    yield "prompt", (o, fin), lambda: gb.gdn_linattn_fwd(x, x, x, decay, out=o, final_out=fin)
+    yield "prompt to a page", (pool,), lambda: gb.gdn_linattn_fwd(x, x, x, decay, final_out=pool, final_pages=i32(1))
+    yield "copy", (p4,), lambda: gb.gdn_pages_copy(p4, p4.clone(), i32(1), i32(0))
+    yield "fork", (p4,), lambda: gb.gdn_pages_fork(p4, i32(0, 1), i32(0, 0))
+    yield "compact", (p4,), lambda: gb.gdn_pages_compact(p4, i32(3))
+
+
+@pytest.mark.parametrize("i", range(7))
+def test_a_write_in_place_is_seen_by_autograd(i):
+    name, written, call = list(writers())[i]
+    for t in written:
+        w = torch.ones_like(t, requires_grad=True)
+        y = (w * t).sum()       # saves t
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+
+@pytest.mark.parametrize("i", range(7))
+def test_tensors_of_inference_mode_are_written_inside_and_outside(i):
+    with torch.inference_mode():
+        name, written, call = list(writers())[i]
+        call()
+    call()
+    torch.cuda.synchronize()
