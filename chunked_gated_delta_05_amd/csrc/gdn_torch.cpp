@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -132,6 +133,9 @@ void written(std::initializer_list<const Tensor*> tensors) {
     for (const Tensor* t : tensors)
         if (t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
+
+// A call launches on its tensors' device, whichever is current.
+using Guard = c10::DeviceGuard;
 
 hipStream_t stream_of(c10::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
@@ -283,6 +287,7 @@ PyObject* linattn_fwd(const Arguments& a) {
     check_device("initial_pages", in_pages, p.dev);
     check_device("final_out", final_out, p.dev);
     check_device("final_pages", out_pages, p.dev);
+    const Guard guard(p.dev);
     size_t bytes = 0;
     check(gdn_linattn_fwd(&p.d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, nullptr,
                           nullptr, &bytes, nullptr),
@@ -324,6 +329,7 @@ PyObject* linattn_bwd(const Arguments& a) {
     check_device("dout", dout, p.dev);
     check_device("initial_state", s_in, p.dev);
     check_device("dht", dht, p.dev);
+    const Guard guard(p.dev);
     size_t bytes = 0;
     check(gdn_linattn_bwd(&p.d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
                           nullptr, nullptr, nullptr, &bytes, nullptr),
@@ -392,6 +398,7 @@ PyObject* linattn_step(const Arguments& a) {
     d.scale = a.scale(5, d.K);
     check_tensor("decay", decay, ScalarType::Float, {d.H});
     step_devices(k, {{"q", &q}, {"v", &v}, {"state", &state}, {"pages", &pages}, {"decay", &decay}, {"out", &out}});
+    const Guard guard(k.device());
     const Tensor o = out.defined() ? out : at::empty({d.N, d.H, d.V}, k.options().dtype(ot));
     check(gdn_linattn_step(&d, ptr(q), ptr(k), ptr(v), ptr<float>(decay), ptr<int32_t>(pages), ptr<float>(state),
                            ptr(o), stream_of(k.device())),
@@ -416,6 +423,7 @@ PyObject* recurrent_step(const Arguments& a) {
     else check_tensor("g", g, ScalarType::Float, {d.N, d.H, d.K});
     check_tensor("beta", beta, k.scalar_type(), {d.N, d.H});
     step_devices(k, {{"q", &q}, {"v", &v}, {"state", &state}, {"pages", &pages}, {"g", &g}, {"beta", &beta}, {"out", &out}});
+    const Guard guard(k.device());
     const Tensor o = out.defined() ? out : at::empty({d.N, d.H, d.V}, k.options().dtype(ot));
     check(gdn_recurrent_step(&d, g.dim() == 3 ? GDN_GATE_PER_KEY : GDN_GATE_SCALAR, a.flag(8), ptr(q), ptr(k), ptr(v),
                              ptr<float>(g), ptr(beta), ptr<int32_t>(pages), ptr<float>(state), ptr(o),
@@ -472,6 +480,7 @@ PyObject* pages_copy(const Arguments& a) {
     check_device("src_pool", src, dst.device());
     check_device("dst_pages", dp, dst.device());
     check_device("src_pages", sp, dst.device());
+    const Guard guard(dst.device());
     check(gdn_pages_copy(ptr(dst), d.pages, ptr(src), s.pages, d.layers, d.bytes, ptr<int32_t>(dp), ptr<int32_t>(sp), n,
                          stream_of(dst.device())),
           "gdn_pages_copy");
@@ -492,6 +501,7 @@ PyObject* pages_fork(const Arguments& a) {
     check_device("table", table, pool.device());
     check_device("parent", parent, pool.device());
     check_device("spare", spare, pool.device());
+    const Guard guard(pool.device());
     const Tensor made = ints(pool, n), left = ints(pool, (int64_t)n + m),
                  ws = ints(pool, (int64_t)gdn_pages_workspace_ints(n));
     check(gdn_pages_fork(ptr(pool), p.layers, p.pages, p.bytes, ptr<int32_t>(table), ptr<int32_t>(parent), n,
@@ -509,6 +519,7 @@ PyObject* pages_compact(const Arguments& a) {
     const int32_t n = list_of("table", table);
     need_gpu("pools", pool);
     check_device("table", table, pool.device());
+    const Guard guard(pool.device());
     const Tensor made = ints(pool, n), count = ints(pool, 1), ws = ints(pool, (int64_t)gdn_pages_workspace_ints(p.pages));
     check(gdn_pages_compact(ptr(pool), p.layers, p.pages, p.bytes, ptr<int32_t>(table), n, ptr<int32_t>(made),
                             ptr<int32_t>(count), ptr<int32_t>(ws), stream_of(pool.device())),

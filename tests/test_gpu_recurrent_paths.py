@@ -133,3 +133,19 @@ def test_tensors_of_inference_mode_are_written_inside_and_outside(i):
         call()
     call()
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ devices
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_calls_run_on_their_tensors_device():
+    # a tensor of a device that is not the current one
+    def both(dev):
+        gen = torch.Generator().manual_seed(3)
+        x = [torch.randn(1, 70, 2, 128, generator=gen).to(dev) for _ in range(3)]
+        decay, pool = torch.full((2,), -0.1, device=dev), torch.zeros(2, 2, 128, 128, device=dev)
+        o, _ = gb.gdn_linattn_fwd(*x, decay)
+        return o, gb.gdn_linattn_step(*(t[:, 0] for t in x), decay, pool), pool
+
+    with torch.cuda.device(0):
+        for a, b in zip(both("cuda:1"), both("cuda:0")):
+            assert torch.equal(a.cpu(), b.cpu())
