@@ -529,6 +529,14 @@ PyObject* pages_compact(const Arguments& a) {
 }
 
 // ---- module
+void out_of_memory(const char* what) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, what);   // else the import's own error is set
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+}
+
 template <PyObject* (*F)(const Arguments&)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     try {
@@ -537,7 +545,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const std::logic_error& e) {
         PyErr_SetString(PyExc_NotImplementedError, e.what());
-    } catch (const c10::Error& e) {   // allocation
+    } catch (const c10::OutOfMemoryError& e) {   // torch.OutOfMemoryError, as from any allocation
+        out_of_memory(e.what_without_backtrace());
+    } catch (const c10::Error& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());

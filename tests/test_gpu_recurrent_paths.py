@@ -149,3 +149,10 @@ def test_calls_run_on_their_tensors_device():
     with torch.cuda.device(0):
         for a, b in zip(both("cuda:1"), both("cuda:0")):
             assert torch.equal(a.cpu(), b.cpu())
+
+
+# ------------------------------------------------------------------ errors
+def test_memory_that_is_not_there_raises_as_from_torch():
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device=DEV).expand(1, 2 ** 21, 1, 64)
+    with pytest.raises(torch.OutOfMemoryError):   # o alone is 1 TiB
+        gb.gdn_linattn_fwd(x, x, x, torch.zeros(4096, device=DEV))
