@@ -52,6 +52,8 @@ int32_t dtype_code(ScalarType t) {
 }
 
 // ---- arguments
+struct Raised {};   // Python's own error is set
+
 struct Arguments {
     PyObject* const* a;
     Py_ssize_t n;
@@ -66,7 +68,11 @@ struct Arguments {
         if (!THPVariable_Check(a[i])) invalid(std::string(what) + " must be a tensor");
         return THPVariable_Unpack(a[i]);
     }
-    bool flag(int i) const { return PyObject_IsTrue(a[i]) == 1; }
+    bool flag(int i) const {
+        const int x = PyObject_IsTrue(a[i]);
+        if (x < 0) throw Raised();
+        return x == 1;
+    }
     int64_t integer(int i) const {
         const long long x = PyLong_AsLongLong(a[i]);
         if (x == -1 && PyErr_Occurred()) {
@@ -541,6 +547,7 @@ template <PyObject* (*F)(const Arguments&)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     try {
         return F(Arguments{args, n, "native entry"});
+    } catch (const Raised&) {
     } catch (const std::invalid_argument& e) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const std::logic_error& e) {

@@ -156,3 +156,11 @@ def test_memory_that_is_not_there_raises_as_from_torch():
     x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device=DEV).expand(1, 2 ** 21, 1, 64)
     with pytest.raises(torch.OutOfMemoryError):   # o alone is 1 TiB
         gb.gdn_linattn_fwd(x, x, x, torch.zeros(4096, device=DEV))
+
+
+def test_a_flag_without_a_truth_value_raises_its_own_error():
+    x, pool = torch.zeros(1, 2, 128, device=DEV), torch.zeros(1, 2, 128, 128, device=DEV)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        gb.gdn_recurrent_step(x, x, x, torch.zeros(1, 2, device=DEV), torch.zeros(1, 2, device=DEV), pool,
+                              use_exp2=torch.zeros(2))
+    assert not pool.any()
