@@ -824,7 +824,11 @@ def _native():
 
 
 def _meta_args(meta):
-    return (None, 0, 0) if meta is None else (meta.offsets_dev, len(meta.offsets) - 1, ctypes.addressof(meta.host))
+    if meta is None:
+        return None, 0, 0
+    if len(meta.host) != len(meta.offsets):
+        raise ValueError(f"meta's host copy has {len(meta.host)} offsets, not {len(meta.offsets)}")
+    return meta.offsets_dev, len(meta.offsets) - 1, ctypes.addressof(meta.host)
 
 
 def gdn_linattn_fwd(q, k, v, decay, scale=None, *, meta: UnitMeta | None = None, initial_state=None,

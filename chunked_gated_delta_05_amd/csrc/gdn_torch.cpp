@@ -232,6 +232,8 @@ Prompt prompt(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& d
     row_strides("v", v, p.d.v_stride);
     p.units = n == 4 ? p.d.B : n_units;
     if (offsets.defined()) {
+        if (n_units < 1) invalid("meta has no documents");
+        check_tensor("meta's device offsets", offsets, ScalarType::Int, {n_units + 1});
         p.d.n_units = narrow(n_units, "units");
         p.d.offsets_host = reinterpret_cast<const int32_t*>(host);
         p.d.offsets_dev = ptr<int32_t>(offsets);

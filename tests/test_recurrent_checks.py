@@ -372,3 +372,22 @@ def test_a_gradient_shifted_against_its_states_is_refused(over, shift, T):
     nb = ctypes.c_size_t(1 << 30)
     assert status_of("gdn_linattn_bwd", ctypes.byref(d), *(ctypes.c_void_p(x) for x in at.values()),
                      ctypes.c_void_p(AT << 4), ctypes.byref(nb), NONE) == gb.GDN_ERR_INVALID
+
+
+# ------------------------------------------------------------------ unit metadata
+@pytest.mark.parametrize("change,msg", [
+    ({"offsets_dev": torch.zeros(2, dtype=I32)}, "offsets must have shape"),     # the kernels read one for every document
+    ({"offsets_dev": torch.zeros(3)}, "offsets must be torch.int32"),
+    ({"offsets_dev": torch.zeros(6, dtype=I32)[::2]}, "offsets must be contiguous"),
+    ({"offsets": [0, 30, 50, 70], "offsets_dev": torch.zeros(4, dtype=I32)}, "host copy"),
+    ({"offsets": [0], "offsets_dev": torch.zeros(1, dtype=I32), "host": (ctypes.c_int32 * 1)(0)}, "no documents"),
+])
+def test_unit_metadata_is_checked(change, msg):
+    x = {n: t[0] if t.dim() == 4 else t for n, t in prompt().items()}
+    m = meta()
+    for n, y in change.items():
+        setattr(m, n, y)
+    with pytest.raises(ValueError, match=msg):
+        fwd(x, meta=m)
+    with pytest.raises(ValueError, match=msg):
+        gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], torch.zeros(T, H, V, dtype=BF), meta=m)
