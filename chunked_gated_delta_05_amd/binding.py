@@ -845,7 +845,7 @@ def gdn_linattn_fwd(q, k, v, decay, scale=None, *, meta: UnitMeta | None = None,
     or a pool [n_pages,H,K,V] with initial_pages int32 [units] (-1: zero
     state). final_out likewise with final_pages (-1: not written); it may be
     the pool that initial_state is. out: contiguous [..,H,V] in o_dtype (the
-    inputs' dtype by default). Returns (o, final state or None)."""
+    inputs' dtype by default), apart from the inputs. Returns (o, final state or None)."""
     return (_NATIVE or _native()).linattn_fwd(q, k, v, decay, scale, *_meta_args(meta), initial_state, initial_pages,
                                               output_final_state, final_out, final_pages, o_dtype, out, workspace)
 
@@ -894,7 +894,8 @@ def gdn_linattn_step(q, k, v, decay, state, scale=None, *, pages=None, o_dtype=N
     v^T, o = scale S^T q, with S updated in place. q [N,Hq,K], k [N,Hk,K], v
     [N,Hv,V] (strides as in gdn_linattn_fwd); decay fp32 [H]; state: fp32 pool
     [n_pages,H,K,V]; pages: int32 [N], distinct (-1: no sequence, o = 0), or
-    None (row n uses page n). Returns o [N,H,V]."""
+    None (row n uses page n). out may not overlap the inputs. Returns o
+    [N,H,V]."""
     return (_NATIVE or _native()).linattn_step(q, k, v, decay, state, scale, pages, o_dtype, out)
 
 

@@ -111,6 +111,21 @@ void check_tensor(const char* name, const Tensor& t, ScalarType dtype, at::IntAr
     if (!t.is_contiguous()) invalid(std::string(name) + " must be contiguous");
 }
 
+// An output given by the caller may not be one of the inputs: workgroups read
+// them while others write it. Of strided inputs everything from the first
+// value to the last counts (their strides are not negative).
+void check_apart(const Tensor& out, std::initializer_list<std::pair<const char*, const Tensor*>> others) {
+    if (!out.defined() || out.numel() == 0) return;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.data_ptr()), a_end = a + out.nbytes();
+    for (const auto& [name, t] : others) {
+        if (!t->defined() || t->numel() == 0) continue;
+        int64_t last = 0;
+        for (int64_t i = 0; i < t->dim(); ++i) last += (t->size(i) - 1) * t->stride(i);
+        const uintptr_t b = reinterpret_cast<uintptr_t>(t->data_ptr());
+        if (a < b + (last + 1) * t->element_size() && b < a_end) invalid(std::string("out overlaps ") + name);
+    }
+}
+
 void check_device(const char* name, const Tensor& t, c10::Device dev) {
     if (t.defined() && t.device() != dev) invalid(std::string(name) + " must be on " + dev.str() + ", got " + t.device().str());
 }
@@ -289,6 +304,7 @@ PyObject* linattn_fwd(const Arguments& a) {
     };
     state("initial_state", s_in, in_pages);
     state("final_out", final_out, out_pages);
+    check_apart(out, {{"q", &q}, {"k", &k}, {"v", &v}, {"initial_state", &s_in}, {"final_out", &final_out}});
     prompt_devices(p, q, k, v, decay, offsets);
     check_device("out", out, p.dev);
     check_device("initial_state", s_in, p.dev);
@@ -387,6 +403,7 @@ gdn_step_desc step(const Tensor& q, const Tensor& k, const Tensor& v, int64_t H,
     row_strides("q", q, d.q_stride);
     row_strides("k", k, d.k_stride);
     row_strides("v", v, d.v_stride);
+    check_apart(out, {{"q", &q}, {"k", &k}, {"v", &v}, {"state", &state}});
     return d;
 }
 

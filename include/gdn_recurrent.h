@@ -78,7 +78,8 @@ typedef struct {
  *                  sequences must not write one page, nor one write a page
  *                  that another reads
  *   n_pages        pages of both pools (ignored without page lists)
- *   o              device [tokens][H][V] in o_dtype, contiguous
+ *   o              device [tokens][H][V] in o_dtype, contiguous; apart from
+ *                  all else
  *   workspace      as for gdn_chunk_fwd (size query with NULL)
  * Products with bf16 inputs run on bf16 MFMA with fp32 accumulation; the
  * values computed on the way are split into two bf16 terms (scores and the
@@ -132,7 +133,7 @@ typedef struct {
 /*
  * gdn_linattn_step - S = d S + k v^T, o = scale * S^T q.
  *   state  device fp32 [n_pages][H][K][V], updated in place
- *   o      device [N][H][V] in o_dtype
+ *   o      device [N][H][V] in o_dtype, apart from all else
  */
 gdn_status gdn_linattn_step(const gdn_step_desc* desc, const void* q, const void* k, const void* v,
                             const float* decay, const int32_t* pages, float* state, void* o, hipStream_t stream);

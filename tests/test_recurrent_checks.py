@@ -391,3 +391,32 @@ def test_unit_metadata_is_checked(change, msg):
         fwd(x, meta=m)
     with pytest.raises(ValueError, match=msg):
         gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], torch.zeros(T, H, V, dtype=BF), meta=m)
+
+
+# ------------------------------------------------------------------ out over an input
+@pytest.mark.parametrize("over", ["q", "k", "v", "initial_state", "final_out"])
+def test_a_prompts_out_over_an_input_is_refused(over):
+    # a head's value columns may be two workgroups' work, and each reads all of q and k
+    n, h = 60, 2
+    buf = {m: torch.zeros(n * h * 64 + 64) for m in "qkv"}
+    x = {m: t[:n * h * 64].view(1, n, h, 64) for m, t in buf.items()}
+    states = {m: torch.zeros(1, h, 64, 64) for m in ("initial_state", "final_out")}
+    if over not in states:
+        out = buf[over][64:].view(1, n, h, 64)    # shifted by a row: contiguous, 16-byte aligned
+    else:                                          # one token that ends inside the state
+        x = {m: t[:, :1, :1] for m, t in x.items()}
+        states = {m: torch.zeros(1, 1, 64, 64) for m in states}
+        out = states[over].flatten()[-64:].view(1, 1, 1, 64)
+    with pytest.raises(ValueError, match=f"out overlaps {over}"):
+        gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], torch.zeros(x["q"].shape[2]), out=out, **states)
+    with pytest.raises(ValueError, match="GPU tensors"):
+        gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], torch.zeros(x["q"].shape[2]), out=out.clone(), **states)
+
+
+@pytest.mark.parametrize("over", ["q", "k", "v", "state"])
+def test_a_steps_out_over_an_input_is_refused(over):
+    x = rows(q=torch.zeros(N, H, 128), k=torch.zeros(N, H, 128), v=torch.zeros(N, H, 128), beta=torch.zeros(N, H))
+    out = x["state"].flatten()[:N * H * 128].view(N, H, 128) if over == "state" else x[over]
+    for f in steps(x, out=out):
+        with pytest.raises(ValueError, match=f"out overlaps {over}"):
+            f()
