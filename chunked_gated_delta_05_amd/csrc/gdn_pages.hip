@@ -17,10 +17,11 @@ constexpr int PIECE = 16384;   // bytes a workgroup copies at a time: 4 x 16 byt
 constexpr int PT = 1024;       // threads of the plans
 
 // The first n pairs of the lists, every layer, spread over the grid.
-// NT_LOAD, NT_STORE: around the caches. Pools beyond the last-level cache
-// (1.6 GB forked, 1.1 GB compacted): stores around it take 316 to 304 us and
-// 203 to 196 us, loads as well 189 us where every page is read once, but 320
-// where beams share parents, whose pages the caches serve.
+// NT_LOAD, NT_STORE: around the caches, where a call walks through more than
+// they hold (beyond_caches). Stores around them: 128 slots of 16.8 MB forked
+// 325 to 268 us. Loads as well only where no page is read twice: 1.1 GB
+// compacted 196 to 189 us, but a page copied to 128 others 322 to 525 (128
+// different ones 656 to 648).
 template <bool NT_LOAD, bool NT_STORE>
 __device__ __forceinline__ void copy_pairs(const PoolArgs& a, const int32_t* dst_pages, const int32_t* src_pages, int n) {
     const int64_t pieces = (a.page_bytes + PIECE - 1) / PIECE;
@@ -293,25 +294,32 @@ __global__ __launch_bounds__(NT) void compact_kernel(PoolArgs a, CompactArgs f) 
 
 namespace {
 
-bool beyond_caches(const PoolArgs& pool) {
-    return (int64_t)pool.n_layers * pool.src_pages * pool.page_bytes > LAST_LEVEL_BYTES;
+// Whether the pages that a call walks through exceed the last-level cache: a
+// fork's and a compaction's slots, both lists of a copy. Not the pool's size:
+// copies of a few pages of a large one stay in the caches for the next step
+// that reads them (slots of 16.8 MB in 3.4 GB, forked or compacted and then
+// read and written by a step of every layer: 8 of them 98 us through the
+// caches and 100 around, 134 and 140; 16 of them 156 and 154, 222 and 221; 24
+// 250 and 242, 345 and 329).
+bool beyond_caches(const PoolArgs& pool, int64_t pages) {
+    return pages * pool.n_layers * pool.page_bytes > LAST_LEVEL_BYTES;
 }
 // Workgroups for at most n pairs: four a compute unit, each making the plan
 // once; beyond the caches, where copying takes far longer than a plan, four
 // times as many, which even out (3.2 GB, 128 slots: 284 to 259 us forked, 313
 // to 273 compacted; 80 MB, 20 slots: 8.0 us at 1024, 9.9 at 4096).
-unsigned copy_blocks(const PoolArgs& pool, int n) {
+unsigned copy_blocks(const PoolArgs& pool, int n, bool beyond) {
     const int64_t items = (pool.page_bytes + PIECE - 1) / PIECE * pool.n_layers * n;
-    const int64_t most = beyond_caches(pool) ? 4096 : 1024;
+    const int64_t most = beyond ? 4096 : 1024;
     return (unsigned)(items < most ? items : most);
 }
 
 // read_once: no page is the source of several
 hipError_t copy_listed(const PoolArgs& pool, const int32_t* dst_pages, const int32_t* src_pages, int n,
-                       const int32_t* n_dev, bool read_once, hipStream_t s) {
-    const unsigned blocks = copy_blocks(pool, n);
+                       const int32_t* n_dev, bool beyond, bool read_once, hipStream_t s) {
+    const unsigned blocks = copy_blocks(pool, n, beyond);
     if (blocks == 0) return hipSuccess;
-    if (!beyond_caches(pool)) copy_kernel<false, false><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
+    if (!beyond) copy_kernel<false, false><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
     else if (read_once) copy_kernel<true, true><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
     else copy_kernel<false, true><<<blocks, NT, 0, s>>>(pool, dst_pages, src_pages, n, n_dev);
     return hipGetLastError();
@@ -321,36 +329,39 @@ hipError_t copy_listed(const PoolArgs& pool, const int32_t* dst_pages, const int
 
 hipError_t launch_pages_copy(const PoolArgs& pool, const int32_t* dst_pages, const int32_t* src_pages, int n,
                              hipStream_t s) {
-    return copy_listed(pool, dst_pages, src_pages, n, nullptr, true, s);
+    return copy_listed(pool, dst_pages, src_pages, n, nullptr, beyond_caches(pool, 2 * (int64_t)n), false, s);
 }
 
 hipError_t launch_fork(const PoolArgs& pool, const int32_t* table, const int32_t* parent, int n, const int32_t* spare,
                        int m, int32_t* new_table, int32_t* left, int32_t* ws, hipStream_t s) {
     const ForkArgs f{pool.src_pages, n, m, table, parent, spare, new_table, left};
+    const bool beyond = beyond_caches(pool, n);
     if (n <= FORK_SMALL && m <= FORK_SMALL) {
-        const unsigned blocks = copy_blocks(pool, n);
-        if (beyond_caches(pool)) fork_kernel<true><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
+        const unsigned blocks = copy_blocks(pool, n, beyond);
+        if (beyond) fork_kernel<true><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
         else fork_kernel<false><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
         return hipGetLastError();
     }
     fork_plan_kernel<<<1, PT, 0, s>>>(f, ws);
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : copy_listed(pool, ws + 1 + n, ws + 1, n, ws, false, s);
+    return e != hipSuccess ? e : copy_listed(pool, ws + 1 + n, ws + 1, n, ws, beyond, false, s);
 }
 
 hipError_t launch_compact(const PoolArgs& pool, const int32_t* table, int n, int32_t* new_table, int32_t* count,
                           int32_t* ws, hipStream_t s) {
     const int n_pages = pool.src_pages;
     const CompactArgs f{n_pages, n, table, new_table, count};
+    const int moves = n < n_pages ? n : n_pages;   // at most
+    const bool beyond = beyond_caches(pool, moves);
     if (n_pages <= COMPACT_SMALL && n <= COMPACT_SMALL) {
-        const unsigned blocks = copy_blocks(pool, n_pages);
-        if (beyond_caches(pool)) compact_kernel<true><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
+        const unsigned blocks = copy_blocks(pool, moves, beyond);
+        if (beyond) compact_kernel<true><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
         else compact_kernel<false><<<blocks ? blocks : 1, NT, 0, s>>>(pool, f);
         return hipGetLastError();
     }
     compact_plan_kernel<<<1, PT, 0, s>>>(f, ws);
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : copy_listed(pool, ws + 1 + n_pages, ws + 1, n_pages, ws, true, s);
+    return e != hipSuccess ? e : copy_listed(pool, ws + 1 + n_pages, ws + 1, moves, ws, beyond, true, s);
 }
 
 }  // namespace gdn
