@@ -6,8 +6,9 @@ import ctypes
 import pytest
 import torch
 
+import recurrent_ref as ref
 from chunked_gated_delta_05_amd import binding as gb
-from test_gpu_recurrent import DEV, prompt
+from test_gpu_recurrent import DEV, DT, prompt, within
 from test_recurrent_checks import LinattnDesc, status_of
 
 pytestmark = pytest.mark.gpu
@@ -164,3 +165,244 @@ def test_a_flag_without_a_truth_value_raises_its_own_error():
         gb.gdn_recurrent_step(x, x, x, torch.zeros(1, 2, device=DEV), torch.zeros(1, 2, device=DEV), pool,
                               use_exp2=torch.zeros(2))
     assert not pool.any()
+
+
+# ------------------------------------------------------------------ full-width walks
+# From 129 segments' heads on (n below), a workgroup takes all 128 value
+# columns; up to there two share them. Everything here has n >= 256 in the
+# forward, where it is one walk a segment and head, and checks that.
+def walks(x):
+    """n: segments x heads of a call, from the workspace that it asks for."""
+    q, k, v, offs = x["q"], x["k"], x["v"], x["offs"]
+    H, K, V = x["decay"].shape[0], q.shape[-1], v.shape[-1]
+    code = 1 if q.dtype == torch.bfloat16 else 0
+    d = LinattnDesc(B=1, T=offs[-1], H=H, Hq=q.shape[-2], Hk=k.shape[-2], Hv=v.shape[-2], K=K, V=V, dtype=code,
+                    o_dtype=code, scale=0.1)
+    if x["meta"] is None:
+        d.B, d.T = q.shape[0], q.shape[1]
+    else:
+        d.n_units = len(offs) - 1
+        d.offsets_host = ctypes.cast(x["meta"].host, ctypes.POINTER(ctypes.c_int32))
+        d.offsets_dev = x["meta"].offsets_dev.data_ptr()
+    for n, t in (("q", q), ("k", k), ("v", v)):
+        getattr(d, n + "_stride")[:] = (t.shape[-2] * t.shape[-1], t.shape[-1])
+    nb, none = ctypes.c_size_t(0), ctypes.c_void_p(None)
+    assert status_of("gdn_linattn_fwd", ctypes.byref(d), *[none] * 8, 0, none, none, ctypes.byref(nb), none) == gb.GDN_OK
+    segs = nb.value // (H * K * V * 4) if nb.value > 256 else len(offs) - 1
+    return segs * H, segs > len(offs) - 1
+
+
+def chunked(q, k, v, decay, scale, offsets, S0, late=0, reverse=False, absolute=False):
+    """o and final states of the recurrence in 64 bits on the GPU, 32 tokens at
+    a time by its own definition: o_i = scale (sum_{j <= i} d^{i-j} (q_i . k_j)
+    v_j + d^{i+1-late} q_i S); late: the decay follows a token's k v^T. [tokens,
+    H, D] each, S0 [units, H, K, V]."""
+    if absolute:
+        q, k, v, S0, scale = q.abs(), k.abs(), v.abs(), S0.abs(), abs(scale)
+    d = torch.exp(decay.double())
+    power = lambda n: torch.where(n == 0, torch.ones_like(n), d[:, None] ** n)      # [H, n]; 0^0 = 1
+    o, final = torch.empty(q.shape[0], q.shape[1], v.shape[2], dtype=torch.float64, device=DEV), S0.clone()
+    for u, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        at = torch.arange(a, b, device=DEV)
+        at = at.flip(0) if reverse else at
+        for c in at.split(32):
+            n, S = len(c), final[u]
+            i = torch.arange(n, device=DEV, dtype=torch.float64)
+            qc, kc, vc = (t[c].transpose(0, 1) for t in (q, k, v))                     # [H, n, D]
+            gap = (i[:, None] - i[None, :]).clamp(min=0)
+            inside = power(gap.flatten()[None].expand(len(d), -1)).view(-1, n, n).tril()
+            y = ((qc @ kc.transpose(1, 2).contiguous()) * inside) @ vc
+            y = y + power((i + 1 - late)[None].expand(len(d), -1))[..., None] * (qc @ S)
+            o[c] = scale * y.transpose(0, 1)
+            left = power((n - 1 + late - i)[None].expand(len(d), -1))[..., None]
+            final[u] = power(torch.full((len(d), 1), float(n), dtype=torch.float64, device=DEV))[..., None] * S + \
+                (left * kc).transpose(1, 2).contiguous() @ vc
+    return o, final
+
+
+def on_gpu(x, absolute=False):
+    """The forward's and the backward's results in 64 bits."""
+    H, scale, offs, decay = x["decay"].shape[0], x["scale"], x["offs"], x["decay"]
+    flat = lambda t: t.double().reshape(-1, *t.shape[-2:])
+    q, k, v, do = (flat(x[n]).repeat_interleave(H // x[n].shape[-2], dim=1) for n in ("q", "k", "v", "dout"))
+    zero = torch.zeros(len(offs) - 1, H, q.shape[2], v.shape[2], dtype=torch.float64, device=DEV)
+    S0 = zero if x["S0"] is None else x["S0"].double()
+    D = zero if x["dht"] is None else x["dht"].double()
+    T = lambda t: t.transpose(-1, -2).contiguous()
+    o, fin = chunked(q, k, v, decay, scale, offs, S0, absolute=absolute)
+    dq, _ = chunked(do, v, k, decay, scale, offs, T(S0), absolute=absolute)
+    dk, _ = chunked(v, scale * do, q, decay, 1.0, offs, T(D), late=1, reverse=True, absolute=absolute)
+    dv, dh0 = chunked(k, scale * q, do, decay, 1.0, offs, D, late=1, reverse=True, absolute=absolute)
+    return {"o": o, "fin": fin, "dq": dq, "dk": dk, "dv": dv, "dh0": dh0}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_reference_in_chunks_is_the_one_by_tokens(dtype):
+    x = prompt(("", [1, 32, 33, 70], True, 4, 4, 2, 1), dtype, 64, 128, "mixed")
+    args = (x["q"], x["k"], x["v"], x["decay"], x["scale"], x["offs"], x["S0"])
+    for absolute in (False, True):
+        got = on_gpu(x, absolute)
+        want = dict(zip(("o", "fin"), ref.linattn(*args, absolute=absolute)))
+        want.update(zip(("dq", "dk", "dv", "dh0"),
+                        ref.linattn_grads(*args, x["dout"], x["dht"], absolute=absolute)))
+        for n in want:
+            torch.testing.assert_close(got[n].cpu(), want[n], rtol=1e-11, atol=1e-11)
+
+
+# name, lengths, packed, H, Hq, Hk, Hv, and whether the forward cuts them
+WIDE = [
+    ("rows, joined", [1000] * 4, False, 16, 16, 16, 16, True),
+    ("rows", [200] * 17, False, 16, 16, 8, 16, False),
+    ("row, merged", [2040], False, 32, 8, 32, 32, True),
+    ("documents", [1 + 37 * i % 331 for i in range(20)], True, 16, 16, 4, 4, False),
+    ("documents, joined", [1000] + [499, 500] * 12, True, 8, 8, 8, 4, True),
+    ("documents, merged", [2600, 130, 1, 64, 300], True, 32, 32, 32, 32, True),
+]
+
+
+@pytest.mark.parametrize("states", [True, False], ids=["states", "no states"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [128, 64])
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: c[0])
+def test_linattn_full_width(case, K, dtype, states):
+    x = prompt(case[:-1], dtype, K, 128, "mixed", seed=7, states=states)
+    n, cut = walks(x)
+    assert n >= 256 and cut == case[-1]
+    o, fin = gb.gdn_linattn_fwd(x["q"], x["k"], x["v"], x["decay"], x["scale"], meta=x["meta"],
+                                initial_state=x["S0"], output_final_state=states)
+    r = gb.gdn_linattn_bwd(x["q"], x["k"], x["v"], x["decay"], x["dout"], x["scale"], meta=x["meta"],
+                           initial_state=x["S0"], dht=x["dht"], want_dh0=states)
+    want, A = ({m: t.cpu() for m, t in on_gpu(x, absolute).items()} for absolute in (False, True))
+    within(o, want["o"], A["o"], 2.0 ** -14, o.dtype, "o")
+    for m, t in (("dq", "q"), ("dk", "k"), ("dv", "v")):
+        h = x[t].shape[-2]
+        within(r[m], ref.shared(want[m], h), ref.shared(A[m], h), 2.0 ** -14, r[m].dtype, m)
+    if states:
+        within(fin, want["fin"], A["fin"], 2.0 ** -17, fin.dtype, "final state")
+        within(r["dh0"], want["dh0"], A["dh0"], 2.0 ** -17, torch.float32, "dh0")
+
+
+# ------------------------------------------------------------------ beyond the last-level cache
+# Steps on more than 256 MB of states, and page calls that walk through more,
+# go around the caches, in kernels of their own.
+BEYOND = 2 ** 28
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K,V,N,H", [(128, 128, 131, 32), (64, 64, 515, 33), (64, 128, 260, 32), (128, 64, 260, 32)])
+def test_a_linear_step_around_the_caches(K, V, N, H, dtype):
+    assert N * H * K * V * 4 > BEYOND
+    gen = torch.Generator(DEV).manual_seed(K + V)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV)
+    q, k, v = (r(N, H, w).to(DT[dtype]) for w in (K, K, V))
+    decay, pool = -torch.rand(H, generator=gen, device=DEV), r(N + 2, H, K, V)
+    pages = torch.randperm(N + 2, generator=gen, device=DEV)[:N].to(torch.int32)
+    pages[0], pages[N - 1] = -1, N + 2       # no page
+    before = pool.clone()
+    o = gb.gdn_linattn_step(q, k, v, decay, pool, pages=pages)
+    assert not o[0].any() and not o[N - 1].any()
+    rest = torch.ones(N + 2, dtype=torch.bool, device=DEV)
+    rest[pages[1:-1].long()] = False
+    assert rest.sum() == 4 and torch.equal(pool[rest], before[rest])
+    for rows in torch.arange(1, N - 1).split(64):
+        rows = rows.to(DEV)
+        at = pages[rows].long()
+        args = (q[rows], k[rows], v[rows], decay, K ** -0.5, before[at])
+        want, S = ref.linattn_step(*args)
+        A, AS = ref.linattn_step(*args, absolute=True)
+        within(o[rows], want, A, 2.0 ** -16, o.dtype, "o")
+        within(pool[at], S, AS, 2.0 ** -21, torch.float32, "state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("per_key", [False, True])
+def test_a_delta_step_around_the_caches(per_key, dtype):
+    N, H = 133, 32
+    assert N * H * 128 * 128 * 4 > BEYOND
+    gen = torch.Generator(DEV).manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV)
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True)
+    q, k, v = (t.to(DT[dtype]) for t in (unit(r(N, 8, 128)), unit(r(N, 8, 128)), r(N, H, 128)))
+    g = -torch.rand(*((N, H, 128) if per_key else (N, H)), generator=gen, device=DEV)
+    beta = torch.rand(N, H, generator=gen, device=DEV).to(DT[dtype])
+    pool = r(N + 1, H, 128, 128)
+    pages = torch.randperm(N + 1, generator=gen, device=DEV)[:N].to(torch.int32)
+    pages[7] = -1
+    before = pool.clone()
+    o = gb.gdn_recurrent_step(q, k, v, g, beta, pool, pages=pages)
+    assert not o[7].any()
+    on = (pages >= 0).nonzero().flatten()
+    rest = torch.ones(N + 1, dtype=torch.bool, device=DEV)
+    rest[pages[on].long()] = False
+    assert torch.equal(pool[rest], before[rest])
+    for rows in on.split(48):
+        at = pages[rows].long()
+        args = (q[rows], k[rows], v[rows], g[rows], beta[rows], 128 ** -0.5, before[at])
+        want, S = ref.delta_step(*args)
+        A, AS = ref.delta_step(*args, absolute=True)
+        within(o[rows], want, A, 2.0 ** -15, o.dtype, "o")
+        within(pool[at], S, AS, 2.0 ** -16, torch.float32, "state")
+
+
+def large_pool(pages, page_bytes, layers=2):
+    """Every 4 bytes of a pool different."""
+    return torch.arange(layers * pages * page_bytes // 4, dtype=torch.int32, device=DEV).view(layers, pages, -1)
+
+
+def after(pool, copies):
+    want = pool.clone()
+    if copies:
+        s, d = (torch.tensor(x, device=DEV) for x in zip(*copies))
+        want[:, d] = pool[:, s]
+    return want
+
+
+@pytest.mark.parametrize("n,pages,page_bytes", [
+    (40, 70, 4 << 20), (200, 230, (1 << 20) + 16), (500, 600, (1 << 19) + 4096),      # around the caches
+    (6, 70, 4 << 20), (300, 600, 1 << 18)])                                             # few of a large pool: through them
+def test_forks_and_compactions_of_large_pools(n, pages, page_bytes):
+    gen = torch.Generator().manual_seed(n)
+    order = torch.randperm(pages, generator=gen).tolist()
+    table, spare = order[:n], order[n:n + 9]
+    parent = torch.randint(-1, n // 2, (n,), generator=gen).tolist()
+    table[2] = -1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    pool = large_pool(pages, page_bytes)
+    assert pool.nbytes > BEYOND
+    new, copies, left = ref.fork(table, parent, spare, pages)
+    want = after(pool, copies)
+    got, gleft = gb.gdn_pages_fork(pool, i32(table), i32(parent), spare=i32(spare))
+    assert got.tolist() == new and gleft.tolist() == left and torch.equal(pool, want)
+    new, moves, count = ref.compact(table, pages)
+    assert moves
+    want = after(pool, moves)
+    got, c = gb.gdn_pages_compact(pool, i32(table))
+    assert got.tolist() == new and c.tolist() == [count] and torch.equal(pool, want)
+
+
+def test_a_compaction_of_many_large_pages():
+    # more pages than one kernel's plan holds
+    pages, n = 1100, 700
+    gen = torch.Generator().manual_seed(1)
+    table = torch.randperm(pages, generator=gen)[:n].tolist()
+    pool = large_pool(pages, 1 << 18)
+    assert n * 2 * (1 << 18) > BEYOND
+    new, moves, count = ref.compact(table, pages)
+    want = after(pool, moves)
+    got, c = gb.gdn_pages_compact(pool, torch.tensor(table, dtype=torch.int32, device=DEV))
+    assert got.tolist() == new and c.tolist() == [count] and torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("n", [3, 60])      # through and around the caches
+def test_copies_of_large_pages(n):
+    src, dst = large_pool(80, (2 << 20) + 48), torch.zeros(2, 70, ((2 << 20) + 48) // 4, dtype=torch.int32, device=DEV)
+    assert src.nbytes > BEYOND
+    gen = torch.Generator().manual_seed(n)
+    d, s = torch.randperm(70, generator=gen)[:n].tolist(), torch.randint(0, 80, (n,), generator=gen).tolist()
+    s[1], d[2] = s[0], 70      # a page twice; none
+    want = dst.clone()
+    for a, b in zip(s, d):
+        if b < 70:
+            want[:, b] = src[:, a]
+    gb.gdn_pages_copy(dst, src, *(torch.tensor(x, dtype=torch.int32, device=DEV) for x in (d, s)))
+    assert torch.equal(dst, want)
