@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -155,8 +156,14 @@ void written(std::initializer_list<const Tensor*> tensors) {
         if (t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
-// A call launches on its tensors' device, whichever is current.
-using Guard = c10::DeviceGuard;
+// A call launches on its tensors' device, whichever is current. (Where it is
+// that one already, a c10::DeviceGuard would set it again at the end.)
+struct Guard {
+    c10::OptionalDeviceGuard other;
+    explicit Guard(c10::Device dev) {
+        if (c10::hip::current_device() != dev.index()) other.reset_device(dev);
+    }
+};
 
 hipStream_t stream_of(c10::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
