@@ -838,7 +838,8 @@ def gdn_linattn_fwd(q, k, v, decay, scale=None, *, meta: UnitMeta | None = None,
     e^decay[h] S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
 
     q [B,T,Hq,K], k [B,T,Hk,K], v [B,T,Hv,V], or packed [T,h,D] with meta
-    (make_meta); K and V are 64 or 128, bf16 or fp32. decay: fp32 [H], log
+    (make_meta); K and V are 64 or 128, bf16 or fp32, and all values finite
+    (one that is not spoils up to 31 tokens before it too). decay: fp32 [H], log
     decays <= 0; Hq, Hk and Hv divide H, head h reading head h // (H // Hx).
     Rows must be contiguous and 16-byte aligned; tokens and heads may be
     strided (views of a fused projection). initial_state: fp32 [units,H,K,V],
@@ -856,7 +857,7 @@ def gdn_linattn_bwd(q, k, v, decay, dout, scale=None, *, meta: UnitMeta | None =
     the inputs' dtype) and dht = dL/d(final state) or None. Returns a dict: dq,
     dk, dv shaped and typed like q, k, v (sums over the heads that share one)
     and dh0 = dL/d(initial state), fp32 [units,H,K,V], when wanted. decay is a
-    constant."""
+    constant. All values must be finite, as in gdn_linattn_fwd."""
     return (_NATIVE or _native()).linattn_bwd(q, k, v, decay, dout, scale, *_meta_args(meta), initial_state, dht,
                                               want_dh0, workspace)
 

@@ -15,10 +15,12 @@
 //
 // Products of bf16 inputs: bf16 MFMA, fp32 accumulation. Where a value
 // computed in fp32 meets a bf16 operand it is split into bf16 terms, not
-// rounded: two terms (16 bits) for what ends in o, whose result is rounded to
-// the output's type - the scores, S in q S, the decayed v that enters S - and
-// three (24 bits) for the decayed v where S itself is returned in fp32. fp32
-// inputs: fp32 MFMA.
+// rounded: two terms (16 bits) for what ends in o - the scores, S in q S, the
+// decayed v that enters S - and three (24 bits) for the decayed v where S
+// itself is returned in fp32. That is 8 bits more than a bf16 o keeps (its
+// error is that of one rounding: 0.00166 relative, as of an fp32 evaluation,
+// with 2 of 1000 values rounded to the other neighbour) and 8 fewer than an
+// fp32 o could. fp32 inputs: fp32 MFMA.
 //
 // A partial chunk fills the last rows of its tile: the factors that enter S
 // then stay those of a full chunk, and only d^{i+1} and d^C change.
@@ -80,9 +82,10 @@ __device__ __forceinline__ int xcd_deal(int b, int n, int each) {
 // The work of this workgroup. Where packed segments give some compute units a
 // second workgroup, which is dealt to them in the order of the first, the
 // longest ones come last of the first, so that they stay alone and the second
-// ones meet the shorter ones: a chunk of K = V = 128 takes a workgroup alone
-// 4.6 us (3.1 with a quarter of the chip at work), one of two 6.9 (T=32768
-// H=16 in 20 prompts: longest first throughout 218 us, like this 204).
+// ones meet the shorter ones: a chunk of K = V = 128 takes a workgroup alone on
+// its unit 4.2 us with all units at work (3.1 with a quarter of them, 2.9 with
+// a few), one of two 6.9 (T=32768 H=16 in 20 prompts: longest first throughout
+// 218 us, like this 204).
 __device__ __forceinline__ int work_of_block(const LaUnits& um, int each) {
     int b = blockIdx.x;
     const int n = gridDim.x;
@@ -198,11 +201,14 @@ struct Tile {
     static constexpr int EPU = 16 / sizeof(T);
     static constexpr int UNITS = W / EPU;
     static constexpr int RB = W * sizeof(T);   // bytes of a row
-    // A permutation of four row bits over the unit bits, in which the rows
-    // that are read together - 16 at one column, four at four neighbouring
-    // units - take all the banks: for bf16 the four are rows r .. r + 3, for
-    // fp32 rows r, r + 4, r + 8, r + 12; a 128-byte row is half the banks, so
-    // its lowest row bit needs no place.
+    // A permutation of four row bits over the unit bits, made to spread the
+    // rows that are read together - 16 at one column, four at four neighbouring
+    // units - over the banks. Not all of the walk's accesses are free of
+    // conflicts (20 packed prompts: 2.1e7 of la_main's 4.5e7 active LDS cycles
+    // are counted as such; of which accesses, tiles or scores, is not known).
+    // For bf16 the four are rows r .. r + 3, for fp32 rows r, r + 4, r + 8,
+    // r + 12; a 128-byte row is half the banks, so its lowest row bit needs no
+    // place.
     __device__ static constexpr int swizzle(int row) {
         const int lo = row & 3, hi = (row >> 2) & 3;
         if (UNITS < 16) return 4 * (lo >> 1) | hi;
@@ -556,8 +562,9 @@ __device__ __forceinline__ void value_frags(const char* tile, int tid, typename 
 // (B=16 T=4096 H=32: 485 us, 4.4 TB/s), with less the latency of one chunk's
 // chain - scores, S's two terms, q S, P v, k v^T - which two workgroups a unit
 // overlap: B=4 T=4096 H=16 81 us of 110 (the rest is the segments' states),
-// 20 prompts of 32768 tokens and 32 heads 280 us, 2.7 TB/s. fp32 MFMA bounds
-// fp32 (T=4096 H=16: 93 us). Eight waves a workgroup, deeper double buffers,
+// 20 prompts of 32768 tokens and 32 heads 280 us, 2.7 TB/s. The same chain
+// bounds fp32, whose MFMA alone would take half the time at a large product's
+// rate (T=4096 H=16: 46 of 92 us). Eight waves a workgroup, deeper double buffers,
 // fewer address instructions and other orders of the products gain nothing.
 // Two workgroups a compute unit (77 KiB of LDS each for K = V = 128): the q
 // and v tiles are free for the next chunk once the scores are written and

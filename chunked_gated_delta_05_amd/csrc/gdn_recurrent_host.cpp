@@ -87,8 +87,9 @@ int64_t segments(const gdn_linattn_desc* d, const LaUnits& u, int64_t seg) {
 }
 
 // About how long n segments of at most seg chunks take. One workgroup's chunk
-// is 2.9 us (fp32 7) and its sum of k v^T 1.5 (2.5); all units together do a
-// chunk in a 200th of that. The last segments to start leave units idle for
+// is 2.9 us (fp32 7) and its sum of k v^T 1.5 (2.5) with few at work; all units
+// together do a chunk in a 200th of that (each is slower then: 4.2 us, fp32
+// 12.2, one workgroup a unit). The last segments to start leave units idle for
 // about 0.6 of a segment. A cut costs a launch of 5 us, 4 more for a merge,
 // and its states, 64 KiB each for K = V = 128, about 6 TB/s. Whether to cut at
 // all is decided by it, which matters where a few chunks are walked before a

@@ -83,10 +83,14 @@ typedef struct {
  *   workspace      as for gdn_chunk_fwd (size query with NULL)
  * Products with bf16 inputs run on bf16 MFMA with fp32 accumulation; the
  * values computed on the way are split into two bf16 terms (scores and the
- * state, where they meet q and v) or three (decayed v, where it enters the
- * state), so o carries about 16 bits more than its rounding needs and the
+ * state, where they meet q and v; decayed v, where it enters the state of a
+ * segment that returns none) or three (decayed v elsewhere). Two terms hold 16
+ * bits: o is right to about 2^-16 of the sum of its absolute terms, 8 bits
+ * more than a bf16 o is rounded to and 8 fewer than an fp32 o holds; the same
+ * goes for the per-head gradients that are summed for shared heads. A returned
  * state keeps fp32 accuracy. fp32 inputs run on fp32 MFMA. Inputs must be
- * finite.
+ * finite: masked products are multiplied by zero, so a value that is not
+ * reaches o up to 31 tokens before it too.
  */
 gdn_status gdn_linattn_fwd(const gdn_linattn_desc* desc, const void* q, const void* k, const void* v,
                            const float* decay, const float* s_in, const int32_t* in_pages, float* s_out,

@@ -1,8 +1,8 @@
 // Host-side fuzz of the recurrent-state operators' C ABI under
 // AddressSanitizer and UndefinedBehaviorSanitizer: random descriptors,
 // offsets, strides, sizes and pointers. The launch functions are stubs that
-// check what the host code hands them: regions inside the workspace, segments
-// that cover the sequences. Input pointers are fake addresses that nothing may
+// check what the host code hands them: regions inside the workspace, a segment
+// at least for each sequence. Input pointers are fake addresses that nothing may
 // dereference. Exit status 0 when every call returned a declared status.
 #include <stdio.h>
 #include <stdlib.h>
