@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 from dataclasses import dataclass
 
@@ -935,3 +936,236 @@ def gdn_pages_compact(pool, table):
     ones, in place: pages below their number stay, the others move, in order,
     into the holes. Returns (new table [n], the number of pages in use [1])."""
     return (_NATIVE or _native()).pages_compact(pool, table)
+
+
+# ------------------------------------------------------------------ operators around the recurrent layers
+# (include/gdn_mixer.h), native like the above (csrc/gdn_mixer_torch.cpp).
+def _silu(activation):
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    return activation == "silu"
+
+
+def gdn_conv_fwd(x, weight, bias=None, *, activation=None, meta: UnitMeta | None = None, initial_state=None,
+                 initial_pages=None, output_final_state=False, final_out=None, final_pages=None, out=None):
+    """The short causal convolution of each channel over whole prompts: z_t =
+    bias + sum_j weight[:, j] x_{t-W+1+j}, y = z or (activation="silu") z
+    sigmoid(z).
+
+    x [B,T,D] or packed [T,D] with meta (make_meta), bf16 or fp32, D a multiple
+    of 8; tokens may be strided (a view of a fused projection), their rows
+    16-byte aligned. weight [D,W] with W of 2 to 4 and bias [D] of one type,
+    bf16 or fp32. initial_state: the W - 1 inputs in front of each sequence,
+    oldest first, in x's type, [units,W-1,D], or a pool [n_pages,W-1,D] with
+    initial_pages int32 [units] (-1: zeros). final_out likewise with final_pages
+    (-1: not written); it may be the pool that initial_state is. out: contiguous,
+    apart from the inputs. Returns (y, final state or None)."""
+    return (_NATIVE or _native()).conv_fwd(x, weight, bias, _silu(activation), *_meta_args(meta), initial_state,
+                                           initial_pages, output_final_state, final_out, final_pages, out)
+
+
+def gdn_conv_bwd(x, weight, bias, dout, *, activation=None, meta: UnitMeta | None = None, initial_state=None,
+                 dfinal=None, want_dinitial=True, workspace=None):
+    """Gradients of gdn_conv_fwd for dout = dL/dy and dfinal = dL/d(final state)
+    or None, both contiguous in x's type. Returns a dict: dx like x, dweight fp32
+    [D,W], dbias fp32 [D] where there is a bias, and dinitial [units,W-1,D] in
+    x's type when wanted."""
+    return (_NATIVE or _native()).conv_bwd(x, weight, bias, dout, _silu(activation), *_meta_args(meta), initial_state,
+                                           dfinal, want_dinitial, workspace)
+
+
+class CausalConv(torch.autograd.Function):
+    """gdn_conv_fwd and gdn_conv_bwd as one autograd op: (x, weight, bias,
+    initial_state, activation, meta) -> (y, final state). Second-order gradients
+    raise."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias=None, initial_state=None, activation=None, meta=None):
+        y, final = gdn_conv_fwd(x, weight, bias, activation=activation, meta=meta, initial_state=initial_state,
+                                output_final_state=True)
+        ctx.save_for_backward(x, weight, bias, initial_state)
+        ctx.activation, ctx.meta = activation, meta
+        ctx.set_materialize_grads(False)
+        return y, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfinal):
+        x, weight, bias, s0 = ctx.saved_tensors
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.to(x.dtype).contiguous()
+        r = gdn_conv_bwd(x, weight, bias, dy, activation=ctx.activation, meta=ctx.meta, initial_state=s0,
+                         dfinal=None if dfinal is None else dfinal.to(x.dtype).contiguous(),
+                         want_dinitial=s0 is not None)
+        return (r["dx"], r["dweight"].to(weight.dtype), None if bias is None else r["dbias"].to(bias.dtype),
+                r.get("dinitial"), None, None)
+
+
+def gdn_conv_step(x, weight, state, bias=None, *, activation=None, pages=None, out=None):
+    """One token of the short convolution for N sequences: x [N,D] (rows may be
+    strided); state: the pool [n_pages,W-1,D] in x's type, shifted in place;
+    pages: int32 [N], distinct (-1: no sequence, y = 0), or None (row n uses page
+    n). Returns y [N,D]."""
+    return (_NATIVE or _native()).conv_step(x, weight, state, bias, _silu(activation), pages, out)
+
+
+def gdn_scan_fwd(u, dt, A, B, C, skip=None, gate=None, *, dt_bias=None, dt_softplus=False,
+                 meta: UnitMeta | None = None, initial_state=None, initial_pages=None, output_final_state=False,
+                 final_out=None, final_pages=None, want_h=False, out=None, workspace=None):
+    """The selective state space scan over whole prompts. For channel d with S
+    states, in group d // (D // G), and t = dt + dt_bias, through softplus with
+    dt_softplus: h = e^{t A} h + t u B, y = C h + skip u, out = y or y gate
+    sigmoid(gate).
+
+    u, dt, gate [B,T,D] or packed [T,D] with meta, B and C [..,G,S], all bf16 or
+    all fp32 and finite; tokens may be strided, their rows 16-byte aligned. A
+    fp32 [D,S], S of 8, 16, 32 or 64; skip and dt_bias fp32 [D]; D / G a multiple
+    of 8. States fp32 [units,D,S] or pools [n_pages,D,S] with pages, as in
+    gdn_conv_fwd. Returns (out, final state or None, h or None): h is what
+    gdn_scan_bwd needs of the states."""
+    return (_NATIVE or _native()).scan_fwd(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, *_meta_args(meta),
+                                           initial_state, initial_pages, output_final_state, final_out, final_pages,
+                                           want_h, out, workspace)
+
+
+def gdn_scan_bwd(u, dt, A, B, C, skip, gate, dout, h, *, dt_bias=None, dt_softplus=False,
+                 meta: UnitMeta | None = None, dht=None, want_dh0=True, workspace=None):
+    """Gradients of gdn_scan_fwd for dout = dL/dout (contiguous, in u's type) and
+    dht = dL/d(final state) or None, with h from the same forward. Returns a
+    dict: du, ddt, dgate, dB, dC in u's type, dA, dskip, ddt_bias fp32 (of what
+    there is), and dh0 = dL/d(initial state), fp32 [units,D,S], when wanted."""
+    return (_NATIVE or _native()).scan_bwd(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, dout, h,
+                                           *_meta_args(meta), dht, want_dh0, workspace)
+
+
+class SelectiveScan(torch.autograd.Function):
+    """gdn_scan_fwd and gdn_scan_bwd as one autograd op: (u, dt, A, B, C, skip,
+    gate, dt_bias, initial_state, dt_softplus, meta) -> (out, final state).
+    Second-order gradients raise."""
+
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, skip=None, gate=None, dt_bias=None, initial_state=None, dt_softplus=False,
+                meta=None):
+        out, final, h = gdn_scan_fwd(u, dt, A, B, C, skip, gate, dt_bias=dt_bias, dt_softplus=dt_softplus, meta=meta,
+                                     initial_state=initial_state, output_final_state=True,
+                                     want_h=any(ctx.needs_input_grad))
+        ctx.save_for_backward(u, dt, A, B, C, skip, gate, dt_bias, h)
+        ctx.dt_softplus, ctx.meta, ctx.has_s0 = dt_softplus, meta, initial_state is not None
+        ctx.set_materialize_grads(False)
+        return out, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dfinal):
+        u, dt, A, B, C, skip, gate, dt_bias, h = ctx.saved_tensors
+        dout = torch.zeros(u.shape, dtype=u.dtype, device=u.device) if dout is None else dout.to(u.dtype).contiguous()
+        r = gdn_scan_bwd(u, dt, A, B, C, skip, gate, dout, h, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
+                         meta=ctx.meta, dht=None if dfinal is None else dfinal.contiguous(), want_dh0=ctx.has_s0)
+        return (*(r.get(n) for n in ("du", "ddt", "dA", "dB", "dC", "dskip", "dgate", "ddt_bias", "dh0")), None, None)
+
+
+def gdn_scan_step(u, dt, A, B, C, state, skip=None, gate=None, *, dt_bias=None, dt_softplus=False, pages=None,
+                  out=None):
+    """One token of the selective scan for N sequences, with the states updated
+    in place: u, dt, gate [N,D], B and C [N,G,S] (rows may be strided); state:
+    fp32 pool [n_pages,D,S]; the rest as in gdn_scan_fwd and gdn_conv_step.
+    Returns out [N,D]."""
+    return (_NATIVE or _native()).scan_step(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, state, pages, out)
+
+
+_NORMS = {None: 0, "rms": 1, "l2": 2}
+
+
+def _norm_code(norm):
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be None, 'rms' or 'l2', got {norm!r}")
+    return _NORMS[norm]
+
+
+def rotary_frequencies(width, base=10000.0, *, factor=1.0, scaling=None, original_length=None, slow=1.0, fast=4.0,
+                       device=None):
+    """Radians a token of the width / 2 pairs of a rotation, fp64, for
+    gdn_qk_rotary_fwd: base^(-2i / width), scaled for contexts `factor` times
+    longer than the original_length that a model was trained on. scaling:
+
+    None        as they are
+    "linear"    all slower by factor (positions interpolated)
+    "base"      base times factor^(width / (width - 2)): the fastest pair keeps
+                its frequency, the slowest becomes slower by factor
+    "by_turns"  pairs that turn more than `fast` times over original_length keep
+                their frequency, those below `slow` times become slower by
+                factor, with a linear blend between"""
+    if width < 2 or width % 2:
+        raise ValueError(f"the rotated width must be even and positive, got {width}")
+    if scaling not in (None, "linear", "base", "by_turns"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'by_turns', got {scaling!r}")
+    if factor <= 0 or base <= 0:
+        raise ValueError("factor and base must be positive")
+    if scaling == "base":
+        if width < 4:
+            raise ValueError("scaling by the base needs at least two pairs")
+        base = base * factor ** (width / (width - 2))
+    f = float(base) ** (-torch.arange(0, width, 2, dtype=torch.float64) / width)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_turns":
+        if original_length is None or not slow < fast:
+            raise ValueError("scaling by turns needs original_length and slow < fast")
+        turns = original_length * f / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    return f.to(device) if device is not None else f
+
+
+def gdn_qk_rotary_fwd(q, k, freqs=None, positions=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6,
+                      interleaved=False, amplitude=1.0, q_out=None, k_out=None):
+    """Norms of queries and keys for each head and their rotation by position,
+    in one pass. Every row x of D values becomes n = x weight / sqrt(mean x^2 +
+    eps) ("rms"), / sqrt(sum x^2 + eps) ("l2") or without a norm (None); then the
+    pairs (i, i + R/2), or (2i, 2i + 1) with interleaved, of its first R = 2
+    len(freqs) values turn by position * freqs[i] and grow by amplitude.
+
+    q [B,T,Hq,D] and k [B,T,Hk,D], or [T,h,D], bf16 or fp32, D a multiple of 8 up
+    to 256; rows contiguous and 16-byte aligned, tokens and heads may be strided.
+    freqs: fp64 [R/2], radians a token (rotary_frequencies), R a multiple of 8,
+    or None. positions: int32 or int64 [B,T] or [T]; None: a token's place in its
+    row of [B,T,..]. q_weight, k_weight: [D], bf16 or fp32. q_out and k_out:
+    contiguous; q_out may be a contiguous q, k_out a contiguous k. Returns (q,
+    k)."""
+    return (_NATIVE or _native()).rotary_fwd(q, k, freqs, positions, _norm_code(norm), q_weight, k_weight, eps,
+                                             interleaved, amplitude, q_out, k_out)
+
+
+def gdn_qk_rotary_bwd(q, k, freqs, positions, dq_out, dk_out, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6,
+                      interleaved=False, amplitude=1.0, workspace=None):
+    """Gradients of gdn_qk_rotary_fwd for dq_out and dk_out (contiguous, in q's
+    type); q and k are the forward's inputs. Returns a dict: dq, dk, and dq_weight
+    and dk_weight, fp32 [D], where there are weights. freqs is a constant."""
+    return (_NATIVE or _native()).rotary_bwd(q, k, freqs, positions, _norm_code(norm), q_weight, k_weight, eps,
+                                             interleaved, amplitude, dq_out, dk_out, workspace)
+
+
+class QKRotary(torch.autograd.Function):
+    """gdn_qk_rotary_fwd and gdn_qk_rotary_bwd as one autograd op: (q, k, freqs,
+    positions, q_weight, k_weight, norm, eps, interleaved, amplitude) -> (q, k).
+    Second-order gradients raise, and so do freqs that require grad."""
+
+    @staticmethod
+    def forward(ctx, q, k, freqs=None, positions=None, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
+                interleaved=False, amplitude=1.0):
+        ctx.options = dict(norm=norm, eps=eps, interleaved=interleaved, amplitude=amplitude)
+        ctx.save_for_backward(q, k, freqs, positions, q_weight, k_weight)
+        ctx.set_materialize_grads(False)
+        return gdn_qk_rotary_fwd(q, k, freqs, positions, q_weight=q_weight, k_weight=k_weight, **ctx.options)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        if ctx.needs_input_grad[2]:
+            raise NotImplementedError("QKRotary has no gradient for freqs: detach them")
+        q, k, freqs, positions, q_weight, k_weight = ctx.saved_tensors
+        full = lambda d, x: torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d is None else d.to(x.dtype).contiguous()
+        r = gdn_qk_rotary_bwd(q, k, freqs, positions, full(dq, q), full(dk, k), q_weight=q_weight, k_weight=k_weight,
+                              **ctx.options)
+        like = lambda d, w: None if w is None else d.to(w.dtype)
+        return (r["dq"], r["dk"], None, None, like(r.get("dq_weight"), q_weight), like(r.get("dk_weight"), k_weight),
+                None, None, None, None)

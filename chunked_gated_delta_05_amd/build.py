@@ -3,8 +3,8 @@
     python -m chunked_gated_delta_05_amd.build [-v]
 
 hipcc compiles the kernels and the host API into one shared library next to
-this file, and g++ the torch marshalling of the recurrent-state operators
-(_native.so). Packed FP32 instructions are disabled for all device code.
+this file, and g++ the torch marshalling of the recurrent-state operators and
+those around them (_native.so). Packed FP32 instructions are disabled for all device code.
 """
 from __future__ import annotations
 
@@ -23,6 +23,9 @@ SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_host.c
 # the recurrent-state operators of include/gdn_recurrent.h
 RECURRENT_HIP = ["gdn_linattn", "gdn_step", "gdn_pages"]
 RECURRENT_HOST = "gdn_recurrent_host"
+# the operators around them, include/gdn_mixer.h
+MIXER_HIP = ["gdn_conv", "gdn_scan", "gdn_rotary"]
+MIXER_HOST = "gdn_mixer_host"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
@@ -68,6 +71,14 @@ def build(verbose: bool = False) -> str:
     robjs.append(os.path.join(BUILD, RECURRENT_HOST + ".o"))
     _run([HIPCC, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__", *warn, *inc, "-I", "/opt/rocm/include",
           "-x", "c++", "-c", os.path.join(CSRC, RECURRENT_HOST + ".cpp"), "-o", robjs[-1]], verbose)
+    for name in MIXER_HIP:
+        robjs.append(os.path.join(BUILD, name + ".o"))
+        _run([HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+              *warn, *inc, "-c", os.path.join(CSRC, name + ".hip"), "-o", robjs[-1]], verbose)
+    robjs.append(os.path.join(BUILD, MIXER_HOST + ".o"))
+    _run([HIPCC, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__", *warn, *inc, "-I", "/opt/rocm/include",
+          "-x", "c++", "-c", os.path.join(CSRC, MIXER_HOST + ".cpp"), "-o", robjs[-1]], verbose)
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", kobj, hobj, nobj, bobj, *robjs, "-o", LIB + ".tmp"],
          verbose)
     os.replace(LIB + ".tmp", LIB)
@@ -76,8 +87,8 @@ def build(verbose: bool = False) -> str:
 
 
 def _build_native(inc, verbose):
-    """_native.so: torch marshalling of the recurrent-state operators (host
-    code; CPython's C API and torch's C++ headers)."""
+    """_native.so: torch marshalling of the recurrent-state operators and those
+    around them (host code; CPython's C API and torch's C++ headers)."""
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
 
@@ -86,7 +97,7 @@ def _build_native(inc, verbose):
     _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, *tinc,
           "-isystem", sysconfig.get_path("include"), "-isystem", "/opt/rocm/include",
-          os.path.join(CSRC, "gdn_torch.cpp"), "-o", NATIVE + ".tmp",
+          os.path.join(CSRC, "gdn_torch.cpp"), os.path.join(CSRC, "gdn_mixer_torch.cpp"), "-o", NATIVE + ".tmp",
           "-L" + HERE, "-l:libgdn.so", "-Wl,-rpath,$ORIGIN", *tlib, "-lc10", "-lc10_hip", "-ltorch_cpu",
           "-ltorch_python"], verbose)
     os.replace(NATIVE + ".tmp", NATIVE)
