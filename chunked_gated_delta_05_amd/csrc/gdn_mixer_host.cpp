@@ -41,6 +41,11 @@ bool flag_ok(int32_t f) { return f == 0 || f == 1; }
 
 int64_t elem_bytes(int32_t d) { return d == GDN_DTYPE_BF16 ? 2 : 4; }
 
+// token distances of less than this keep a tile's rows within 32-bit offsets
+constexpr int64_t kMaxStrideBytes = int64_t(1) << 24;
+
+bool stride_small(int64_t s, int32_t dtype) { return s * elem_bytes(dtype) < kMaxStrideBytes; }
+
 // a distance that keeps rows 16-byte aligned and n of them below 2^60 elements
 bool stride_ok(int64_t s, int64_t n, int32_t dtype) {
     const int64_t lim = int64_t(1) << 60;
@@ -97,6 +102,14 @@ gdn_status check_seqs(int32_t B, int32_t T, int32_t n_units, const int32_t* host
 int64_t pieces(const MxUnits& u, int64_t P) {
     if (u.dense) return int64_t(u.n_units) * (u.T > P ? (u.T + P - 1) / P : 1);
     return u.total / P + u.n_units;
+}
+
+// pieces of P tokens that there are
+int64_t segments(const MxUnits& u, const int32_t* host, int64_t P) {
+    if (u.dense) return pieces(u, P);
+    int64_t n = 0;
+    for (int32_t i = 0; i < u.n_units; ++i) n += (int64_t(host[i + 1]) - host[i] + P - 1) / P;
+    return n;
 }
 
 // false: more than a launch's numbers
@@ -231,6 +244,9 @@ gdn_status check_scan(const gdn_scan_desc* d, Scan* s) {
         !stride_ok(d->c_stride[0], total, d->dtype) || !stride_ok(d->b_stride[1], d->G, d->dtype) ||
         !stride_ok(d->c_stride[1], d->G, d->dtype))
         return GDN_ERR_INVALID;
+    if (!stride_small(d->u_stride, d->dtype) || !stride_small(d->dt_stride, d->dtype) ||
+        !stride_small(d->gate_stride, d->dtype) || !stride_small(d->D, d->dtype))
+        return GDN_ERR_UNSUPPORTED;
     memset(s, 0, sizeof(*s));
     ScanArgs& a = s->a;
     a.D = d->D;
@@ -245,19 +261,29 @@ gdn_status check_scan(const gdn_scan_desc* d, Scan* s) {
     memcpy(a.c_stride, d->c_stride, sizeof(a.c_stride));
     const int ch = gdn::scan_channels(d->S), per = d->D / d->G;
     a.blocks = (per + ch - 1) / ch;
+    a.bwd_blocks = (per + ch / 2 - 1) / (ch / 2);
     a.un = a.keep = q.un;
     if (!cut(&a.keep, gdn::SCAN_KEEP)) return GDN_ERR_UNSUPPORTED;
     if (a.keep.n_pieces > kMaxElems / d->S / d->D) return GDN_ERR_UNSUPPORTED;
-    // Segments: where the sequences' workgroups are fewer than the compute
-    // units, as many as give every unit two.
+    // Segments. A cut costs a second walk (summary and main take 0.7 and 1 of a
+    // whole walk's time) and two launches with a merge between, about 15 us or 130
+    // tokens of one workgroup. So nothing is cut unless one sequence takes longer,
+    // on a compute unit of its own, than both walks of everything on all 256
+    // (T=8192 in 6 documents, D=4096: 254 us cut, 331 whole; T=61 D=512: 9 and 19).
+    // Then there are as many segments as give every unit four workgroups (two:
+    // B=2 T=4096 D=4096 with gradients 792 us, four: 763, eight: 768), but none
+    // shorter than what the merge, which walks through them one by one, saves.
     const int64_t tile = gdn::SCAN_TILE, whole = (q.longest + tile - 1) / tile * tile;
-    const int64_t walks = int64_t(a.G) * a.blocks, groups = walks * q.un.n_units;
+    const int64_t walks = int64_t(a.G) * a.blocks;
     int64_t P = whole > 0 ? whole : tile;
-    if (groups < 256) {
-        P = (total * walks / 512 + tile - 1) / tile * tile;
-        if (P < tile) P = tile;
-        if (P > whole) P = whole;
-        if (P < tile) P = tile;
+    if (q.longest > 1.4 * double(total) * walks / 256 + 130) {
+        int64_t lo = ((int64_t)sqrt(0.44 * double(q.longest)) + tile) / tile * tile, hi = P;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2 / tile * tile;
+            if (segments(q.un, d->offsets_host, mid) * walks <= 1024) hi = mid;
+            else lo = mid + tile;
+        }
+        P = hi;
     }
     if (!cut(&a.un, P)) return GDN_ERR_UNSUPPORTED;
     a.cut = q.longest > P;
@@ -331,7 +357,8 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
     gdn_status st = check_scan(d, &s);
     if (st != GDN_OK) return st;
     ScanArgs& a = s.a;
-    const int64_t walks = int64_t(a.G) * a.blocks;
+    const int64_t walks = int64_t(a.G) * a.bwd_blocks;
+    if (a.un.n_pieces > kMaxThreads / 256 / walks) return GDN_ERR_UNSUPPORTED;
     if (a.un.total > kMaxElems / (walks * 2 * d->S) || a.un.total * d->G * (d->S / 2) > kMaxThreads) return GDN_ERR_UNSUPPORTED;
     const int64_t rows = int64_t(a.un.n_pieces) + gdn::row_sums_rows(a.un.n_pieces);
     const int64_t bc = align256(walks * a.un.total * 2 * d->S * 4), ap = align256(rows * d->D * (d->S + 2) * 4);

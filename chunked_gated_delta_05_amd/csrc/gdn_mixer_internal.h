@@ -63,7 +63,7 @@ struct ScanArgs {
     MxUnits keep;             // the same with P = SCAN_KEEP: rows of h
     int32_t cut;              // some sequence has more than one segment
     int32_t D, G, S, dtype, softplus, n_pages;
-    int32_t blocks;           // of channels in a group
+    int32_t blocks, bwd_blocks;   // of channels in a group; the backward's workgroups hold half as many
     const void *u, *dt, *gate, *b, *c;
     int64_t u_stride, dt_stride, gate_stride, b_stride[2], c_stride[2];
     const float *A, *skip, *dt_bias;
@@ -78,11 +78,11 @@ struct ScanArgs {
     const void* dout;
     void *du, *ddt, *dgate, *db, *dc;
     float *dA, *dskip, *ddt_bias;
-    float *bc_parts;          // [G * blocks][tokens][2][S]
+    float *bc_parts;          // [G * bwd_blocks][tokens][2][S]
     float *a_parts;           // [pieces][D (S + 2)]
 };
 // channels of a workgroup
-constexpr int scan_channels(int S) { return 1024 / S; }
+constexpr int scan_channels(int S) { return S == 8 ? 128 : 2048 / S; }
 hipError_t launch_scan_summary(const ScanArgs& a, bool reverse, hipStream_t s);
 hipError_t launch_scan_merge(const ScanArgs& a, bool reverse, hipStream_t s);
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s);

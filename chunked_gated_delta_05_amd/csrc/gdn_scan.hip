@@ -4,83 +4,121 @@
 // A state differs from every other in its decays, so nothing of the recurrence
 // is a matrix product: a token costs each state a product for the exponent, an
 // exponential, the update (two operations) and one for y. The prompts' kernels
-// are bound by vector issue, not by memory. The layout keeps everything else
-// off the vector units: a lane holds four states of one channel, S / 4 lanes a
-// channel, so that sums over states cross few lanes; what belongs to a token
-// and channel (the softplus, the products with u, the gate) is computed once,
-// by the thread that loads it, and read from LDS by the lanes that need it.
-// Long sequences of few channels are cut into segments, whose own states are
-// summed up first (summary), carried over (merge) and then entered with.
+// are bound by vector issue, not by memory: an exponential takes a SIMD 8.5
+// cycles a wave, a product or sum 2.6 (with two waves or more; 4.7 with one), an
+// exchange of lanes 4.2. The layout keeps everything else off the vector units:
+// a lane holds four states of two channels, S / 4 lanes a pair, so that sums
+// over states cross few lanes and B and C are read from LDS once for both; what
+// belongs to a token and channel (the softplus, the products with u, the gate)
+// is computed once, by the thread that loads it.
+// Sequences are cut into segments where their channels alone would not fill the
+// card, whose own states are summed up first (summary), carried over (merge) and
+// then entered with.
 #include "gdn_mixer_device.h"
 
 namespace gdn {
 
 namespace {
 
-constexpr int NT = 256;
-
-template <int S>
+constexpr int NT = 256;                            // threads where the states do not matter
+constexpr int FT = 16;                             // tokens of a tile
+constexpr int KC = 2;                              // channels of a lane, neighbours; one in the backward
+template <int S, int K = KC>
 struct Shape {
-    static constexpr int LPC = S / 4;              // lanes of a channel
-    static constexpr int CH = 1024 / S;            // channels of a workgroup
-    static constexpr int CPW = 64 / LPC;           // of a wave
+    static constexpr int LPC = S / 4;              // lanes of a channel pair
+    static constexpr int CH = scan_channels(S) * K / KC;   // channels of a workgroup
+    static constexpr int CPW = K * 64 / LPC;       // of a wave
     static constexpr int V = CH / 4;               // vectors of a token's channels
     static constexpr int SV = S / 4;
+    static constexpr int NW = CH / CPW;            // waves: 4, or 2 where they have many channels
+    static constexpr int NT = 64 * NW;
 };
+
+// A lane's channels and states
+template <int S, int K = KC>
+struct Lane {
+    int lane, wave, c, sl;      // c: first channel in the workgroup
+    bool mine;                  // the channels exist (they are of one vector of 8)
+    int d;                      // of the first
+    int64_t at;                 // of its states in a page; the second channel's follow S later
+    __device__ __forceinline__ Lane(int ch, int ch_end) {
+        lane = threadIdx.x & 63;
+        wave = threadIdx.x >> 6;
+        c = wave * Shape<S, K>::CPW + K * (lane / Shape<S, K>::LPC);
+        sl = lane % Shape<S, K>::LPC;
+        mine = ch + c < ch_end;
+        d = mine ? ch + c : ch_end - K;
+        at = (int64_t)d * S + 4 * sl;
+    }
+};
+__device__ __forceinline__ void load_states(f32x4 (&h)[KC], const float* p, int S) {
+#pragma unroll
+    for (int k = 0; k < KC; ++k) h[k] = *reinterpret_cast<const f32x4*>(p + k * S);
+}
+__device__ __forceinline__ void store_states(float* p, const f32x4 (&h)[KC], int S) {
+#pragma unroll
+    for (int k = 0; k < KC; ++k) *reinterpret_cast<f32x4*>(p + k * S) = h[k];
+}
 
 // Channels of this workgroup: [ch, ch_end) in group g
 struct Block {
     int g, ch, ch_end;
 };
-template <int S>
+template <typename Sh>
 __device__ __forceinline__ Block block_of(const ScanArgs& a, int b) {
-    const int g = b / a.blocks, per = a.D / a.G, ch = (b - g * a.blocks) * Shape<S>::CH;
+    const int per = a.D / a.G, blocks = (per + Sh::CH - 1) / Sh::CH, g = b / blocks, ch = (b - g * blocks) * Sh::CH;
     return {g, g * per + ch, (g + 1) * per};
 }
 
-// One tile's inputs in registers, on their way to LDS. A thread's channels are
-// the same in every tile; tokens and channels past the end are read from the
-// last ones and made to do nothing: dt = 0 is a decay of 1 and adds no input.
-template <typename T, int S, int TT, bool GRAD>
-struct Tile {
-    typedef Shape<S> Sh;
-    static constexpr int N = TT * Sh::V, NV = (N + NT - 1) / NT;         // vectors of u, dt, ..
-    static constexpr int NB = 2 * TT * Sh::SV, NBV = (NB + NT - 1) / NT; // of B and C together
-    typename Four<T>::raw u[NV], dt[NV], gate[NV], dout[GRAD ? NV : 1], bc[NBV];
+// Where a thread's vectors of a tile lie in a tensor [tokens][..]: a resource
+// over the tile's tokens below the piece's end, so that tokens past it read as
+// zero and are not written; 32-bit offsets made once, as a thread's channels
+// and rows are the same in every tile.
+template <typename T, typename Sh, int TT>
+struct Rows {
+    static constexpr int N = TT * Sh::V, NV = (N + Sh::NT - 1) / Sh::NT, STEP = Sh::NT / Sh::V;
+    const T* base;
+    int64_t stride;
+    uint32_t lane;
+    static __device__ __forceinline__ int row(int i) { return threadIdx.x / Sh::V + i * STEP; }
+    static __device__ __forceinline__ bool has(int i) { return N % Sh::NT == 0 || row(i) < TT; }
+    __device__ __forceinline__ Rows(const void* p, int64_t start, int64_t stride_, int ch)
+        : base(static_cast<const T*>(p) + start * stride_), stride(stride_),
+          lane((uint32_t)(row(0) * stride_ + ch) * (uint32_t)sizeof(T)) {}
+    __device__ __forceinline__ rsrc_t tile(int t0, int end, int D) const {
+        return make_rsrc(base + t0 * stride, (uint32_t)((min(TT, end - t0) - 1) * stride + D) * (uint32_t)sizeof(T));
+    }
+    __device__ __forceinline__ uint32_t bytes(int i) const { return (uint32_t)(i * STEP * stride) * (uint32_t)sizeof(T); }
+    __device__ __forceinline__ void load(typename Four<T>::raw (&x)[NV], int t0, int end, int D) const {
+        const rsrc_t r = tile(t0, end, D);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = buffer_load4<T>(r, lane, bytes(i));
+    }
+};
 
-    static __device__ __forceinline__ int row(int i) { return (threadIdx.x + i * NT) / Sh::V; }
-    static __device__ __forceinline__ bool has(int i) { return N % NT == 0 || threadIdx.x + i * NT < N; }
-
-    // tokens [t0, t0 + TT) of the sequence at start, of which those below end count
-    __device__ __forceinline__ void load(const ScanArgs& a, const Block& k, int64_t start, int t0, int end) {
-        const int cv = threadIdx.x % Sh::V;
-        const int ch = min(k.ch + 4 * cv, k.ch_end - 4);
+// A tile's B and C in registers, on their way to LDS as floats [2][TT][S / 4]
+template <typename T, typename Sh, int TT>
+struct States {
+    static constexpr int NB = 2 * TT * Sh::SV, NV = (NB + Sh::NT - 1) / Sh::NT;
+    typename Four<T>::raw x[NV];
+    __device__ __forceinline__ void load(const ScanArgs& a, int g, int64_t start, int t0, int end) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t t = start + min(t0 + row(i), end - 1);
-            u[i] = load4(static_cast<const T*>(a.u) + t * a.u_stride + ch);
-            dt[i] = load4(static_cast<const T*>(a.dt) + t * a.dt_stride + ch);
-            if (a.gate) gate[i] = load4(static_cast<const T*>(a.gate) + t * a.gate_stride + ch);
-            if constexpr (GRAD) dout[i] = load4(static_cast<const T*>(a.dout) + t * a.D + ch);
-        }
-#pragma unroll
-        for (int i = 0; i < NBV; ++i) {
-            const int j = min((int)threadIdx.x + i * NT, NB - 1), r = j % (NB / 2);
+            const int j = min((int)threadIdx.x + i * Sh::NT, NB - 1), r = j % (NB / 2);
             const int64_t t = start + min(t0 + r / Sh::SV, end - 1);
-            const bool is_c = j >= NB / 2;
-            const T* p = is_c ? static_cast<const T*>(a.c) + t * a.c_stride[0] + k.g * a.c_stride[1]
-                              : static_cast<const T*>(a.b) + t * a.b_stride[0] + k.g * a.b_stride[1];
-            bc[i] = load4(p + 4 * (r % Sh::SV));
+            const T* p = j >= NB / 2 ? static_cast<const T*>(a.c) + t * a.c_stride[0] + g * a.c_stride[1]
+                                     : static_cast<const T*>(a.b) + t * a.b_stride[0] + g * a.b_stride[1];
+            x[i] = load4(p + 4 * (r % Sh::SV));
         }
     }
-    // B and C as floats, [2][TT][S / 4]; zero past the end
-    __device__ __forceinline__ void put_bc(f32x4* at, int t0, int end) const {
+    // zero past the end
+    __device__ __forceinline__ void put(f32x4* at, int t0, int end) const {
 #pragma unroll
-        for (int i = 0; i < NBV; ++i) {
-            const int j = threadIdx.x + i * NT;
-            if (NB % NT != 0 && j >= NB) break;
-            const f32x4 x = Four<T>::wide(bc[i]);
-            at[j] = t0 + (j % (NB / 2)) / Sh::SV < end ? x : f32x4{0, 0, 0, 0};
+        for (int i = 0; i < NV; ++i) {
+            const int j = threadIdx.x + i * Sh::NT;
+            if (NB % Sh::NT != 0 && j >= NB) break;
+            const f32x4 v = Four<T>::wide(x[i]);
+            at[j] = t0 + (j % (NB / 2)) / Sh::SV < end ? v : f32x4{0, 0, 0, 0};
         }
     }
 };
@@ -99,101 +137,128 @@ __device__ __forceinline__ f32x4 step_sizes(f32x4 raw, int softplus) {
 
 // ------------------------------------------------------------------ prompts
 template <typename T, int S>
-__global__ __launch_bounds__(NT) void scan_fwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__(Shape<S>::NT, 2) void scan_fwd_kernel(ScanArgs a) {
     typedef Shape<S> Sh;
-    constexpr int TT = SCAN_TILE, G4 = Sh::LPC < 4 ? Sh::LPC : 4;
-    typedef Tile<T, S, TT, false> Tl;
-    __shared__ f32x2 xs[TT][Sh::CH];                 // dt, dt u
+    constexpr int TT = FT;
+    typedef Rows<T, Sh, TT> Rw;
+    __shared__ f32x4 xs[TT][Sh::CH / 2];             // dt, dt u of two channels
     __shared__ f32x4 bc[2 * TT * Sh::SV];
     __shared__ float ys[TT][Sh::CH + 4];
 
     const int nb = a.G * a.blocks;
-    const Block k = block_of<S>(a, blockIdx.x % nb);
+    const Block k = block_of<Sh>(a, blockIdx.x % nb);
     const int piece = blockIdx.x / nb;
     const Piece pc = piece_of(a.un, piece);
     if (pc.none) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = wave * Sh::CPW + lane / Sh::LPC, sl = lane % Sh::LPC;
-    const bool mine = k.ch + c < k.ch_end;
-    const int d = mine ? k.ch + c : k.ch_end - 1;
-    const int64_t at = (int64_t)d * S + 4 * sl, page_size = (int64_t)a.D * S;
-
-    const f32x4 A2 = *reinterpret_cast<const f32x4*>(a.A + at) * LOG2E;
-    f32x4 h = {0, 0, 0, 0};
+    const Lane<S> l(k.ch, k.ch_end);
+    const int64_t page_size = (int64_t)a.D * S;
+    f32x4 A2[KC], h[KC] = {};
+    load_states(A2, a.A + l.at, S);
+#pragma unroll
+    for (int i = 0; i < KC; ++i) A2[i] *= LOG2E;
     if (a.cut) {
-        h = *reinterpret_cast<const f32x4*>(a.slots + piece * page_size + at);
+        load_states(h, a.slots + piece * page_size + l.at, S);
     } else if (a.s_in) {
         const int64_t page = page_of(a.in_pages, a.n_pages, pc.unit);
-        if (page >= 0) h = *reinterpret_cast<const f32x4*>(a.s_in + page * page_size + at);
+        if (page >= 0) load_states(h, a.s_in + page * page_size + l.at, S);
     }
-    float* keep = a.h ? a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + at : nullptr;
+    float* keep = a.h ? a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + l.at : nullptr;
 
     const int cv = threadIdx.x % Sh::V;
     const bool cv_ok = k.ch + 4 * cv < k.ch_end;
     const int cch = min(k.ch + 4 * cv, k.ch_end - 4);
     const f32x4 bias = load_f4(a.dt_bias, cch), skip = load_f4(a.skip, cch);
-    T* out = static_cast<T*>(a.out) + cch;
+    const Rw ru(a.u, pc.seq.start, a.u_stride, cch), rt(a.dt, pc.seq.start, a.dt_stride, cch),
+        rg(a.gate, pc.seq.start, a.gate_stride, cch), ro(a.out, pc.seq.start, a.D, cch);
 
-    Tl tile;
-    if (pc.first < pc.end) tile.load(a, k, pc.seq.start, pc.first, pc.end);
+    typename Four<T>::raw u[Rw::NV], dt[Rw::NV], gate[Rw::NV] = {};
+    States<T, Sh, TT> st;
+    auto load = [&](int t0) {
+        ru.load(u, t0, pc.end, a.D);
+        rt.load(dt, t0, pc.end, a.D);
+        if (a.gate) rg.load(gate, t0, pc.end, a.D);
+        st.load(a, k.g, pc.seq.start, t0, pc.end);
+    };
+    if (pc.first < pc.end) load(pc.first);
     for (int t0 = pc.first; t0 < pc.end; t0 += TT) {
-        f32x4 u[Tl::NV], gate[Tl::NV];
+        typename Four<T>::raw own_u[Rw::NV], own_gate[Rw::NV];
 #pragma unroll
-        for (int i = 0; i < Tl::NV; ++i) {
-            u[i] = Four<T>::wide(tile.u[i]);
-            gate[i] = Four<T>::wide(tile.gate[i]);
-            f32x4 dt = step_sizes(Four<T>::wide(tile.dt[i]) + bias, a.softplus);
-            if (t0 + Tl::row(i) >= pc.end) dt = f32x4{0, 0, 0, 0};
-            if (Tl::has(i)) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) xs[Tl::row(i)][4 * cv + j] = f32x2{dt[j], dt[j] * u[i][j]};
+        for (int i = 0; i < Rw::NV; ++i) {
+            own_u[i] = u[i];
+            own_gate[i] = gate[i];
+            f32x4 t = step_sizes(Four<T>::wide(dt[i]) + bias, a.softplus);
+            if (t0 + Rw::row(i) >= pc.end) t = f32x4{0, 0, 0, 0};   // a decay of 1, no input
+            const f32x4 du = t * Four<T>::wide(u[i]);
+            if (Rw::has(i)) {
+                xs[Rw::row(i)][2 * cv] = f32x4{t[0], du[0], t[1], du[1]};
+                xs[Rw::row(i)][2 * cv + 1] = f32x4{t[2], du[2], t[3], du[3]};
             }
         }
-        tile.put_bc(bc, t0, pc.end);
+        st.put(bc, t0, pc.end);
         lds_barrier();
-        if (t0 + TT < pc.end) tile.load(a, k, pc.seq.start, t0 + TT, pc.end);
+        if (t0 + TT < pc.end) load(t0 + TT);
 
         const int n = min(TT, pc.end - t0);
-#pragma unroll 1
-        for (int q = 0; q < n; q += 8) {
-            if (keep && q % SCAN_KEEP == 0 && mine)
-                *reinterpret_cast<f32x4*>(keep + (t0 + q) / SCAN_KEEP * page_size) = h;
+        struct Step {
+            f32x4 x, b, c;
+        };
+        auto read = [&](Step (&s)[2], int t) {
 #pragma unroll
-            for (int r = 0; r < 8; r += G4) {
-                float got = 0.0f;
+            for (int e = 0; e < 2; ++e) s[e] = Step{xs[t + e][l.c / 2], bc[(t + e) * Sh::SV + l.sl], bc[(TT + t + e) * Sh::SV + l.sl]};
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto step = [&](const Step (&s)[2], int t) {
+            f32x4 y;
 #pragma unroll
-                for (int e = 0; e < G4; ++e) {
-                    const int t = q + r + e;
-                    const f32x2 x = xs[t][c];
-                    const f32x4 B = bc[t * Sh::SV + sl], C = bc[(TT + t) * Sh::SV + sl];
-                    float y = 0.0f;
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int i = 0; i < KC; ++i) {
+                    float sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        h[j] = fmaf(__builtin_amdgcn_exp2f(x[0] * A2[j]), h[j], x[1] * B[j]);
-                        y = j ? fmaf(C[j], h[j], y) : C[j] * h[j];
+                        h[i][j] = fmaf(__builtin_amdgcn_exp2f(s[e].x[2 * i] * A2[i][j]), h[i][j], s[e].x[2 * i + 1] * s[e].b[j]);
+                        sum = j ? fmaf(s[e].c[j], h[i][j], sum) : s[e].c[j] * h[i][j];
                     }
-                    y = lane_sum<Sh::LPC>(y);
-                    got = e == 0 || sl == e ? y : got;
+                    y[2 * e + i] = sum;
                 }
-                if (sl < G4) ys[q + r + sl][c] = got;
             }
+            const f32x2 r = four_sums<Sh::LPC>(y, l.lane);
+            if constexpr (Sh::LPC == 2) {
+                ys[t][l.c + l.sl] = r[0];
+                ys[t + 1][l.c + l.sl] = r[1];
+            } else {
+                ys[t + (l.lane >> 1 & 1)][l.c + (l.lane & 1)] = r[0];
+            }
+        };
+        static_assert(TT == SCAN_KEEP, "");
+        if (keep && l.mine) store_states(keep + t0 / TT * page_size, h, S);
+        // two steps' operands are on their way from LDS while two others run
+        Step even[2], odd[2];
+        read(even, 0);
+#pragma unroll 1
+        for (int q = 0; q < n; q += 4) {
+            read(odd, q + 2);
+            step(even, q);
+            read(even, min(q + 4, TT - 2));
+            step(odd, q + 2);
         }
         lds_barrier();
+        const rsrc_t out = ro.tile(t0, pc.end, a.D);
 #pragma unroll
-        for (int i = 0; i < Tl::NV; ++i) {
-            const int row = Tl::row(i);
-            if (!Tl::has(i) || !cv_ok || t0 + row >= pc.end) continue;
-            f32x4 y = *reinterpret_cast<const f32x4*>(&ys[row][4 * cv]) + skip * u[i];
+        for (int i = 0; i < Rw::NV; ++i) {
+            if (!Rw::has(i) || !cv_ok) continue;
+            f32x4 y = *reinterpret_cast<const f32x4*>(&ys[Rw::row(i)][4 * cv]) + skip * Four<T>::wide(own_u[i]);
             if (a.gate) {
+                const f32x4 g = Four<T>::wide(own_gate[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] *= gate[i][j] * sigmoid1(gate[i][j]);
+                for (int j = 0; j < 4; ++j) y[j] *= g[j] * sigmoid1(g[j]);
             }
-            store4(out + (pc.seq.start + t0 + row) * a.D, y);
+            buffer_store4<T>(out, ro.lane, ro.bytes(i), y);
         }
     }
-    if (a.s_out && pc.end == pc.seq.len && mine) {
+    if (a.s_out && pc.end == pc.seq.len && l.mine) {
         const int64_t page = page_of(a.out_pages, a.n_pages, pc.unit);
-        if (page >= 0) *reinterpret_cast<f32x4*>(a.s_out + page * page_size + at) = h;
+        if (page >= 0) store_states(a.s_out + page * page_size + l.at, h, S);
     }
 }
 
@@ -201,81 +266,114 @@ __global__ __launch_bounds__(NT) void scan_fwd_kernel(ScanArgs a) {
 // the gradient that it passes on to the token in front of it. The segment that
 // nothing follows needs neither.
 template <typename T, int S, bool REVERSE>
-__global__ __launch_bounds__(NT) void scan_summary_kernel(ScanArgs a) {
+__global__ __launch_bounds__(Shape<S>::NT, 2) void scan_summary_kernel(ScanArgs a) {
     typedef Shape<S> Sh;
-    constexpr int TT = SCAN_TILE;
-    typedef Tile<T, S, TT, REVERSE> Tl;
-    __shared__ f32x2 xs[TT][Sh::CH];                 // dt and dt u, or dy
+    constexpr int TT = FT;
+    typedef Rows<T, Sh, TT> Rw;
+    __shared__ f32x4 xs[TT][Sh::CH / 2];             // dt and dt u, or dy, of two channels
     __shared__ f32x4 bc[2 * TT * Sh::SV];
 
     const int nb = a.G * a.blocks;
-    const Block k = block_of<S>(a, blockIdx.x % nb);
+    const Block k = block_of<Sh>(a, blockIdx.x % nb);
     const int piece = blockIdx.x / nb;
     const Piece pc = piece_of(a.un, piece);
     if (pc.none || (REVERSE ? pc.first == 0 : pc.end == pc.seq.len)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = wave * Sh::CPW + lane / Sh::LPC, sl = lane % Sh::LPC;
-    const bool mine = k.ch + c < k.ch_end;
-    const int d = mine ? k.ch + c : k.ch_end - 1;
-    const int64_t at = (int64_t)d * S + 4 * sl, page_size = (int64_t)a.D * S;
-    const f32x4 A2 = *reinterpret_cast<const f32x4*>(a.A + at) * LOG2E;
-    f32x4 h = {0, 0, 0, 0};
-    float sum = 0.0f;
+    const Lane<S> l(k.ch, k.ch_end);
+    const int64_t page_size = (int64_t)a.D * S;
+    f32x4 A2[KC], h[KC] = {};
+    load_states(A2, a.A + l.at, S);
+#pragma unroll
+    for (int i = 0; i < KC; ++i) A2[i] *= LOG2E;
+    f32x4 sum = {0, 0, 0, 0};                        // of dt, of this thread's channels and rows
     const int cv = threadIdx.x % Sh::V;
     const int cch = min(k.ch + 4 * cv, k.ch_end - 4);
     const f32x4 bias = load_f4(a.dt_bias, cch);
 
-    Tl tile;
+    const Rw rx(REVERSE ? a.dout : a.u, pc.seq.start, REVERSE ? a.D : a.u_stride, cch),
+        rt(a.dt, pc.seq.start, a.dt_stride, cch), rg(a.gate, pc.seq.start, a.gate_stride, cch);
+    typename Four<T>::raw u[Rw::NV], dt[Rw::NV], gate[Rw::NV] = {};
+    States<T, Sh, TT> st;
     const int tiles = (pc.end - pc.first + TT - 1) / TT;
     auto first_of = [&](int i) { return pc.first + (REVERSE ? tiles - 1 - i : i) * TT; };
-    tile.load(a, k, pc.seq.start, first_of(0), pc.end);
+    auto load = [&](int t0) {
+        rx.load(u, t0, pc.end, a.D);
+        rt.load(dt, t0, pc.end, a.D);
+        if (REVERSE && a.gate) rg.load(gate, t0, pc.end, a.D);
+        st.load(a, k.g, pc.seq.start, t0, pc.end);
+    };
+    load(first_of(0));
     for (int it = 0; it < tiles; ++it) {
         const int t0 = first_of(it);
 #pragma unroll
-        for (int i = 0; i < Tl::NV; ++i) {
-            f32x4 dt = step_sizes(Four<T>::wide(tile.dt[i]) + bias, a.softplus);
-            f32x4 x;
+        for (int i = 0; i < Rw::NV; ++i) {
+            f32x4 t = step_sizes(Four<T>::wide(dt[i]) + bias, a.softplus);
+            if (t0 + Rw::row(i) >= pc.end || !Rw::has(i)) t = f32x4{0, 0, 0, 0};
+            sum += t;
+            f32x4 x = Four<T>::wide(u[i]);           // zero past the end
             if constexpr (REVERSE) {
-                x = Four<T>::wide(tile.dout[i]);
                 if (a.gate) {
-                    const f32x4 g = Four<T>::wide(tile.gate[i]);
+                    const f32x4 g = Four<T>::wide(gate[i]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] *= g[j] * sigmoid1(g[j]);
                 }
             } else {
-                x = Four<T>::wide(tile.u[i]) * dt;
+                x *= t;
             }
-            if (t0 + Tl::row(i) >= pc.end) dt = x = f32x4{0, 0, 0, 0};
-            if (Tl::has(i)) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) xs[Tl::row(i)][4 * cv + j] = f32x2{dt[j], x[j]};
+            if (Rw::has(i)) {
+                xs[Rw::row(i)][2 * cv] = f32x4{t[0], x[0], t[1], x[1]};
+                xs[Rw::row(i)][2 * cv + 1] = f32x4{t[2], x[2], t[3], x[3]};
             }
         }
-        tile.put_bc(bc, t0, pc.end);
+        st.put(bc, t0, pc.end);
         lds_barrier();
-        if (it + 1 < tiles) tile.load(a, k, pc.seq.start, first_of(it + 1), pc.end);
-        const int n = min(TT, pc.end - t0);
-#pragma unroll 1
-        for (int q = 0; q < n; q += 8) {
+        if (it + 1 < tiles) load(first_of(it + 1));
+        const int n = (min(TT, pc.end - t0) + 7) & ~7;
+        struct Step {
+            f32x4 x, b;
+        };
+        auto read = [&](Step (&s)[4], int q) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int t = REVERSE ? (n + 7) / 8 * 8 - 1 - q - e : q + e;
-                const f32x2 x = xs[t][c];
-                const f32x4 B = bc[((REVERSE ? TT : 0) + t) * Sh::SV + sl];
-                sum += x[0];
+            for (int e = 0; e < 4; ++e) {
+                const int t = REVERSE ? n - 1 - q - e : q + e;
+                s[e] = Step{xs[t][l.c / 2], bc[((REVERSE ? TT : 0) + t) * Sh::SV + l.sl]};
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto step = [&](const Step (&s)[4]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float e2 = __builtin_amdgcn_exp2f(x[0] * A2[j]);
-                    if constexpr (REVERSE) h[j] = e2 * fmaf(x[1], B[j], h[j]);
-                    else h[j] = fmaf(e2, h[j], x[1] * B[j]);
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int i = 0; i < KC; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float e2 = __builtin_amdgcn_exp2f(s[e].x[2 * i] * A2[i][j]);
+                        if constexpr (REVERSE) h[i][j] = e2 * fmaf(s[e].x[2 * i + 1], s[e].b[j], h[i][j]);
+                        else h[i][j] = fmaf(e2, h[i][j], s[e].x[2 * i + 1] * s[e].b[j]);
+                    }
                 }
             }
+        };
+        Step even[4], odd[4];
+        read(even, 0);
+#pragma unroll 1
+        for (int q = 0; q < n; q += 8) {
+            read(odd, q + 4);
+            step(even);
+            read(even, min(q + 8, n - 4));
+            step(odd);
         }
         lds_barrier();
     }
-    if (mine) {
-        *reinterpret_cast<f32x4*>(a.slots + piece * page_size + at) = h;
-        if (sl == 0) a.sums[(int64_t)piece * a.D + d] = sum;
+    if (l.mine) {
+        store_states(a.slots + piece * page_size + l.at, h, S);
+    }
+    f32x4* red = &xs[0][0];                          // nobody reads it any more
+    static_assert(sizeof(xs) >= Sh::NT * sizeof(f32x4), "");
+    red[threadIdx.x] = sum;
+    lds_barrier();
+    if (threadIdx.x < Sh::V && k.ch + 4 * cv < k.ch_end) {
+        for (int i = cv + Sh::V; i < Sh::NT; i += Sh::V) sum += red[i];
+        *reinterpret_cast<f32x4*>(a.sums + (int64_t)piece * a.D + cch) = sum;
     }
 }
 
@@ -318,47 +416,56 @@ __global__ __launch_bounds__(NT) void scan_merge_kernel(ScanArgs a, int blocks) 
 }
 
 // ------------------------------------------------------------------ gradients
-// A wave's sums over its channels of dB's and dC's terms (four states each in a
-// lane): every exchange halves the values, so 8 values over 16 channels take 16
-// operations. Where lane l's result belongs: value (l >> 5: dB, dC), state 4 sl
-// + 2 bit 3 + bit 4 of l; with S = 64 bit 3 is of sl, and there are two results.
+// dB and dC are sums over channels, which lie across lanes. Their terms of four
+// tokens (two vectors of four states a lane and token) go through LDS, where a
+// lane finds one vector's terms of eight channels: 2 sums for each element where
+// exchanges of lanes take 5 and the matrix unit, which holds up the vector units
+// in fp32, 64 cycles (B=2 T=4096 D=4096: 455 us, exchanges 750, products with
+// ones 670).
 template <int S>
-__device__ __forceinline__ f32x2 channel_sums(f32x4 b, f32x4 c, int lane) {
-    const float r0 = halves_sum(b[0], c[0]), r1 = halves_sum(b[1], c[1]);
-    const float r2 = halves_sum(b[2], c[2]), r3 = halves_sum(b[3], c[3]);
-    float q0 = rows_sum(r0, r1), q1 = rows_sum(r2, r3);
-    if constexpr (S <= 32) {
-        q0 += dpp<ROW_ROR8>(q0);
-        q1 += dpp<ROW_ROR8>(q1);
-        if constexpr (S <= 16) {
-            q0 += dpp<ROW_ROR4>(q0);
-            q1 += dpp<ROW_ROR4>(q1);
-        }
-        q0 = lane & 8 ? q1 : q0;
-        if constexpr (S == 8) q0 += dpp<QUAD_XOR2>(q0);
+struct ChannelSums {
+    static constexpr int LPC = S / 4, OUT = 8 * LPC;           // vectors that come out
+    static constexpr int SHARE = LPC < 8 ? 8 / LPC : 1;        // lanes of one of them
+    static constexpr int TERMS = LPC < 16 ? 8 : 4, ROUNDS = 8 / TERMS;
+    int first, turn;
+    // the terms are read in an order that keeps 16 neighbouring lanes on different banks
+    __device__ __forceinline__ ChannelSums(int lane) {
+        const int o = lane / SHARE, part = lane % SHARE;
+        first = o / LPC * 64 + part * 8 * LPC + o % LPC;
+        turn = LPC < 16 ? o / LPC % 2 * SHARE + part : 0;
     }
-    return f32x2{q0, q1};
-}
+    // p: this wave's vectors [token][dB, dC][lane]; out: [token][dB, dC][S / 4]
+    __device__ __forceinline__ void sum(const f32x4* p, f32x4* out, int lane) const {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i) s += p[first + r * (64 / LPC) * 64 + ((i + turn) & 7) * LPC];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = lane_sum<SHARE>(s[j]);
+            out[lane / SHARE + r * 64] = s;
+        }
+    }
+};
 
 template <typename T, int S>
-__global__ __launch_bounds__(NT) void scan_bwd_kernel(ScanArgs a) {
-    typedef Shape<S> Sh;
-    constexpr int TT = SCAN_KEEP, G4 = Sh::LPC < 4 ? Sh::LPC : 4;
-    typedef Tile<T, S, TT, true> Tl;
-    __shared__ f32x4 xs[TT][Sh::CH];                 // dt, dt u, dy
+__global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs a) {
+    typedef Shape<S, 1> Sh;
+    constexpr int TT = SCAN_KEEP;
+    typedef Rows<T, Sh, TT> Rw;
+    __shared__ __align__(16) f32x2 xs[TT][Sh::CH];   // dt, dt u
+    __shared__ __align__(16) float dys[TT][Sh::CH];
     __shared__ f32x4 bc[2 * TT * Sh::SV];
-    __shared__ float sums[3][TT][Sh::CH + 4];        // over states: B g, E h A, C h
-    __shared__ float parts[4][TT][2 * S];            // over a wave's channels: dB, dC
+    __shared__ __align__(16) float sums[3][TT][Sh::CH + 4];   // over states: B g, E h A, C h
+    __shared__ f32x4 parts[Sh::NW][TT][2 * Sh::SV];  // over a wave's channels: dB, dC
+    __shared__ f32x4 terms[Sh::NW][4][2][64];        // of four tokens, by lanes
 
-    const int nb = a.G * a.blocks, blk = blockIdx.x % nb;
-    const Block k = block_of<S>(a, blk);
+    const int nb = a.G * a.bwd_blocks, blk = blockIdx.x % nb;
+    const Block k = block_of<Sh>(a, blk);
     const int piece = blockIdx.x / nb;
     const Piece pc = piece_of(a.un, piece);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = wave * Sh::CPW + lane / Sh::LPC, sl = lane % Sh::LPC;
-    const bool mine = k.ch + c < k.ch_end;
-    const int d = mine ? k.ch + c : k.ch_end - 1;
-    const int64_t at = (int64_t)d * S + 4 * sl, page_size = (int64_t)a.D * S;
+    const Lane<S, 1> l(k.ch, k.ch_end);
+    const int64_t page_size = (int64_t)a.D * S;
     // this piece's part of dA, and of dskip and ddt_bias
     float* part = a.a_parts + piece * ((int64_t)a.D * (S + 2));
     const int cv = threadIdx.x % Sh::V;
@@ -367,156 +474,184 @@ __global__ __launch_bounds__(NT) void scan_bwd_kernel(ScanArgs a) {
     f32x4 dA = {0, 0, 0, 0}, dskip = {0, 0, 0, 0}, dbias = {0, 0, 0, 0};
 
     if (!pc.none) {
-        const f32x4 A2 = *reinterpret_cast<const f32x4*>(a.A + at) * LOG2E;
+        const f32x4 A2 = *reinterpret_cast<const f32x4*>(a.A + l.at) * LOG2E;
         f32x4 E = {0, 0, 0, 0};
-        if (a.cut) E = *reinterpret_cast<const f32x4*>(a.slots + piece * page_size + at);
-        else if (a.s_in) E = *reinterpret_cast<const f32x4*>(a.s_in + pc.unit * page_size + at);
-        const float* keep = a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + at;
+        if (a.cut) E = *reinterpret_cast<const f32x4*>(a.slots + piece * page_size + l.at);
+        else if (a.s_in) E = *reinterpret_cast<const f32x4*>(a.s_in + pc.unit * page_size + l.at);
+        const float* keep = a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + l.at;
         const f32x4 bias = load_f4(a.dt_bias, cch), skip = load_f4(a.skip, cch);
+        const ChannelSums<S> channels(l.lane);
 
-        Tl tile;
+        const Rw ru(a.u, pc.seq.start, a.u_stride, cch), rt(a.dt, pc.seq.start, a.dt_stride, cch),
+            rg(a.gate, pc.seq.start, a.gate_stride, cch), rd(a.dout, pc.seq.start, a.D, cch);
+        typename Four<T>::raw u[Rw::NV], dt[Rw::NV], gate[Rw::NV] = {}, dout[Rw::NV];
+        States<T, Sh, TT> st;
         f32x4 entry = {0, 0, 0, 0};
         auto load = [&](int t0) {
-            tile.load(a, k, pc.seq.start, t0, pc.end);
+            ru.load(u, t0, pc.end, a.D);
+            rt.load(dt, t0, pc.end, a.D);
+            rd.load(dout, t0, pc.end, a.D);
+            if (a.gate) rg.load(gate, t0, pc.end, a.D);
+            st.load(a, k.g, pc.seq.start, t0, pc.end);
             entry = *reinterpret_cast<const f32x4*>(keep + t0 / TT * page_size);
         };
         const int last = pc.first + (pc.end - pc.first - 1) / TT * TT;
         if (pc.first < pc.end) load(last);
         for (int t0 = last; t0 >= pc.first && pc.first < pc.end; t0 -= TT) {
-            f32x4 u[Tl::NV], dt[Tl::NV], raw[Tl::NV], gate[Tl::NV], dout[Tl::NV], dy[Tl::NV];
+            typename Four<T>::raw own_u[Rw::NV], own_dt[Rw::NV], own_gate[Rw::NV], own_dout[Rw::NV];
 #pragma unroll
-            for (int i = 0; i < Tl::NV; ++i) {
-                u[i] = Four<T>::wide(tile.u[i]);
-                raw[i] = Four<T>::wide(tile.dt[i]) + bias;
-                dt[i] = step_sizes(raw[i], a.softplus);
-                dy[i] = dout[i] = Four<T>::wide(tile.dout[i]);
+            for (int i = 0; i < Rw::NV; ++i) {
+                own_u[i] = u[i];
+                own_dt[i] = dt[i];
+                own_gate[i] = gate[i];
+                own_dout[i] = dout[i];
+                f32x4 t = step_sizes(Four<T>::wide(dt[i]) + bias, a.softplus);
+                f32x4 dy = Four<T>::wide(dout[i]);   // zero past the end
                 if (a.gate) {
-                    gate[i] = Four<T>::wide(tile.gate[i]);
+                    const f32x4 g = Four<T>::wide(gate[i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dy[i][j] *= gate[i][j] * sigmoid1(gate[i][j]);
+                    for (int j = 0; j < 4; ++j) dy[j] *= g[j] * sigmoid1(g[j]);
                 }
-                if (t0 + Tl::row(i) >= pc.end || !cv_ok) dt[i] = dy[i] = f32x4{0, 0, 0, 0};
-                if (Tl::has(i)) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        xs[Tl::row(i)][4 * cv + j] = f32x4{dt[i][j], dt[i][j] * u[i][j], dy[i][j], 0.0f};
+                if (t0 + Rw::row(i) >= pc.end || !cv_ok) t = dy = f32x4{0, 0, 0, 0};
+                const f32x4 du = t * Four<T>::wide(u[i]);
+                if (Rw::has(i)) {
+                    const int row = Rw::row(i);
+                    *reinterpret_cast<f32x4*>(&xs[row][4 * cv]) = f32x4{t[0], du[0], t[1], du[1]};
+                    *reinterpret_cast<f32x4*>(&xs[row][4 * cv + 2]) = f32x4{t[2], du[2], t[3], du[3]};
+                    *reinterpret_cast<f32x4*>(&dys[row][4 * cv]) = dy;
                 }
             }
-            tile.put_bc(bc, t0, pc.end);
+            st.put(bc, t0, pc.end);
             const f32x4 h0 = entry;
             lds_barrier();
             if (t0 > pc.first) load(t0 - TT);
 
-            // the states of the tile once more
+            // the states of the tile once more, and the decays
             f32x4 h[TT], ea[TT];
 #pragma unroll
-            for (int t = 0; t < TT; t += G4) {
-                float got = 0.0f;
+            for (int t = 0; t < TT; t += 4) {
+                f32x4 y;
 #pragma unroll
-                for (int e = 0; e < G4; ++e) {
-                    const f32x4 x = xs[t + e][c];
-                    const f32x4 B = bc[(t + e) * Sh::SV + sl], C = bc[(TT + t + e) * Sh::SV + sl];
-                    float y = 0.0f;
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 x = xs[t + e][l.c];
+                    const f32x4 B = bc[(t + e) * Sh::SV + l.sl], C = bc[(TT + t + e) * Sh::SV + l.sl];
+                    float s = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         ea[t + e][j] = __builtin_amdgcn_exp2f(x[0] * A2[j]);
-                        h[t + e][j] = fmaf(ea[t + e][j], t + e ? h[t + e - 1][j] : h0[j], x[1] * B[j]);
-                        y = j ? fmaf(C[j], h[t + e][j], y) : C[j] * h[t + e][j];
+                        const float now = fmaf(ea[t + e][j], t + e ? h[t + e - 1][j] : h0[j], x[1] * B[j]);
+                        h[t + e][j] = now;
+                        s = j ? fmaf(C[j], now, s) : C[j] * now;
                     }
-                    if (a.gate) {
-                        y = lane_sum<Sh::LPC>(y);
-                        got = e == 0 || sl == e ? y : got;
-                    }
+                    y[e] = s;
                 }
-                if (a.gate && sl < G4) sums[2][t + sl][c] = got;
+                const f32x2 r = four_sums<Sh::LPC>(y, l.lane);
+                sums[2][t + (l.lane & (Sh::LPC == 2 ? 1 : 3))][l.c] = r[0];
+                if constexpr (Sh::LPC == 2) sums[2][t + 2 + l.sl][l.c] = r[1];
+                __builtin_amdgcn_sched_barrier(0);
             }
             // and their gradients, backwards
 #pragma unroll
-            for (int t = TT - G4; t >= 0; t -= G4) {
-                float gu = 0.0f, gt = 0.0f;
+            for (int t = TT - 4; t >= 0; t -= 4) {
+                f32x4 su, sa;
 #pragma unroll
-                for (int e = G4 - 1; e >= 0; --e) {
-                    const f32x4 x = xs[t + e][c];
-                    const f32x4 B = bc[(t + e) * Sh::SV + sl], C = bc[(TT + t + e) * Sh::SV + sl];
+                for (int e = 3; e >= 0; --e) {
+                    const int n = t + e;
+                    const f32x2 x = xs[n][l.c];
+                    const float dy = dys[n][l.c];
+                    const f32x4 B = bc[n * Sh::SV + l.sl], C = bc[(TT + n) * Sh::SV + l.sl];
                     f32x4 pb, pcv;
-                    float su = 0.0f, st = 0.0f;
+                    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float g = fmaf(C[j], x[2], E[j]);
+                        const float g = fmaf(C[j], dy, E[j]);
                         pb[j] = x[1] * g;
-                        pcv[j] = x[2] * h[t + e][j];
-                        su = j ? fmaf(B[j], g, su) : B[j] * g;
-                        E[j] = ea[t + e][j] * g;
-                        const float w = E[j] * (t + e ? h[t + e - 1][j] : h0[j]);
-                        st = j ? fmaf(w, A2[j], st) : w * A2[j];
+                        pcv[j] = dy * h[n][j];
+                        s0 = j ? fmaf(B[j], g, s0) : B[j] * g;
+                        E[j] = ea[n][j] * g;
+                        const float w = E[j] * (n ? h[n - 1][j] : h0[j]);
+                        s1 = j ? fmaf(w, A2[j], s1) : w * A2[j];
                         dA[j] = fmaf(w, x[0], dA[j]);
                     }
-                    su = lane_sum<Sh::LPC>(su);
-                    st = lane_sum<Sh::LPC>(st);
-                    gu = e == G4 - 1 || sl == e ? su : gu;
-                    gt = e == G4 - 1 || sl == e ? st : gt;
-                    const f32x2 r = channel_sums<S>(pb, pcv, lane);
-                    float* p = &parts[wave][t + e][(lane >> 5) * S + 4 * sl + ((lane >> 4) & 1)];
-                    if constexpr (S == 64) {
-                        p[0] = r[0];
-                        p[2] = r[1];
-                    } else {
-                        p[(lane >> 3 & 1) * 2] = r[0];
-                    }
+                    terms[l.wave][e][0][l.lane] = pb;
+                    terms[l.wave][e][1][l.lane] = pcv;
+                    su[e] = s0;
+                    sa[e] = s1;
                 }
-                if (sl < G4) {
-                    sums[0][t + sl][c] = gu;
-                    sums[1][t + sl][c] = gt;
+                __builtin_amdgcn_wave_barrier();     // a wave's LDS accesses keep their order
+                channels.sum(&terms[l.wave][0][0][0], &parts[l.wave][t][0], l.lane);
+                __builtin_amdgcn_wave_barrier();
+                const f32x2 r0 = four_sums<Sh::LPC>(su, l.lane), r1 = four_sums<Sh::LPC>(sa, l.lane);
+                sums[0][t + (l.lane & (Sh::LPC == 2 ? 1 : 3))][l.c] = r0[0];
+                sums[1][t + (l.lane & (Sh::LPC == 2 ? 1 : 3))][l.c] = r1[0];
+                if constexpr (Sh::LPC == 2) {
+                    sums[0][t + 2 + l.sl][l.c] = r0[1];
+                    sums[1][t + 2 + l.sl][l.c] = r1[1];
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
             lds_barrier();
             // dB and dC of this workgroup's channels
             const int n = min(TT, pc.end - t0);
-            for (int i = threadIdx.x; i < n * (2 * S / 4); i += NT) {
-                const f32x4* p = reinterpret_cast<const f32x4*>(&parts[0][0][0]) + i;
-                constexpr int W = TT * 2 * S / 4;
-                const f32x4 r = (p[0] + p[W]) + (p[2 * W] + p[3 * W]);
+            for (int i = threadIdx.x; i < n * 2 * Sh::SV; i += Sh::NT) {
+                const f32x4* p = &parts[0][0][0] + i;
+                constexpr int W = TT * 2 * Sh::SV;
+                f32x4 r = p[0] + p[W];
+                if constexpr (Sh::NW == 4) r += p[2 * W] + p[3 * W];
                 reinterpret_cast<f32x4*>(a.bc_parts + ((int64_t)blk * a.un.total + pc.seq.start + t0) * (2 * S))[i] = r;
             }
+            const Rw ro(a.du, pc.seq.start, a.D, cch);
+            const rsrc_t du_out = ro.tile(t0, pc.end, a.D), ddt_out = Rw(a.ddt, pc.seq.start, a.D, cch).tile(t0, pc.end, a.D),
+                         dgate_out = Rw(a.dgate, pc.seq.start, a.D, cch).tile(t0, pc.end, a.D);
 #pragma unroll
-            for (int i = 0; i < Tl::NV; ++i) {
-                const int row = Tl::row(i);
-                if (!Tl::has(i) || !cv_ok || t0 + row >= pc.end) continue;
+            for (int i = 0; i < Rw::NV; ++i) {
+                const int row = Rw::row(i);
+                if (!Rw::has(i) || !cv_ok) continue;
+                const f32x4 uu = Four<T>::wide(own_u[i]);    // zero past the end, as are dt, dy and dout
+                const f32x4 x0 = *reinterpret_cast<const f32x4*>(&xs[row][4 * cv]),
+                            x1 = *reinterpret_cast<const f32x4*>(&xs[row][4 * cv + 2]), t = {x0[0], x0[2], x1[0], x1[2]};
+                const f32x4 dy = *reinterpret_cast<const f32x4*>(&dys[row][4 * cv]);
                 const f32x4 gu = *reinterpret_cast<const f32x4*>(&sums[0][row][4 * cv]);
                 const f32x4 gt = *reinterpret_cast<const f32x4*>(&sums[1][row][4 * cv]) * LN2;
-                const int64_t o = (pc.seq.start + t0 + row) * a.D + cch;
-                f32x4 ddt = gu * u[i] + gt;
+                f32x4 ddt = gu * uu + gt;
                 if (a.softplus) {
+                    const f32x4 raw = Four<T>::wide(own_dt[i]) + bias;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) ddt[j] *= sigmoid1(raw[i][j]);
+                    for (int j = 0; j < 4; ++j) ddt[j] *= sigmoid1(raw[j]);
                 }
-                store4(static_cast<T*>(a.du) + o, dt[i] * gu + skip * dy[i]);
-                store4(static_cast<T*>(a.ddt) + o, ddt);
-                dskip += dy[i] * u[i];
-                dbias += ddt;
+                buffer_store4<T>(du_out, ro.lane, ro.bytes(i), t * gu + skip * dy);
+                buffer_store4<T>(ddt_out, ro.lane, ro.bytes(i), ddt);
+                dskip += dy * uu;
+                if (t0 + row < pc.end) dbias += ddt;
                 if (a.gate) {
-                    f32x4 y = *reinterpret_cast<const f32x4*>(&sums[2][row][4 * cv]) + skip * u[i];
+                    const f32x4 g = Four<T>::wide(own_gate[i]), d = Four<T>::wide(own_dout[i]);
+                    f32x4 y = *reinterpret_cast<const f32x4*>(&sums[2][row][4 * cv]) + skip * uu;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] *= dout[i][j] * silu_slope(gate[i][j], sigmoid1(gate[i][j]));
-                    store4(static_cast<T*>(a.dgate) + o, y);
+                    for (int j = 0; j < 4; ++j) y[j] *= d[j] * silu_slope(g[j], sigmoid1(g[j]));
+                    buffer_store4<T>(dgate_out, ro.lane, ro.bytes(i), y);
                 }
             }
+            lds_barrier();
         }
-        if (a.s_out && pc.first == 0 && mine) *reinterpret_cast<f32x4*>(a.s_out + pc.unit * page_size + at) = E;
+        if (a.s_out && pc.first == 0 && l.mine) *reinterpret_cast<f32x4*>(a.s_out + pc.unit * page_size + l.at) = E;
     }
     // this piece's sums over its tokens
-    if (mine) *reinterpret_cast<f32x4*>(part + at) = dA;
+    if (l.mine) *reinterpret_cast<f32x4*>(part + l.at) = dA;
     lds_barrier();
-    f32x4(*red)[NT] = reinterpret_cast<f32x4(*)[NT]>(S == 8 ? &sums[0][0][0] : &parts[0][0][0]);
-    static_assert((S == 8 ? sizeof(sums) : sizeof(parts)) >= 2 * NT * sizeof(f32x4), "");
-    red[0][threadIdx.x] = dskip;
-    red[1][threadIdx.x] = dbias;
-    lds_barrier();
-    if (threadIdx.x < 2 * Sh::V && cv_ok) {
-        const f32x4* p = red[threadIdx.x / Sh::V] + cv;
-        f32x4 s = p[0];
-        for (int i = Sh::V; i < NT; i += Sh::V) s += p[i];
-        *reinterpret_cast<f32x4*>(part + page_size + (threadIdx.x / Sh::V) * a.D + cch) = s;
+    typedef f32x4 Red[Sh::NT];
+    float* room = S == 64 ? reinterpret_cast<float*>(&parts[0][0][0]) : &sums[0][0][0];
+    Red* red = reinterpret_cast<Red*>(room);
+    static_assert((S == 64 ? sizeof(parts) : sizeof(sums)) >= sizeof(Red), "");
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        red[0][threadIdx.x] = which ? dbias : dskip;
+        lds_barrier();
+        if (threadIdx.x < Sh::V && cv_ok) {
+            f32x4 s = red[0][cv];
+            for (int i = cv + Sh::V; i < Sh::NT; i += Sh::V) s += red[0][i];
+            *reinterpret_cast<f32x4*>(part + page_size + which * a.D + cch) = s;
+        }
+        lds_barrier();
     }
 }
 
@@ -528,11 +663,11 @@ __global__ __launch_bounds__(NT) void scan_bc_kernel(ScanArgs a) {
     if (rows >= a.un.total * a.G) return;
     const int64_t t = rows / a.G;
     const int g = (int)(rows % a.G), v = (int)(i % per);
-    const f32x4* p = reinterpret_cast<const f32x4*>(a.bc_parts) + ((int64_t)g * a.blocks * a.un.total + t) * per + v;
+    const f32x4* p = reinterpret_cast<const f32x4*>(a.bc_parts) + ((int64_t)g * a.bwd_blocks * a.un.total + t) * per + v;
     const int64_t step = a.un.total * per;
     f32x4 s = {0, 0, 0, 0};
 #pragma unroll 8
-    for (int b = 0; b < a.blocks; ++b) s += p[b * step];
+    for (int b = 0; b < a.bwd_blocks; ++b) s += p[b * step];
     T* o = static_cast<T*>(v < per / 2 ? a.db : a.dc);
     store4(o + rows * a.S + 4 * (v % (per / 2)), s);
 }
@@ -612,8 +747,8 @@ unsigned grid_of(const ScanArgs& a) { return (unsigned)((int64_t)a.un.n_pieces *
 
 hipError_t launch_scan_summary(const ScanArgs& a, bool reverse, hipStream_t s) {
     return by_type(a.dtype, a.S, [&](auto t, auto n) {
-        if (reverse) scan_summary_kernel<decltype(t), n(), true><<<grid_of(a), NT, 0, s>>>(a);
-        else scan_summary_kernel<decltype(t), n(), false><<<grid_of(a), NT, 0, s>>>(a);
+        if (reverse) scan_summary_kernel<decltype(t), n(), true><<<grid_of(a), Shape<n()>::NT, 0, s>>>(a);
+        else scan_summary_kernel<decltype(t), n(), false><<<grid_of(a), Shape<n()>::NT, 0, s>>>(a);
     });
 }
 
@@ -627,12 +762,13 @@ hipError_t launch_scan_merge(const ScanArgs& a, bool reverse, hipStream_t s) {
 
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) {
     return by_type(a.dtype, a.S,
-                   [&](auto t, auto n) { scan_fwd_kernel<decltype(t), n()><<<grid_of(a), NT, 0, s>>>(a); });
+                   [&](auto t, auto n) { scan_fwd_kernel<decltype(t), n()><<<grid_of(a), Shape<n()>::NT, 0, s>>>(a); });
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) {
+    const unsigned grid = (unsigned)((int64_t)a.un.n_pieces * a.G * a.bwd_blocks);
     const hipError_t e = by_type(
-        a.dtype, a.S, [&](auto t, auto n) { scan_bwd_kernel<decltype(t), n()><<<grid_of(a), NT, 0, s>>>(a); });
+        a.dtype, a.S, [&](auto t, auto n) { scan_bwd_kernel<decltype(t), n()><<<grid, Shape<n(), 1>::NT, 0, s>>>(a); });
     if (e != hipSuccess) return e;
     const unsigned bc = (unsigned)((a.un.total * a.G * (2 * a.S / 4) + NT - 1) / NT);
     if (bc > 0) {

@@ -17,7 +17,8 @@
  * gdn_status; a page number outside [0, n_pages) means "no page". Outputs are
  * apart from the inputs and from each other unless said otherwise. dtype is
  * GDN_DTYPE_F32 or GDN_DTYPE_BF16. Work that a launch cannot hold (2^32 threads)
- * is GDN_ERR_UNSUPPORTED, and so is a token stride of 2^24 bytes or more.
+ * is GDN_ERR_UNSUPPORTED, and so are token strides of 2^24 bytes or more in a
+ * scan.
  *
  * Sequences are the B rows of T tokens (n_units = 0) or packed documents of
  * one row, offsets as in gdn_desc (none is empty).
