@@ -122,10 +122,15 @@ bool cut(MxUnits* u, int64_t P) {
 }
 
 // ------------------------------------------------------------------ convolution
-// longest: the largest piece. A piece reads W - 1 tokens before its own (its
-// gradients as many after), so pieces are as long as leave enough threads to
-// keep the memory busy.
-gdn_status check_conv(const gdn_conv_desc* d, int64_t longest, ConvArgs* a) {
+int64_t vector_channels(int32_t dtype) { return 16 / elem_bytes(dtype); }
+
+// longest: the largest piece; channels: of a thread. A piece reads W - 1 tokens
+// before its own (its gradients as many after, and write a row of sums), but a
+// thread waits for memory every few tokens: pieces are as long as leave enough
+// threads to keep the memory busy (forward and gradients in pieces of 16, 64
+// and 128: B=4 T=4096 D=6144 304, 245 and 240 us, B=2 T=2048 D=2048 35, 64 and
+// 109; 256: 268 and 202).
+gdn_status check_conv(const gdn_conv_desc* d, int64_t longest, int64_t channels, ConvArgs* a) {
     if (d == nullptr) return GDN_ERR_INVALID;
     if (d->W < 2 || d->W > 4) return GDN_ERR_UNSUPPORTED;
     if (d->D < 1 || d->D % 8 != 0 || !dtype_ok(d->dtype) || !dtype_ok(d->w_dtype) || !flag_ok(d->silu)) return GDN_ERR_INVALID;
@@ -135,7 +140,7 @@ gdn_status check_conv(const gdn_conv_desc* d, int64_t longest, ConvArgs* a) {
     if (s.un.total > kMaxElems / d->D || !stride_ok(d->x_stride, s.un.total, d->dtype)) return GDN_ERR_INVALID;
     memset(a, 0, sizeof(*a));
     a->un = s.un;
-    const int64_t vectors = d->D / (16 / elem_bytes(d->dtype));
+    const int64_t vectors = d->D / channels;
     int64_t P = longest;
     while (P > 8 && pieces(s.un, P) * vectors < 100000) P /= 2;
     if (!cut(&a->un, P) || int64_t(a->un.n_pieces) * vectors > kMaxThreads || int64_t(s.un.n_units) * vectors > kMaxThreads)
@@ -155,7 +160,7 @@ extern "C" gdn_status gdn_conv_fwd(const gdn_conv_desc* d, const void* x, const 
                                    const void* s_in, const int32_t* in_pages, void* s_out, const int32_t* out_pages,
                                    int32_t n_pages, void* y, hipStream_t stream) {
     ConvArgs a;
-    const gdn_status st = check_conv(d, 64, &a);
+    const gdn_status st = check_conv(d, 64, vector_channels(d ? d->dtype : 0), &a);
     if (st != GDN_OK) return st;
     if (!weight || (a.un.total > 0 && (!x || !y))) return GDN_ERR_INVALID;
     if (n_pages < 0 || (in_pages && !s_in) || (out_pages && !s_out)) return GDN_ERR_INVALID;
@@ -180,7 +185,7 @@ extern "C" gdn_status gdn_conv_bwd(const gdn_conv_desc* d, const void* x, const 
                                    float* dbias, void* dinitial, void* workspace, size_t* workspace_bytes,
                                    hipStream_t stream) {
     ConvArgs a;
-    gdn_status st = check_conv(d, 128, &a);
+    gdn_status st = check_conv(d, 128, gdn::CONV_BWD_CHANNELS, &a);
     if (st != GDN_OK) return st;
     const int64_t rows = int64_t(a.un.n_pieces) + gdn::row_sums_rows(a.un.n_pieces);
     if (rows > kMaxElems / (int64_t(d->D) * (d->W + 1))) return GDN_ERR_UNSUPPORTED;
@@ -207,7 +212,7 @@ extern "C" gdn_status gdn_conv_step(const gdn_conv_desc* d, const void* x, const
                                     const int32_t* pages, int32_t n_pages, void* state, void* y, hipStream_t stream) {
     if (d != nullptr && d->B == 0 && d->T == 1) return GDN_OK;
     ConvArgs a;
-    const gdn_status st = check_conv(d, 8, &a);
+    const gdn_status st = check_conv(d, 8, vector_channels(d ? d->dtype : 0), &a);
     if (st != GDN_OK) return st;
     if (d->T != 1 || d->n_units != 0 || n_pages < 0) return GDN_ERR_INVALID;
     if (!x || !weight || !y || (n_pages > 0 && !state) || !all_aligned16(x, weight, bias, state, y)) return GDN_ERR_INVALID;
@@ -229,7 +234,8 @@ struct Scan {
     int64_t slots, sums;   // bytes in front of the workspace
 };
 
-gdn_status check_scan(const gdn_scan_desc* d, Scan* s) {
+// alone: tokens that one workgroup walks in the time that a cut costs in launches
+gdn_status check_scan(const gdn_scan_desc* d, int alone, Scan* s) {
     if (d == nullptr) return GDN_ERR_INVALID;
     if (d->S != 8 && d->S != 16 && d->S != 32 && d->S != 64) return GDN_ERR_UNSUPPORTED;
     if (d->D < 1 || d->G < 1 || d->D % d->G != 0 || d->D / d->G % 8 != 0) return GDN_ERR_INVALID;
@@ -266,17 +272,18 @@ gdn_status check_scan(const gdn_scan_desc* d, Scan* s) {
     if (!cut(&a.keep, gdn::SCAN_KEEP)) return GDN_ERR_UNSUPPORTED;
     if (a.keep.n_pieces > kMaxElems / d->S / d->D) return GDN_ERR_UNSUPPORTED;
     // Segments. A cut costs a second walk (summary and main take 0.7 and 1 of a
-    // whole walk's time) and two launches with a merge between, about 15 us or 130
-    // tokens of one workgroup. So nothing is cut unless one sequence takes longer,
-    // on a compute unit of its own, than both walks of everything on all 256
-    // (T=8192 in 6 documents, D=4096: 254 us cut, 331 whole; T=61 D=512: 9 and 19).
+    // whole walk's time) and two launches with a merge between. So nothing is cut
+    // unless one sequence takes longer, on a compute unit of its own, than both
+    // walks of everything on all 256 (whole and cut: T=8192 in 6 documents, D=4096
+    // 331 and 254 us; D=1024, one sequence of T=96 13.7 and 18.3, 128 17.2 and 19.7,
+    // 160 20.7 and 18.2, with gradients T=96 54 and 57, 128 67 and 56).
     // Then there are as many segments as give every unit four workgroups (two:
     // B=2 T=4096 D=4096 with gradients 792 us, four: 763, eight: 768), but none
     // shorter than what the merge, which walks through them one by one, saves.
     const int64_t tile = gdn::SCAN_TILE, whole = (q.longest + tile - 1) / tile * tile;
     const int64_t walks = int64_t(a.G) * a.blocks;
     int64_t P = whole > 0 ? whole : tile;
-    if (q.longest > 1.4 * double(total) * walks / 256 + 130) {
+    if (q.longest > 1.4 * double(total) * walks / 256 + alone) {
         int64_t lo = ((int64_t)sqrt(0.44 * double(q.longest)) + tile) / tile * tile, hi = P;
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2 / tile * tile;
@@ -312,7 +319,7 @@ void scan_inputs(ScanArgs* a, const void* u, const void* dt, const float* A, con
 
 extern "C" int64_t gdn_scan_h_rows(const gdn_scan_desc* d) {
     Scan s;
-    return check_scan(d, &s) == GDN_OK ? s.a.keep.n_pieces : -1;
+    return check_scan(d, 130, &s) == GDN_OK ? s.a.keep.n_pieces : -1;
 }
 
 extern "C" gdn_status gdn_scan_fwd(const gdn_scan_desc* d, const void* u, const void* dt, const float* A,
@@ -321,7 +328,7 @@ extern "C" gdn_status gdn_scan_fwd(const gdn_scan_desc* d, const void* u, const 
                                    const int32_t* out_pages, int32_t n_pages, float* h, void* out, void* workspace,
                                    size_t* workspace_bytes, hipStream_t stream) {
     Scan s;
-    gdn_status st = check_scan(d, &s);
+    gdn_status st = check_scan(d, 130, &s);
     if (st != GDN_OK) return st;
     bool query = false;
     st = check_workspace(s.slots + s.sums, workspace, workspace_bytes, &query);
@@ -354,7 +361,7 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
                                    float* ddt_bias, float* dh0, void* workspace, size_t* workspace_bytes,
                                    hipStream_t stream) {
     Scan s;
-    gdn_status st = check_scan(d, &s);
+    gdn_status st = check_scan(d, 85, &s);
     if (st != GDN_OK) return st;
     ScanArgs& a = s.a;
     const int64_t walks = int64_t(a.G) * a.bwd_blocks;
@@ -402,7 +409,7 @@ extern "C" gdn_status gdn_scan_step(const gdn_scan_desc* d, const void* u, const
                                     void* out, hipStream_t stream) {
     if (d != nullptr && d->B == 0 && d->T == 1) return GDN_OK;
     Scan s;
-    const gdn_status st = check_scan(d, &s);
+    const gdn_status st = check_scan(d, 130, &s);
     if (st != GDN_OK) return st;
     if (d->T != 1 || d->n_units != 0 || n_pages < 0) return GDN_ERR_INVALID;
     ScanArgs& a = s.a;

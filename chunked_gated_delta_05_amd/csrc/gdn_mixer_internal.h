@@ -12,9 +12,11 @@
 
 namespace gdn {
 
-// Memory that a call walks through is read and written around the caches
-// where it exceeds the last-level cache, which it would only flush.
-constexpr int64_t MX_LAST_LEVEL_BYTES = int64_t(256) << 20;
+// States of half the last-level cache or more are read and written around it:
+// by the next token others have taken their place (states of three layers in
+// turn, 128 sequences of D=8192: 67 MB 30 us through the caches, 34 around; 256
+// sequences 71 and 66; 512, 135 and 124).
+constexpr int64_t MX_AROUND_BYTES = int64_t(128) << 20;
 
 // The sequences, and pieces of at most P tokens that they are cut into. The
 // pieces of sequence u begin at number u * ceil(T / P) (rows), or, without a
@@ -52,6 +54,7 @@ struct ConvArgs {
     void *dx, *dinitial;
     float *dweight, *dbias, *parts;   // parts [pieces][D (W + 1)]
 };
+constexpr int CONV_BWD_CHANNELS = 4;  // of a thread; the other kernels take 16 bytes of them
 hipError_t launch_conv_fwd(const ConvArgs& a, bool states_after, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t s);

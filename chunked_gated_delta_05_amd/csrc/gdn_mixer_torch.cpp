@@ -16,11 +16,22 @@ std::vector<int64_t> with(at::IntArrayRef lead, std::initializer_list<int64_t> r
 
 at::IntArrayRef lead_of(const Tensor& t, int64_t n) { return t.sizes().slice(0, t.dim() - n); }
 
-// Distance of tokens in elements of [B,T,D] or [tokens,D]
+// Distance of tokens in elements of [B,T,D] or [tokens,D], as row_strides has it for rows with heads
 int64_t token_stride(const char* name, const Tensor& t) {
-    int64_t s[2];
-    row_strides(name, t.unsqueeze(-2), s);
-    return s[0];
+    const auto n = t.sizes(), s = t.strides();
+    const int64_t d = t.dim(), D = n[d - 1];
+    if (D > 1 && s[d - 1] != 1) invalid(std::string(name) + ": the values of a row must be contiguous");
+    int64_t ts = s[d - 2];
+    if (d == 3) {
+        if (n[0] * n[1] <= 1) ts = D;
+        else if (n[1] == 1) ts = s[0];
+        else if (n[0] > 1 && s[0] != n[1] * ts) invalid(std::string(name) + ": batch rows must follow each other at the token stride");
+    } else if (n[0] <= 1) {
+        ts = D;
+    }
+    if (ts * t.element_size() % 16 || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 || ts < 0)
+        invalid(std::string(name) + ": rows must be 16-byte aligned");
+    return ts;
 }
 
 void check_like(const char* name, const Tensor& t, ScalarType dtype, const std::vector<int64_t>& shape) {
