@@ -322,11 +322,12 @@ __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
 // ------------------------------------------------------------------ sums of rows
 // Row b of out = rows [b q, b q + q) of x added up, n columns: 16 threads a
 // column vector, joined through LDS in a fixed order.
-constexpr int SUM_ROWS = 64;
-__global__ __launch_bounds__(NT) void row_sums_kernel(const float* x, int64_t rows, int64_t n, RowSums out, int q) {
+__global__ __launch_bounds__(NT) void row_sums_kernel(const float* x, int64_t rows, int64_t n, RowSums out, int q,
+                                                      unsigned cols) {
     __shared__ f32x4 part[16][17];
     const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const int64_t col = ((int64_t)blockIdx.x * 16 + cl) * 4, r0 = (int64_t)blockIdx.y * q;
+    const unsigned b = blockIdx.x / cols;
+    const int64_t col = ((int64_t)(blockIdx.x - b * cols) * 16 + cl) * 4, r0 = (int64_t)b * q;
     const int64_t r1 = r0 + q < rows ? r0 + q : rows;
     f32x4 s = {0, 0, 0, 0};
     if (col < n) {
@@ -338,7 +339,7 @@ __global__ __launch_bounds__(NT) void row_sums_kernel(const float* x, int64_t ro
     if (rl == 0 && col < n) {
 #pragma unroll
         for (int i = 1; i < 16; ++i) s += part[i][cl];
-        int64_t at = col + (int64_t)blockIdx.y * n;
+        int64_t at = col + (int64_t)b * n;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             if (at >= 0 && at < out.n[i] && out.p[i]) *reinterpret_cast<f32x4*>(out.p[i] + at) = s;
@@ -396,8 +397,6 @@ hipError_t launch_conv_step(const ConvArgs& a, hipStream_t s) {
     });
 }
 
-int64_t row_sums_rows(int64_t rows) { return rows > 4 * SUM_ROWS ? (rows + SUM_ROWS - 1) / SUM_ROWS : 0; }
-
 // Many rows in two steps, so that a narrow row's sum is not one workgroup's;
 // the first one's rows follow x's.
 hipError_t launch_row_sums(float* x, int64_t rows, int64_t n, const RowSums& out, hipStream_t s) {
@@ -405,12 +404,12 @@ hipError_t launch_row_sums(float* x, int64_t rows, int64_t n, const RowSums& out
     const int64_t more = row_sums_rows(rows);
     if (more) {
         float* mid = x + rows * n;
-        const dim3 grid(cols, (unsigned)more);
-        row_sums_kernel<<<grid, NT, 0, s>>>(x, rows, n, RowSums{{mid, nullptr, nullptr}, {more * n, 0, 0}}, SUM_ROWS);
+        row_sums_kernel<<<(unsigned)(cols * more), NT, 0, s>>>(x, rows, n, RowSums{{mid, nullptr, nullptr}, {more * n, 0, 0}},
+                                                               SUM_ROWS, cols);
         x = mid;
         rows = more;
     }
-    row_sums_kernel<<<cols, NT, 0, s>>>(x, rows, n, out, (int)rows);
+    row_sums_kernel<<<cols, NT, 0, s>>>(x, rows, n, out, (int)rows, cols);
     return hipGetLastError();
 }
 

@@ -189,6 +189,7 @@ extern "C" gdn_status gdn_conv_bwd(const gdn_conv_desc* d, const void* x, const 
     if (st != GDN_OK) return st;
     const int64_t rows = int64_t(a.un.n_pieces) + gdn::row_sums_rows(a.un.n_pieces);
     if (rows > kMaxElems / (int64_t(d->D) * (d->W + 1))) return GDN_ERR_UNSUPPORTED;
+    if (gdn::row_sums_workgroups(a.un.n_pieces, int64_t(d->D) * (d->W + 1)) > kMaxThreads / 256) return GDN_ERR_UNSUPPORTED;
     bool query = false;
     st = check_workspace(rows * d->D * (d->W + 1) * 4, workspace, workspace_bytes, &query);
     if (st != GDN_OK || query) return st;
@@ -368,6 +369,9 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
     if (a.un.n_pieces > kMaxThreads / 256 / walks) return GDN_ERR_UNSUPPORTED;
     if (a.un.total > kMaxElems / (walks * 2 * d->S) || a.un.total * d->G * (d->S / 2) > kMaxThreads) return GDN_ERR_UNSUPPORTED;
     const int64_t rows = int64_t(a.un.n_pieces) + gdn::row_sums_rows(a.un.n_pieces);
+    if (rows > kMaxElems / (int64_t(d->D) * (d->S + 2)) ||
+        gdn::row_sums_workgroups(a.un.n_pieces, int64_t(d->D) * (d->S + 2)) > kMaxThreads / 256)
+        return GDN_ERR_UNSUPPORTED;
     const int64_t bc = align256(walks * a.un.total * 2 * d->S * 4), ap = align256(rows * d->D * (d->S + 2) * 4);
     bool query = false;
     st = check_workspace(s.slots + s.sums + bc + ap, workspace, workspace_bytes, &query);

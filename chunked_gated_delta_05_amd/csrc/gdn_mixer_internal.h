@@ -36,7 +36,12 @@ struct RowSums {
     float* p[3];
     int64_t n[3];
 };
-int64_t row_sums_rows(int64_t rows);
+constexpr int SUM_ROWS = 64;   // of a workgroup, where there are many
+constexpr int64_t row_sums_rows(int64_t rows) { return rows > 4 * SUM_ROWS ? (rows + SUM_ROWS - 1) / SUM_ROWS : 0; }
+// of its largest launch
+constexpr int64_t row_sums_workgroups(int64_t rows, int64_t n) {
+    return (n + 63) / 64 * (row_sums_rows(rows) ? row_sums_rows(rows) : 1);
+}
 hipError_t launch_row_sums(float* x, int64_t rows, int64_t n, const RowSums& out, hipStream_t s);
 
 struct ConvArgs {
@@ -105,8 +110,19 @@ struct RotaryArgs {
     float *dq_weight, *dk_weight, *parts;   // parts [workgroups][2][D]
     int32_t workgroups;
 };
+// Tokens that a workgroup makes the angles of at a time: as many as leave every
+// compute unit several workgroups
+constexpr int ROTARY_TOKENS = 8;
+constexpr int rotary_tokens(int64_t tokens) {
+    int n = ROTARY_TOKENS;
+    while (n > 1 && tokens < int64_t(n) * 2048) n /= 2;
+    return n;
+}
 // workgroups of the backward, each with a row of partial sums
-int32_t rotary_bwd_workgroups(int64_t tokens);
+constexpr int32_t rotary_bwd_workgroups(int64_t tokens) {
+    const int64_t all = (tokens + rotary_tokens(tokens) - 1) / rotary_tokens(tokens);
+    return (int32_t)(all < 1024 ? all : 1024);
+}
 hipError_t launch_rotary_fwd(const RotaryArgs& a, hipStream_t s);
 hipError_t launch_rotary_bwd(const RotaryArgs& a, hipStream_t s);
 

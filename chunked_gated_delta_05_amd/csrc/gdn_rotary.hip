@@ -14,7 +14,6 @@ namespace gdn {
 namespace {
 
 constexpr int NT = 256;
-constexpr int MAX_TOKENS = 8;      // of a workgroup at a time
 constexpr int MAX_PAIRS = 128;
 
 // cos and sin of a turn's fraction f: f = n / 4 + r, |r| <= 1/8, and the Taylor
@@ -126,7 +125,7 @@ struct Rows {
 
 template <typename T, int L>
 __global__ __launch_bounds__(NT) void rotary_fwd_kernel(RotaryArgs a, int tokens) {
-    __shared__ __align__(16) f32x2 cs[MAX_TOKENS][MAX_PAIRS];
+    __shared__ __align__(16) f32x2 cs[ROTARY_TOKENS][MAX_PAIRS];
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int n = (int)(a.tokens - t0 < tokens ? a.tokens - t0 : tokens);
     const int l = threadIdx.x % L;
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(NT) void rotary_fwd_kernel(RotaryArgs a, int tokens
 // turned-back gradient times n over rows.
 template <typename T, int L>
 __global__ __launch_bounds__(NT) void rotary_bwd_kernel(RotaryArgs a, int tokens) {
-    __shared__ __align__(16) f32x2 cs[MAX_TOKENS][MAX_PAIRS];
+    __shared__ __align__(16) f32x2 cs[ROTARY_TOKENS][MAX_PAIRS];
     __shared__ f32x4 red[NT][4];
     const int l = threadIdx.x % L;
     const Place p = place_of(a, l);
@@ -249,24 +248,11 @@ hipError_t by_type(const RotaryArgs& a, F f) {
     return hipGetLastError();
 }
 
-// tokens of a workgroup: as many as leave every compute unit several
-int tokens_of(int64_t tokens) {
-    int n = MAX_TOKENS;
-    while (n > 1 && tokens < (int64_t)n * 2048) n /= 2;
-    return n;
-}
-
 }  // namespace
-
-int32_t rotary_bwd_workgroups(int64_t tokens) {
-    const int n = tokens_of(tokens);
-    const int64_t all = (tokens + n - 1) / n;
-    return (int32_t)(all < 1024 ? all : 1024);
-}
 
 hipError_t launch_rotary_fwd(const RotaryArgs& a, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
-    const int n = tokens_of(a.tokens);
+    const int n = rotary_tokens(a.tokens);
     const unsigned grid = (unsigned)((a.tokens + n - 1) / n);
     return by_type(a, [&](auto t, auto l) { rotary_fwd_kernel<decltype(t), l()><<<grid, NT, 0, s>>>(a, n); });
 }
@@ -275,7 +261,7 @@ hipError_t launch_rotary_bwd(const RotaryArgs& a, hipStream_t s) {
     const int64_t d = a.D;
     if (a.tokens > 0) {
         const hipError_t e = by_type(a, [&](auto t, auto l) {
-            rotary_bwd_kernel<decltype(t), l()><<<(unsigned)a.workgroups, NT, 0, s>>>(a, tokens_of(a.tokens));
+            rotary_bwd_kernel<decltype(t), l()><<<(unsigned)a.workgroups, NT, 0, s>>>(a, rotary_tokens(a.tokens));
         });
         if (e != hipSuccess || !a.parts) return e;
     }
