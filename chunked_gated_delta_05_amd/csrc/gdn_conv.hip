@@ -320,32 +320,9 @@ __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
 }
 
 // ------------------------------------------------------------------ sums of rows
-// Row b of out = rows [b q, b q + q) of x added up, n columns: 16 threads a
-// column vector, joined through LDS in a fixed order.
 __global__ __launch_bounds__(NT) void row_sums_kernel(const float* x, int64_t rows, int64_t n, RowSums out, int q,
                                                       unsigned cols) {
-    __shared__ f32x4 part[16][17];
-    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const unsigned b = blockIdx.x / cols;
-    const int64_t col = ((int64_t)(blockIdx.x - b * cols) * 16 + cl) * 4, r0 = (int64_t)b * q;
-    const int64_t r1 = r0 + q < rows ? r0 + q : rows;
-    f32x4 s = {0, 0, 0, 0};
-    if (col < n) {
-#pragma unroll 4
-        for (int64_t r = r0 + rl; r < r1; r += 16) s += *reinterpret_cast<const f32x4*>(x + r * n + col);
-    }
-    part[rl][cl] = s;
-    lds_barrier();
-    if (rl == 0 && col < n) {
-#pragma unroll
-        for (int i = 1; i < 16; ++i) s += part[i][cl];
-        int64_t at = col + (int64_t)b * n;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            if (at >= 0 && at < out.n[i] && out.p[i]) *reinterpret_cast<f32x4*>(out.p[i] + at) = s;
-            at -= out.n[i];
-        }
-    }
+    sum_rows(x, rows, n, out, q, cols, blockIdx.x);
 }
 
 template <typename F>

@@ -164,4 +164,34 @@ __device__ __forceinline__ f32x2 four_sums(f32x4 v, int lane) {
     return f32x2{r, 0.0f};
 }
 
+// ------------------------------------------------------------------ sums of rows
+// Workgroup (of 256) w: row b = w / cols of out = rows [b q, b q + q) of x added
+// up, 64 of its n columns: 16 threads a column vector, joined through LDS in a
+// fixed order.
+__device__ __forceinline__ void sum_rows(const float* x, int64_t rows, int64_t n, const RowSums& out, int q, unsigned cols,
+                                         unsigned w) {
+    __shared__ f32x4 part[16][17];
+    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
+    const unsigned b = w / cols;
+    const int64_t col = ((int64_t)(w - b * cols) * 16 + cl) * 4, r0 = (int64_t)b * q;
+    const int64_t r1 = r0 + q < rows ? r0 + q : rows;
+    f32x4 s = {0, 0, 0, 0};
+    if (col < n) {
+#pragma unroll 4
+        for (int64_t r = r0 + rl; r < r1; r += 16) s += *reinterpret_cast<const f32x4*>(x + r * n + col);
+    }
+    part[rl][cl] = s;
+    lds_barrier();
+    if (rl == 0 && col < n) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += part[i][cl];
+        int64_t at = col + (int64_t)b * n;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            if (at >= 0 && at < out.n[i] && out.p[i]) *reinterpret_cast<f32x4*>(out.p[i] + at) = s;
+            at -= out.n[i];
+        }
+    }
+}
+
 }  // namespace gdn

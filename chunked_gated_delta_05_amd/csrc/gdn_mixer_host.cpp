@@ -19,6 +19,10 @@ using gdn::ScanArgs;
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;                   // sanity bound on any tensor
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 256;         // of a launch along x, in workgroups of 256
+// Segments of a sequence up to which each adds up those before its own, which
+// saves the launch of a merge (T=160 D=1024 20.1 to 15.8 us, T=800 26.7 to 23.8,
+// gradients of T=400 61 to 53; where 32 of them do, T=1000 D=4096 147 to 156).
+constexpr int64_t kJoin = 16;
 constexpr int32_t kMaxTokens = INT32_MAX - 4096;                  // of a sequence: its tiles' ends are ints
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
@@ -295,6 +299,7 @@ gdn_status check_scan(const gdn_scan_desc* d, int alone, Scan* s) {
     }
     if (!cut(&a.un, P)) return GDN_ERR_UNSUPPORTED;
     a.cut = q.longest > P;
+    a.join = a.cut && (q.longest + P - 1) / P <= kJoin;
     const int64_t merge = int64_t(q.un.n_units) * ((int64_t(d->D) * d->S + 255) / 256) * 256;
     if (a.un.n_pieces > kMaxThreads / 256 / walks || merge > kMaxThreads) return GDN_ERR_UNSUPPORTED;
     if (a.cut) {
@@ -346,11 +351,16 @@ extern "C" gdn_status gdn_scan_fwd(const gdn_scan_desc* d, const void* u, const 
     a.n_pages = n_pages;
     a.h = h;
     a.out = out;
+    // a sequence's last segment may replace the state before its others have read
+    // it: where the two share memory the merge reads it in front of all
+    const uint64_t page = uint64_t(d->D) * d->S * 4;
+    if (overlap(s_in, page * (in_pages ? n_pages : a.un.n_units), s_out, page * (out_pages ? n_pages : a.un.n_units)))
+        a.join = 0;
     if (a.cut) {
         a.slots = static_cast<float*>(workspace);
         a.sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + s.slots);
         if (gdn::launch_scan_summary(a, false, stream) != hipSuccess) return GDN_ERR_DEVICE;
-        if (gdn::launch_scan_merge(a, false, stream) != hipSuccess) return GDN_ERR_DEVICE;
+        if (!a.join && gdn::launch_scan_merge(a, false, stream) != hipSuccess) return GDN_ERR_DEVICE;
     }
     return run(gdn::launch_scan_fwd(a, stream));
 }
@@ -382,6 +392,7 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
         return GDN_ERR_INVALID;
     const uint64_t states = uint64_t(a.un.n_units) * d->D * d->S * 4;
     if (dh0 != dht && overlap(dh0, states, dht, states)) return GDN_ERR_INVALID;
+    if (dh0 == dht) a.join = 0;   // as in gdn_scan_fwd
     scan_inputs(&a, u, dt, A, B, C, skip, gate, dt_bias);
     a.s_in = dht;
     a.s_out = dh0;
@@ -402,7 +413,7 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
     a.a_parts = reinterpret_cast<float*>(base + s.slots + s.sums + bc);
     if (a.cut) {
         if (gdn::launch_scan_summary(a, true, stream) != hipSuccess) return GDN_ERR_DEVICE;
-        if (gdn::launch_scan_merge(a, true, stream) != hipSuccess) return GDN_ERR_DEVICE;
+        if (!a.join && gdn::launch_scan_merge(a, true, stream) != hipSuccess) return GDN_ERR_DEVICE;
     }
     return run(gdn::launch_scan_bwd(a, stream));
 }

@@ -70,6 +70,7 @@ struct ScanArgs {
     MxUnits un;               // P: tokens of a segment
     MxUnits keep;             // the same with P = SCAN_KEEP: rows of h
     int32_t cut;              // some sequence has more than one segment
+    int32_t join;             // a segment adds up those before it itself, no merge
     int32_t D, G, S, dtype, softplus, n_pages;
     int32_t blocks, bwd_blocks;   // of channels in a group; the backward's workgroups hold half as many
     const void *u, *dt, *gate, *b, *c;

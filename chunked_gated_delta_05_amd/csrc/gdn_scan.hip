@@ -138,6 +138,48 @@ __device__ __forceinline__ f32x4 step_sizes(f32x4 raw, int softplus) {
     return r;
 }
 
+// ------------------------------------------------------------------ segments
+// The states that a segment is entered with, or in reverse the gradients: those
+// in front of the sequence and the segments' own between, added up by the segment
+// itself where there are few (join), by a merge beforehand where
+// there are many.
+template <bool REVERSE, int S, int K>
+__device__ __forceinline__ void entry_states(const ScanArgs& a, const Piece& pc, int piece, const Lane<S, K>& l,
+                                             const f32x4 (&A2)[K], f32x4 (&h)[K]) {
+    const int64_t page_size = (int64_t)a.D * S;
+    if (a.cut && !a.join) {
+        load_states(h, a.slots + piece * page_size + l.at, S);
+        return;
+    }
+    if (a.s_in) {
+        const int64_t page = page_of(a.in_pages, a.n_pages, pc.unit);
+        if (page >= 0) load_states(h, a.s_in + page * page_size + l.at, S);
+    }
+    if (!a.cut) return;
+    const int n = REVERSE ? (pc.seq.len - 1) / a.un.P - pc.first / a.un.P : pc.first / a.un.P;   // segments before
+    constexpr int AHEAD = 4;
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+        f32x4 own[AHEAD][K];
+        float sum[AHEAD][K];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int64_t p = piece + (REVERSE ? 1 : -1) * (n - min(i0 + i, n - 1));
+            load_states(own[i], a.slots + p * page_size + l.at, S);
+#pragma unroll
+            for (int k = 0; k < K; ++k) sum[i][k] = a.sums[p * a.D + l.d + k];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i0 + i >= n) break;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    h[k][j] = fmaf(__builtin_amdgcn_exp2f(sum[i][k] * A2[k][j]), h[k][j], own[i][k][j]);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ prompts
 template <typename T, int S, int K>
 __global__ __launch_bounds__((Shape<S, K>::NT), 2) void scan_fwd_kernel(ScanArgs a) {
@@ -159,12 +201,7 @@ __global__ __launch_bounds__((Shape<S, K>::NT), 2) void scan_fwd_kernel(ScanArgs
     load_states(A2, a.A + l.at, S);
 #pragma unroll
     for (int i = 0; i < K; ++i) A2[i] *= LOG2E;
-    if (a.cut) {
-        load_states(h, a.slots + piece * page_size + l.at, S);
-    } else if (a.s_in) {
-        const int64_t page = page_of(a.in_pages, a.n_pages, pc.unit);
-        if (page >= 0) load_states(h, a.s_in + page * page_size + l.at, S);
-    }
+    entry_states<false, S, K>(a, pc, piece, l, A2, h);
     float* keep = a.h ? a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + l.at : nullptr;
 
     const int cv = threadIdx.x % Sh::V;
@@ -487,9 +524,13 @@ __global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs
 
     if (!pc.none) {
         const f32x4 A2 = *reinterpret_cast<const f32x4*>(a.A + l.at) * LOG2E;
-        f32x4 E = {0, 0, 0, 0};
-        if (a.cut) E = *reinterpret_cast<const f32x4*>(a.slots + piece * page_size + l.at);
-        else if (a.s_in) E = *reinterpret_cast<const f32x4*>(a.s_in + pc.unit * page_size + l.at);
+        f32x4 E;
+        {
+            const f32x4 rate[1] = {A2};
+            f32x4 e[1] = {};
+            entry_states<true, S, 1>(a, pc, piece, l, rate, e);
+            E = e[0];
+        }
         const float* keep = a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + l.at;
         const f32x4 bias = load_f4(a.dt_bias, cch), skip = load_f4(a.skip, cch);
         const ChannelSums<S> channels(l.lane);
@@ -667,9 +708,15 @@ __global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs
     }
 }
 
-// dB and dC: sums over the workgroups of a group's channels, four values a thread
+// dB and dC: sums over the workgroups of a group's channels, four values a
+// thread. The workgroups behind those add up the rows of dA, dskip and ddt_bias
+// where these are few.
 template <typename T>
-__global__ __launch_bounds__(NT) void scan_bc_kernel(ScanArgs a, int blocks) {
+__global__ __launch_bounds__(NT) void scan_bc_kernel(ScanArgs a, int blocks, unsigned bc_groups, RowSums out, unsigned cols) {
+    if (blockIdx.x >= bc_groups) {
+        sum_rows(a.a_parts, a.un.n_pieces, (int64_t)a.D * (a.S + 2), out, a.un.n_pieces, cols, blockIdx.x - bc_groups);
+        return;
+    }
     const int per = 2 * a.S / 4;
     const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x, rows = i / per;
     if (rows >= a.un.total * a.G) return;
@@ -805,14 +852,16 @@ hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) {
         scan_bwd_kernel<decltype(t), n()><<<grid_of<Sh>(a), Sh::NT, 0, s>>>(a);
     });
     if (e != hipSuccess) return e;
-    const unsigned bc = (unsigned)((a.un.total * a.G * (2 * a.S / 4) + NT - 1) / NT);
-    if (bc > 0) {
-        if (a.dtype == GDN_DTYPE_BF16) scan_bc_kernel<bf16><<<bc, NT, 0, s>>>(a, a.bwd_blocks);
-        else scan_bc_kernel<float><<<bc, NT, 0, s>>>(a, a.bwd_blocks);
+    const int64_t d = a.D, n = d * (a.S + 2);
+    const RowSums out{{a.dA, a.dskip, a.ddt_bias}, {d * a.S, d, d}};
+    const bool few = row_sums_rows(a.un.n_pieces) == 0;
+    const unsigned bc = (unsigned)((a.un.total * a.G * (2 * a.S / 4) + NT - 1) / NT), cols = (unsigned)((n + 63) / 64);
+    const unsigned grid = bc + (few ? cols : 0);
+    if (grid > 0) {
+        if (a.dtype == GDN_DTYPE_BF16) scan_bc_kernel<bf16><<<grid, NT, 0, s>>>(a, a.bwd_blocks, bc, out, cols);
+        else scan_bc_kernel<float><<<grid, NT, 0, s>>>(a, a.bwd_blocks, bc, out, cols);
     }
-    const int64_t d = a.D;
-    return launch_row_sums(a.a_parts, a.un.n_pieces, d * (a.S + 2),
-                           RowSums{{a.dA, a.dskip, a.ddt_bias}, {d * a.S, d, d}}, s);
+    return few ? hipGetLastError() : launch_row_sums(a.a_parts, a.un.n_pieces, n, out, s);
 }
 
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t s) {
