@@ -282,20 +282,34 @@ gdn_status check_scan(const gdn_scan_desc* d, int alone, Scan* s) {
     // walks of everything on all 256 (whole and cut: T=8192 in 6 documents, D=4096
     // 331 and 254 us; D=1024, one sequence of T=96 13.7 and 18.3, 128 17.2 and 19.7,
     // 160 20.7 and 18.2, with gradients T=96 54 and 57, 128 67 and 56).
-    // Then there are as many segments as give every unit four workgroups (two:
-    // B=2 T=4096 D=4096 with gradients 792 us, four: 763, eight: 768), but none
-    // shorter than what the merge, which walks through them one by one, saves.
+    // Four workgroups run on a unit at a time and share its issue, so all take about
+    // as long as the most of them on one unit, at segments of P tokens (and 10 for a
+    // start); where fewer are left, instructions wait (kRest). Of 2 to 8 on a unit the best (3 documents,
+    // T=6000 D=4096, in 28 segments 202 us, in 48 176; 12, T=16384 D=1024, 155 and
+    // 134; B=2 T=4096 D=4096 with gradients, 16, 32 and 64: 785, 756 and 762). None
+    // is shorter than what the merge, which walks through them one by one, saves.
     const int64_t tile = gdn::SCAN_TILE, whole = (q.longest + tile - 1) / tile * tile;
     const int64_t walks = int64_t(a.G) * a.blocks;
     int64_t P = whole > 0 ? whole : tile;
     if (q.longest > 1.4 * double(total) * walks / 256 + alone) {
-        int64_t lo = ((int64_t)sqrt(0.44 * double(q.longest)) + tile) / tile * tile, hi = P;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2 / tile * tile;
-            if (segments(q.un, d->offsets_host, mid) * walks <= 1024) hi = mid;
-            else lo = mid + tile;
+        const int64_t least = ((int64_t)sqrt(0.44 * double(q.longest)) + tile) / tile * tile, most = P;
+        const bool many = q.un.n_units > 64;   // sequences to count through: four a unit it is
+        constexpr double kRest[4] = {0, 1.7, 2.4, 3.15};
+        double best = 0;
+        for (int per = many ? 4 : 2; per <= (many ? 4 : 8); ++per) {
+            int64_t lo = least < most ? least : most, hi = most;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) / 2 / tile * tile;
+                if (segments(q.un, d->offsets_host, mid) * walks <= per * 256) hi = mid;
+                else lo = mid + tile;
+            }
+            const int64_t on = (segments(q.un, d->offsets_host, hi) * walks + 255) / 256;
+            const double cost = double(hi + 10) * (on / 4 * 4 + kRest[on % 4]);
+            if (best == 0 || cost < best) {
+                best = cost;
+                P = hi;
+            }
         }
-        P = hi;
     }
     if (!cut(&a.un, P)) return GDN_ERR_UNSUPPORTED;
     a.cut = q.longest > P;

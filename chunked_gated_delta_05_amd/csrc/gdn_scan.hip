@@ -182,7 +182,7 @@ __device__ __forceinline__ void entry_states(const ScanArgs& a, const Piece& pc,
 
 // ------------------------------------------------------------------ prompts
 template <typename T, int S, int K>
-__global__ __launch_bounds__((Shape<S, K>::NT), 2) void scan_fwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__((Shape<S, K>::NT), (sizeof(T) == 2 && S > 8 && K == 2 ? 4 : 2)) void scan_fwd_kernel(ScanArgs a) {
     typedef Shape<S, K> Sh;
     constexpr int TT = FT, E = 4 / K;                // E tokens give a lane four sums over states
     typedef Rows<T, Sh, TT> Rw;
