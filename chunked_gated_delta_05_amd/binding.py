@@ -974,6 +974,15 @@ def gdn_conv_bwd(x, weight, bias, dout, *, activation=None, meta: UnitMeta | Non
                                            dfinal, want_dinitial, workspace)
 
 
+def _gradient(d, like):
+    """A gradient as the calls take it: like's type, contiguous, 16-byte aligned;
+    zeros where none arrived."""
+    if d is None:
+        return torch.zeros(like.shape, dtype=like.dtype, device=like.device)
+    d = d.to(like.dtype).contiguous()
+    return d if d.data_ptr() % 16 == 0 else d.clone()
+
+
 class CausalConv(torch.autograd.Function):
     """gdn_conv_fwd and gdn_conv_bwd as one autograd op: (x, weight, bias,
     initial_state, activation, meta) -> (y, final state). Second-order gradients
@@ -992,9 +1001,8 @@ class CausalConv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dfinal):
         x, weight, bias, s0 = ctx.saved_tensors
-        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.to(x.dtype).contiguous()
-        r = gdn_conv_bwd(x, weight, bias, dy, activation=ctx.activation, meta=ctx.meta, initial_state=s0,
-                         dfinal=None if dfinal is None else dfinal.to(x.dtype).contiguous(),
+        r = gdn_conv_bwd(x, weight, bias, _gradient(dy, x), activation=ctx.activation, meta=ctx.meta, initial_state=s0,
+                         dfinal=None if dfinal is None else _gradient(dfinal, x),
                          want_dinitial=s0 is not None)
         return (r["dx"], r["dweight"].to(weight.dtype), None if bias is None else r["dbias"].to(bias.dtype),
                 r.get("dinitial"), None, None)
@@ -1057,9 +1065,9 @@ class SelectiveScan(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout, dfinal):
         u, dt, A, B, C, skip, gate, dt_bias, h = ctx.saved_tensors
-        dout = torch.zeros(u.shape, dtype=u.dtype, device=u.device) if dout is None else dout.to(u.dtype).contiguous()
-        r = gdn_scan_bwd(u, dt, A, B, C, skip, gate, dout, h, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
-                         meta=ctx.meta, dht=None if dfinal is None else dfinal.contiguous(), want_dh0=ctx.has_s0)
+        r = gdn_scan_bwd(u, dt, A, B, C, skip, gate, _gradient(dout, u), h, dt_bias=dt_bias,
+                         dt_softplus=ctx.dt_softplus, meta=ctx.meta,
+                         dht=None if dfinal is None else _gradient(dfinal, A), want_dh0=ctx.has_s0)
         return (*(r.get(n) for n in ("du", "ddt", "dA", "dB", "dC", "dskip", "dgate", "ddt_bias", "dh0")), None, None)
 
 
@@ -1163,9 +1171,8 @@ class QKRotary(torch.autograd.Function):
         if ctx.needs_input_grad[2]:
             raise NotImplementedError("QKRotary has no gradient for freqs: detach them")
         q, k, freqs, positions, q_weight, k_weight = ctx.saved_tensors
-        full = lambda d, x: torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d is None else d.to(x.dtype).contiguous()
-        r = gdn_qk_rotary_bwd(q, k, freqs, positions, full(dq, q), full(dk, k), q_weight=q_weight, k_weight=k_weight,
-                              **ctx.options)
+        r = gdn_qk_rotary_bwd(q, k, freqs, positions, _gradient(dq, q), _gradient(dk, k), q_weight=q_weight,
+                              k_weight=k_weight, **ctx.options)
         like = lambda d, w: None if w is None else d.to(w.dtype)
         return (r["dq"], r["dk"], None, None, like(r.get("dq_weight"), q_weight), like(r.get("dk_weight"), k_weight),
                 None, None, None, None)

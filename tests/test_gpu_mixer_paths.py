@@ -2,6 +2,7 @@
 reach: both widths of the scan's walks, cut and whole, many pieces, large steps,
 values beyond 2^31, streams, graphs, versions, autograd, values that are not
 finite, and a run of them together."""
+import ctypes
 import os
 import sys
 
@@ -44,6 +45,55 @@ def test_scan_wide_equals_narrow():
     one = dict(c, **{k: c[k][77:78].contiguous() for k in ("u", "dt", "gate", "B", "C", "s0")})
     o, f, hh = scan_gpu(one, want_h=True)
     assert torch.equal(o[0], out[77]) and torch.equal(f[0], final[77]) and torch.equal(hh, h[77 * 3:78 * 3])
+
+
+@pytest.mark.parametrize("lead", [(2, 400), [400, 1, 90]])
+def test_scan_cut_pages_in_place(lead):
+    # cut sequences whose states are replaced where they were read
+    c = scan_case(lead, 72, 16, 1, "bf16", seed=11)
+    n = len(c["offs"]) - 1
+    pool = randn(gen(12), n + 2, 72, 16)
+    before = pool.clone()
+    pages = torch.arange(n, 0, -1, dtype=I32, device="cuda")
+    c["s0"], c["dout"] = pool, None
+    out, _, _ = scan_gpu(c, initial_pages=pages, final_out=pool, final_pages=pages)
+    c["s0"] = before[pages.long()]
+    a = scan_args(c)
+    want, scale = ref.scan(*a), ref.scan(*a, absolute=True)
+    near(out, want[0], scale[0], 24 * 400 + 64, "out")
+    near(pool[pages.long()], want[1], scale[1], 24 * 400 + 64, "final")
+    assert torch.equal(pool[[0, n + 1]], before[[0, n + 1]])
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "D", "G", "S", "dtype", "softplus", "n_units")] + \
+               [(n, ctypes.c_int64) for n in ("u_stride", "dt_stride", "gate_stride", "b0", "b1", "c0", "c1")] + \
+               [("offsets_host", ctypes.c_void_p), ("offsets_dev", ctypes.c_void_p)]
+
+
+@pytest.mark.parametrize("T", [400, 1500])     # segments joined and merged
+def test_entry_gradients_replace_those_of_the_final_states(T):
+    c = scan_case((2, T), 72, 16, 1, "fp32", seed=13)
+    for k in ("u", "dt", "gate", "B", "C"):
+        c[k] = c[k].contiguous()
+    h = scan_gpu(c, want_h=True)[2]
+    r = scan_gpu_bwd(c, h)
+    d = ScanDesc(2, T, 72, 1, 16, 0, 1, 0, 72, 72, 72, 16, 16, 16, 16, None, None)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    dh = c["dht"].clone()
+    got = {k: torch.empty_like(t) for k, t in r.items()}
+    ins = [p(c[k]) for k in ("u", "dt", "A", "B", "C", "skip", "gate", "dt_bias")] + [p(h), p(c["dout"]), p(dh)]
+    outs = [p(got[k]) for k in ("du", "ddt", "dA", "dB", "dC", "dskip", "dgate", "ddt_bias")] + [p(dh)]
+    f, size = gb.lib().gdn_scan_bwd, ctypes.c_size_t(0)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert f(ctypes.byref(d), *ins, *outs, None, ctypes.byref(size), stream) == 0
+    ws = torch.empty(size.value, dtype=torch.uint8, device="cuda")
+    assert f(ctypes.byref(d), *ins, *outs, p(ws), ctypes.byref(size), stream) == 0
+    got["dh0"] = dh
+    a = scan_args(c)
+    want, scale = ref.scan(*a)[2], ref.scan(*a, absolute=True)[2]
+    for k, t in got.items():
+        near(t, want[k], scale[k], 2 * (24 * T + 64) + 72 + 2 * T, k)
 
 
 @pytest.mark.parametrize("N", [259, 1030])   # four sequences a workgroup; states around the caches
@@ -290,6 +340,60 @@ def test_autograd_ops_match_the_calls():
     r = gb.gdn_qk_rotary_bwd(q.detach(), k.detach(), f, None, a.detach(), b2.detach(), q_weight=wt.detach(), k_weight=wt.detach())
     assert torch.equal(grads[0], r["dq"]) and torch.equal(grads[1], r["dk"])
     assert torch.equal(grads[2], r["dq_weight"].to(BF) + r["dk_weight"].to(BF))
+
+
+def hybrid_leaves():
+    shapes = dict(x=(2, 70, 72), w=(72, 4), dt=(2, 70, 72), A=(72, 16), B=(2, 70, 1, 16), C=(2, 70, 1, 16), skip=(72,),
+                  k=(2, 70, 3, 24), wt=(24,))
+    return {n: (randn(gen(i), *s) if n != "A" else -randn(gen(i), *s).abs()).requires_grad_() for i, (n, s) in enumerate(shapes.items())}
+
+
+def hybrid_outputs(p, f):
+    y, s1 = gb.CausalConv.apply(p["x"], p["w"], None, None, "silu")
+    o, s2 = gb.SelectiveScan.apply(y, p["dt"], p["A"], p["B"], p["C"], p["skip"], y, None, None, True)
+    q, k = gb.QKRotary.apply(o.unflatten(-1, (3, 24)), p["k"], f, None, p["wt"], p["wt"])
+    return [q, k, s1, s2]
+
+
+def test_captured_training_step_repeats_the_eager_one():
+    p, f = hybrid_leaves(), gb.rotary_frequencies(24, device="cuda")
+
+    def step():
+        outs = hybrid_outputs(p, f)
+        return [o.detach() for o in outs] + list(torch.autograd.grad(outs, list(p.values()), [torch.ones_like(o) for o in outs]))
+
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gradients_may_arrive_expanded_or_off_alignment():
+    p, f = hybrid_leaves(), gb.rotary_frequencies(24, device="cuda")
+    outs, leaves = hybrid_outputs(p, f), list(p.values())
+    want = torch.autograd.grad(outs, leaves, [torch.ones_like(o) for o in outs], retain_graph=True)
+    expanded = torch.autograd.grad([o.sum() for o in outs], leaves, retain_graph=True)
+    odd = []
+    for o in outs:
+        room = torch.ones(o.numel() + 1, dtype=o.dtype, device="cuda")
+        odd.append(room[1:].view(o.shape))
+        assert odd[-1].data_ptr() % 16
+    shifted = torch.autograd.grad(outs, leaves, odd)
+    for a, b, c in zip(want, expanded, shifted):
+        assert torch.equal(a, b) and torch.equal(a, c)
 
 
 def test_second_order_gradients_and_constants_raise():
