@@ -128,6 +128,7 @@ __device__ __forceinline__ float dpp(float x) {
     return u2f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f2u(x), CTRL, 0xf, 0xf, true));
 }
 constexpr int QUAD_XOR1 = 0xB1, QUAD_XOR2 = 0x4E, ROW_ROR4 = 0x124, ROW_ROR8 = 0x128, HALF_MIRROR = 0x141;
+constexpr int ROW_BCAST = 0x150;   // + i: lane i of 16 to all of them
 
 // sum over N neighbouring lanes, in all of them
 template <int N>

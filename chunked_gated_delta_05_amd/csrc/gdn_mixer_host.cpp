@@ -239,8 +239,46 @@ struct Scan {
     int64_t slots, sums;   // bytes in front of the workspace
 };
 
-// alone: tokens that one workgroup walks in the time that a cut costs in launches
-gdn_status check_scan(const gdn_scan_desc* d, int alone, Scan* s) {
+// Tokens that the workgroups of whole sequences, nb each, bring to the compute
+// unit that gets the most, dealt out in turn.
+int64_t fullest(const MxUnits& u, const int32_t* host, int64_t nb, int64_t P) {
+    if (u.dense) return (u.n_units * nb + 255) / 256 * u.T;
+    int64_t step[257] = {}, all = 0, most = 0, on = 0;
+    for (int32_t i = 0; i < u.n_units; ++i) {
+        const int64_t len = int64_t(host[i + 1]) - host[i], at = (host[i] / P + i) * nb % 256, end = at + nb % 256;
+        all += nb / 256 * len;
+        step[at] += len;
+        step[end < 256 ? end : 256] -= len;
+        if (end > 256) {
+            step[0] += len;
+            step[end - 256] -= len;
+        }
+    }
+    for (int i = 0; i < 256; ++i) {
+        on += step[i];
+        most = on > most ? on : most;
+    }
+    return all + most;
+}
+
+// The forward of sequences that would leave compute units with less than two
+// workgroups of one channel a lane: walked whole by one state a lane, or cut. Both
+// are estimated in ns. One state a lane: 16 for each token of the longest sequence
+// and `state` for each token of the waves that a SIMD gets; a cut 10.5 us for its
+// launches and short walks and 1.45 times the waves' part, level (cut and whole:
+// D=4096, one sequence of T=400 25 and 19 us, 1000 42.5 and 40.7, 2000 68 and 78;
+// four of 1000 113 and 92; D=1024, T=300 16 and 14.3, 400 17.3 and 18.4; 12
+// documents, T=16384, 134 and 172; S=64 D=1024, one and four of T=1000 44 and 87,
+// 112 and 90. Beyond: eight of T=1000 D=4096 156 with one channel a lane and 168
+// with one state).
+bool whole_pays(const ScanArgs& a, const int32_t* host, int64_t longest, int64_t P) {
+    const double state = a.S == 8 ? 26 : a.S == 16 ? 18.5 : a.S == 32 ? 32 : 67;
+    const int ch = gdn::scan_narrow_channels(a.S);
+    const int64_t nb = int64_t(a.G) * ((a.D / a.G + ch - 1) / ch), most = fullest(a.un, host, nb, P);
+    return 16.0 * longest + state * most < 10500 + 1.45 * state * a.un.total * nb / 256;
+}
+
+gdn_status check_scan(const gdn_scan_desc* d, bool forward, Scan* s) {
     if (d == nullptr) return GDN_ERR_INVALID;
     if (d->S != 8 && d->S != 16 && d->S != 32 && d->S != 64) return GDN_ERR_UNSUPPORTED;
     if (d->D < 1 || d->G < 1 || d->D % d->G != 0 || d->D / d->G % 8 != 0) return GDN_ERR_INVALID;
@@ -279,9 +317,8 @@ gdn_status check_scan(const gdn_scan_desc* d, int alone, Scan* s) {
     // Segments. A cut costs a second walk (summary and main take 0.7 and 1 of a
     // whole walk's time) and two launches with a merge between. So nothing is cut
     // unless one sequence takes longer, on a compute unit of its own, than both
-    // walks of everything on all 256 (whole and cut: T=8192 in 6 documents, D=4096
-    // 331 and 254 us; D=1024, one sequence of T=96 13.7 and 18.3, 128 17.2 and 19.7,
-    // 160 20.7 and 18.2, with gradients T=96 54 and 57, 128 67 and 56).
+    // walks of everything on all 256 (with gradients D=1024, one sequence of T=96
+    // whole and cut 54 and 57 us, 128 67 and 56).
     // Four workgroups run on a unit at a time and share its issue, so all take about
     // as long as the most of them on one unit, at segments of P tokens (and 10 for a
     // start); where fewer are left, instructions wait (kRest). Of 2 to 8 on a unit the best (3 documents,
@@ -291,7 +328,9 @@ gdn_status check_scan(const gdn_scan_desc* d, int alone, Scan* s) {
     const int64_t tile = gdn::SCAN_TILE, whole = (q.longest + tile - 1) / tile * tile;
     const int64_t walks = int64_t(a.G) * a.blocks;
     int64_t P = whole > 0 ? whole : tile;
-    if (q.longest > 1.4 * double(total) * walks / 256 + alone) {
+    const bool few = forward && int64_t(q.un.n_units) * a.G * a.bwd_blocks < 512;
+    a.narrow = few && whole_pays(a, d->offsets_host, q.longest, P);
+    if (few ? !a.narrow : q.longest > 1.4 * double(total) * walks / 256 + (forward ? 130 : 85)) {
         const int64_t least = ((int64_t)sqrt(0.44 * double(q.longest)) + tile) / tile * tile, most = P;
         const bool many = q.un.n_units > 64;   // sequences to count through: four a unit it is
         constexpr double kRest[4] = {0, 1.7, 2.4, 3.15};
@@ -339,7 +378,7 @@ void scan_inputs(ScanArgs* a, const void* u, const void* dt, const float* A, con
 
 extern "C" int64_t gdn_scan_h_rows(const gdn_scan_desc* d) {
     Scan s;
-    return check_scan(d, 130, &s) == GDN_OK ? s.a.keep.n_pieces : -1;
+    return check_scan(d, true, &s) == GDN_OK ? s.a.keep.n_pieces : -1;
 }
 
 extern "C" gdn_status gdn_scan_fwd(const gdn_scan_desc* d, const void* u, const void* dt, const float* A,
@@ -348,7 +387,7 @@ extern "C" gdn_status gdn_scan_fwd(const gdn_scan_desc* d, const void* u, const 
                                    const int32_t* out_pages, int32_t n_pages, float* h, void* out, void* workspace,
                                    size_t* workspace_bytes, hipStream_t stream) {
     Scan s;
-    gdn_status st = check_scan(d, 130, &s);
+    gdn_status st = check_scan(d, true, &s);
     if (st != GDN_OK) return st;
     bool query = false;
     st = check_workspace(s.slots + s.sums, workspace, workspace_bytes, &query);
@@ -386,7 +425,7 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
                                    float* ddt_bias, float* dh0, void* workspace, size_t* workspace_bytes,
                                    hipStream_t stream) {
     Scan s;
-    gdn_status st = check_scan(d, 85, &s);
+    gdn_status st = check_scan(d, false, &s);
     if (st != GDN_OK) return st;
     ScanArgs& a = s.a;
     const int64_t walks = int64_t(a.G) * a.bwd_blocks;
@@ -438,7 +477,7 @@ extern "C" gdn_status gdn_scan_step(const gdn_scan_desc* d, const void* u, const
                                     void* out, hipStream_t stream) {
     if (d != nullptr && d->B == 0 && d->T == 1) return GDN_OK;
     Scan s;
-    const gdn_status st = check_scan(d, 130, &s);
+    const gdn_status st = check_scan(d, true, &s);
     if (st != GDN_OK) return st;
     if (d->T != 1 || d->n_units != 0 || n_pages < 0) return GDN_ERR_INVALID;
     ScanArgs& a = s.a;

@@ -71,6 +71,7 @@ struct ScanArgs {
     MxUnits keep;             // the same with P = SCAN_KEEP: rows of h
     int32_t cut;              // some sequence has more than one segment
     int32_t join;             // a segment adds up those before it itself, no merge
+    int32_t narrow;           // forward: a lane holds one state, nothing is cut
     int32_t D, G, S, dtype, softplus, n_pages;
     int32_t blocks, bwd_blocks;   // of channels in a group; the backward's workgroups hold half as many
     const void *u, *dt, *gate, *b, *c;
@@ -92,6 +93,7 @@ struct ScanArgs {
 };
 // channels of a workgroup
 constexpr int scan_channels(int S) { return S == 8 ? 128 : 2048 / S; }
+constexpr int scan_narrow_channels(int S) { return S == 8 ? 32 : 16; }
 hipError_t launch_scan_summary(const ScanArgs& a, bool reverse, hipStream_t s);
 hipError_t launch_scan_merge(const ScanArgs& a, bool reverse, hipStream_t s);
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s);

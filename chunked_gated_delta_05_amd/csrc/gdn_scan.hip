@@ -52,15 +52,16 @@ struct Lane {
         at = (int64_t)d * S + 4 * sl;
     }
 };
-template <int K>
-__device__ __forceinline__ void load_states(f32x4 (&h)[K], const float* p, int S) {
+// K vectors, `step` values apart
+template <typename V, int K>
+__device__ __forceinline__ void load_states(V (&h)[K], const float* p, int step) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) h[k] = *reinterpret_cast<const f32x4*>(p + k * S);
+    for (int k = 0; k < K; ++k) h[k] = *reinterpret_cast<const V*>(p + k * step);
 }
-template <int K>
-__device__ __forceinline__ void store_states(float* p, const f32x4 (&h)[K], int S) {
+template <typename V, int K>
+__device__ __forceinline__ void store_states(float* p, const V (&h)[K], int step) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) *reinterpret_cast<f32x4*>(p + k * S) = h[k];
+    for (int k = 0; k < K; ++k) *reinterpret_cast<V*>(p + k * step) = h[k];
 }
 
 // Channels of this workgroup: [ch, ch_end) in group g
@@ -112,6 +113,19 @@ struct States {
             const T* p = j >= NB / 2 ? static_cast<const T*>(a.c) + t * a.c_stride[0] + g * a.c_stride[1]
                                      : static_cast<const T*>(a.b) + t * a.b_stride[0] + g * a.b_stride[1];
             x[i] = load4(p + 4 * (r % Sh::SV));
+        }
+    }
+    // the same as [2][S][pitch], tokens along a row
+    __device__ __forceinline__ void put_turned(float* at, int pitch, int t0, int end) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = threadIdx.x + i * Sh::NT;
+            if (NB % Sh::NT != 0 && j >= NB) break;
+            const int t = j % (NB / 2) / Sh::SV;
+            const f32x4 v = t0 + t < end ? Four<T>::wide(x[i]) : f32x4{0, 0, 0, 0};
+            float* o = at + (j / (NB / 2) * 4 * Sh::SV + j % Sh::SV * 4) * pitch + t;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k * pitch] = v[k];
         }
     }
     // zero past the end
@@ -308,6 +322,237 @@ __global__ __launch_bounds__((Shape<S, K>::NT), (sizeof(T) == 2 && S > 8 && K ==
     if (a.s_out && pc.end == pc.seq.len && l.mine) {
         const int64_t page = page_of(a.out_pages, a.n_pages, pc.unit);
         if (page >= 0) store_states(a.s_out + page * page_size + l.at, h, S);
+    }
+}
+
+// The same for whole sequences of few channels: a lane holds one state (of 32 and
+// 64 states two and four), so that few sequences need not be cut, and walked
+// twice, to fill the card (six prompts, T=8192 D=4096: 233 us cut, 180 so; T=160
+// D=1024 15.6 and 9.6). A token costs a lane 10 instructions where the lane of
+// eight states takes 7.5 a state: sums over 16 lanes, and dt and dt u from another
+// lane. Two waves a SIMD issue one every 4 cycles, one wave every 7.
+constexpr int NARROW_TILE = 64;
+template <int S>
+struct Narrow {
+    static constexpr int Q = S <= 16 ? 1 : S / 16;  // states of a lane, LPC apart
+    static constexpr int LPC = S / Q, CPW = 64 / LPC, NW = 4, NT = 64 * NW, CH = CPW * NW, V = CH / 4, SV = S / 4;
+    static_assert(CH == scan_narrow_channels(S), "");
+    static __device__ __host__ __forceinline__ int blocks(const ScanArgs& a) { return (a.D / a.G + CH - 1) / CH; }
+};
+typedef float f32x1 __attribute__((ext_vector_type(1)));
+template <int S>
+struct NarrowLane {
+    static constexpr int STEP = Narrow<S>::LPC;    // from a state to the next
+    int lane, c, sl, d;
+    bool mine;
+    int64_t at;
+    __device__ __forceinline__ NarrowLane(int ch, int ch_end) {
+        lane = threadIdx.x & 63;
+        c = (threadIdx.x >> 6) * Narrow<S>::CPW + lane / Narrow<S>::LPC;
+        sl = lane % Narrow<S>::LPC;
+        mine = ch + c < ch_end;
+        d = mine ? ch + c : ch_end - 1;
+        at = (int64_t)d * S + sl;
+    }
+};
+// a and b added up with the partner lane's: lanes below it get a's sum, those above b's
+template <int CTRL>
+__device__ __forceinline__ float fold(float a, float b, bool above) {
+    return (above ? b : a) + dpp<CTRL>(above ? a : b);
+}
+// Sixteen values over 16 lanes twice so, from 16 to 4 a lane: lanes 4 g .. 4 g + 3
+// get values 4 g .. 4 g + 3 in y[0 .. 3], added up over the other quads. Adds that
+// write only some quads take the place of the selects (119 to 114 us for 5
+// prompts of T=1000 D=4096). A value is exchanged two waits or more after it was
+// written, the one at the end for what follows.
+__device__ __forceinline__ void fold16(float (&y)[16]) {
+#define GDN_HALVES(a, b) \
+    "v_add_f32_dpp " a ", " a ", " a " row_ror:8 row_mask:0xf bank_mask:0x3\n" \
+    "v_add_f32_dpp " a ", " b ", " b " row_ror:8 row_mask:0xf bank_mask:0xc\n"
+#define GDN_QUADS(a, b) \
+    "v_add_f32_dpp " a ", " a ", " a " row_half_mirror row_mask:0xf bank_mask:0x5\n" \
+    "v_add_f32_dpp " a ", " b ", " b " row_half_mirror row_mask:0xf bank_mask:0xa\n"
+    asm("s_nop 1\n"
+        GDN_HALVES("%0", "%8") GDN_HALVES("%1", "%9") GDN_HALVES("%2", "%10") GDN_HALVES("%3", "%11")
+        GDN_HALVES("%4", "%12") GDN_HALVES("%5", "%13") GDN_HALVES("%6", "%14") GDN_HALVES("%7", "%15")
+        "s_nop 1\n"
+        GDN_QUADS("%0", "%4") GDN_QUADS("%1", "%5") GDN_QUADS("%2", "%6") GDN_QUADS("%3", "%7")
+        "s_nop 1"
+        : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]), "+v"(y[4]), "+v"(y[5]), "+v"(y[6]), "+v"(y[7])
+        : "v"(y[8]), "v"(y[9]), "v"(y[10]), "v"(y[11]), "v"(y[12]), "v"(y[13]), "v"(y[14]), "v"(y[15]));
+#undef GDN_HALVES
+#undef GDN_QUADS
+}
+
+template <typename F, int... I>
+__device__ __forceinline__ void unrolled_(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+// f of the constants 0 .. N - 1
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+    unrolled_(f, std::make_integer_sequence<int, N>());
+}
+
+template <typename T, int S>
+__global__ __launch_bounds__(Narrow<S>::NT, 2) void scan_narrow_kernel(ScanArgs a) {
+    typedef Narrow<S> Sh;
+    constexpr int TT = NARROW_TILE, Q = Sh::Q, E = Q == 1 ? 8 : 4;   // E tokens' operands are read at a time
+    typedef Rows<T, Sh, TT> Rw;
+    // tokens along the rows, which are padded for the banks: 16 rows' next four tokens are read at once
+    __shared__ __align__(16) f32x2 xs[Sh::CH][TT + 4];      // dt, dt u
+    __shared__ __align__(16) float bc[2][S][TT + 4];
+    __shared__ __align__(16) float ys[Sh::CH][TT + 4];
+
+    const int nb = a.G * Sh::blocks(a);
+    int blk = blockIdx.x % nb;
+    if (nb % 8 == 0) blk = blk % 8 * (nb / 8) + blk / 8;    // neighbours share cache lines: on one die
+    const Block k = block_of<Sh>(a, blk);
+    const int piece = blockIdx.x / nb;
+    const Piece pc = piece_of(a.un, piece);
+    if (pc.none) return;
+    const NarrowLane<S> l(k.ch, k.ch_end);
+    const int64_t page_size = (int64_t)a.D * S;
+    f32x1 A2[Q], h[Q] = {};
+    load_states(A2, a.A + l.at, l.STEP);
+#pragma unroll
+    for (int i = 0; i < Q; ++i) A2[i] *= LOG2E;
+    if (a.s_in) {
+        const int64_t page = page_of(a.in_pages, a.n_pages, pc.unit);
+        if (page >= 0) load_states(h, a.s_in + page * page_size + l.at, l.STEP);
+    }
+    float* keep = a.h ? a.h + piece_base(a.keep, pc.unit, pc.seq.start) * page_size + l.at : nullptr;
+
+    const int cv = threadIdx.x % Sh::V;
+    const bool cv_ok = k.ch + 4 * cv < k.ch_end;
+    const int cch = min(k.ch + 4 * cv, k.ch_end - 4);
+    const f32x4 bias = load_f4(a.dt_bias, cch), skip = load_f4(a.skip, cch);
+    const Rw ru(a.u, pc.seq.start, a.u_stride, cch), rt(a.dt, pc.seq.start, a.dt_stride, cch),
+        rg(a.gate, pc.seq.start, a.gate_stride, cch), ro(a.out, pc.seq.start, a.D, cch);
+    typename Four<T>::raw u[Rw::NV], dt[Rw::NV], gate[Rw::NV] = {};
+    States<T, Sh, TT> st;
+    auto load = [&](int t0) {
+        ru.load(u, t0, pc.end, a.D);
+        rt.load(dt, t0, pc.end, a.D);
+        if (a.gate) rg.load(gate, t0, pc.end, a.D);
+        st.load(a, k.g, pc.seq.start, t0, pc.end);
+    };
+    if (pc.first < pc.end) load(pc.first);
+    for (int t0 = pc.first; t0 < pc.end; t0 += TT) {
+        typename Four<T>::raw own_u[Rw::NV], own_gate[Rw::NV];
+#pragma unroll
+        for (int i = 0; i < Rw::NV; ++i) {
+            own_u[i] = u[i];
+            own_gate[i] = gate[i];
+            f32x4 t = step_sizes(Four<T>::wide(dt[i]) + bias, a.softplus);
+            if (t0 + Rw::row(i) >= pc.end) t = f32x4{0, 0, 0, 0};   // a decay of 1, no input
+            const f32x4 du = t * Four<T>::wide(u[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xs[4 * cv + j][Rw::row(i)] = f32x2{t[j], du[j]};
+        }
+        st.put_turned(&bc[0][0][0], TT + 4, t0, pc.end);
+        lds_barrier();
+        if (t0 + TT < pc.end) load(t0 + TT);
+
+        const int n = min(TT, pc.end - t0);
+        // Of a channel with 16 lanes each lane holds one token's dt and dt u, which an
+        // exchange hands to the others on its way into the product.
+        constexpr bool HELD = Sh::LPC == 16;
+        struct Step {
+            f32x4 x[HELD ? 1 : E / 2], b[Q][E / 4], c[Q][E / 4];
+        };
+        auto read = [&](Step& s, int t) {
+            if constexpr (!HELD) {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) s.x[e] = *reinterpret_cast<const f32x4*>(&xs[l.c][t + 2 * e]);
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) {
+                    s.b[i][e] = *reinterpret_cast<const f32x4*>(&bc[0][l.sl + i * l.STEP][t + 4 * e]);
+                    s.c[i][e] = *reinterpret_cast<const f32x4*>(&bc[1][l.sl + i * l.STEP][t + 4 * e]);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        float y[16];
+        f32x2 held = {0, 0};
+        auto step = [&](const Step& s, auto first) {
+            unrolled<E>([&](auto e) {
+                float d, du;
+                if constexpr (HELD) {
+                    d = dpp<ROW_BCAST + first + e>(held[0]);
+                    du = dpp<ROW_BCAST + first + e>(held[1]);
+                } else {
+                    d = s.x[e / 2][e % 2 * 2];
+                    du = s.x[e / 2][e % 2 * 2 + 1];
+                }
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    h[i][0] = fmaf(__builtin_amdgcn_exp2f(d * A2[i][0]), h[i][0], du * s.b[i][e / 4][e % 4]);
+                    sum = i ? fmaf(s.c[i][e / 4][e % 4], h[i][0], sum) : s.c[i][e / 4][e % 4] * h[i][0];
+                }
+                y[first + e] = sum;
+            });
+        };
+        Step even, odd;
+        f32x2 next = xs[l.c][HELD ? l.sl : 0];
+        read(even, 0);
+#pragma unroll 1
+        for (int q = 0; q < n; q += 16) {
+            static_assert(SCAN_KEEP == 16, "");
+            if (keep && l.mine) store_states(keep + (t0 + q) / SCAN_KEEP * page_size, h, l.STEP);
+            held = next;
+            if (HELD) next = xs[l.c][min(q + 16, TT - 16) + l.sl];
+            unrolled<16 / (2 * E)>([&](auto i) {
+                constexpr int e = i * 2 * E;
+                read(odd, q + e + E);
+                step(even, std::integral_constant<int, e>());
+                read(even, min(q + e + 2 * E, TT - E));
+                step(odd, std::integral_constant<int, e + E>());
+            });
+            // the sums over states of 16 tokens: each exchange halves the tokens of a lane
+            constexpr int NR = Sh::LPC == 16 ? 1 : 2;
+            f32x4 r[NR];
+            if constexpr (Sh::LPC == 16) fold16(y);
+#pragma unroll
+            for (int i = 0; i < 4 * NR; ++i) {
+                float v = Sh::LPC == 16 ? y[i] : fold<HALF_MIRROR>(y[i], y[(i + 8) % 16], l.lane & 4);
+                v += dpp<QUAD_XOR1>(v);
+                v += dpp<QUAD_XOR2>(v);
+                r[i / 4][i % 4] = v;
+            }
+            if ((l.lane & 3) == 0) {
+                float* to = &ys[l.c][q];
+                if constexpr (Sh::LPC == 16) {
+                    *reinterpret_cast<f32x4*>(to + (l.lane & 12)) = r[0];
+                } else {
+                    *reinterpret_cast<f32x4*>(to + 2 * (l.lane & 4)) = r[0];
+                    *reinterpret_cast<f32x4*>(to + 2 * (l.lane & 4) + 4) = r[1];
+                }
+            }
+        }
+        lds_barrier();
+        const rsrc_t out = ro.tile(t0, pc.end, a.D);
+#pragma unroll
+        for (int i = 0; i < Rw::NV; ++i) {
+            if (!cv_ok) continue;
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = ys[4 * cv + j][Rw::row(i)];
+            v += skip * Four<T>::wide(own_u[i]);
+            if (a.gate) {
+                const f32x4 g = Four<T>::wide(own_gate[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] *= g[j] * sigmoid1(g[j]);
+            }
+            buffer_store4<T>(out, ro.lane, ro.bytes(i), v);
+        }
+    }
+    if (a.s_out && pc.end == pc.seq.len && l.mine) {
+        const int64_t page = page_of(a.out_pages, a.n_pages, pc.unit);
+        if (page >= 0) store_states(a.s_out + page * page_size + l.at, h, l.STEP);
     }
 }
 
@@ -838,10 +1083,12 @@ hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) {
     return by_type(a.dtype, a.S, [&](auto t, auto n) {
         typedef Shape<n(), 2> Two;
         typedef Shape<n(), 1> One;
+        typedef Narrow<n()> Few;
         // Fewer workgroups than two a compute unit hold half the channels each, which
-        // are then twice as many (T=61 D=512: 14.5 to 10.5 us, B=5 T=1000 D=4096, 160
-        // of them, 183 to 157; 512 of them 266 and 289).
-        if (grid_of<Two>(a) >= 512) scan_fwd_kernel<decltype(t), n(), 2><<<grid_of<Two>(a), Two::NT, 0, s>>>(a);
+        // are then twice as many (B=8 T=1000 D=4096, 256 of them, 183 to 156 us; 512 of
+        // them 266 and 289).
+        if (a.narrow) scan_narrow_kernel<decltype(t), n()><<<grid_of<Few>(a), Few::NT, 0, s>>>(a);
+        else if (grid_of<Two>(a) >= 512) scan_fwd_kernel<decltype(t), n(), 2><<<grid_of<Two>(a), Two::NT, 0, s>>>(a);
         else scan_fwd_kernel<decltype(t), n(), 1><<<grid_of<One>(a), One::NT, 0, s>>>(a);
     });
 }

@@ -108,6 +108,11 @@ hipError_t launch_scan_merge(const ScanArgs& a, bool, hipStream_t) {
 }
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t) {
     check_scan(a);
+    if (a.narrow) {
+        if (a.cut) fail("one state a lane and cut");
+        const int ch = scan_narrow_channels(a.S);
+        in_grid(int64_t(a.un.n_pieces) * a.G * ((a.D / a.G + ch - 1) / ch));
+    }
     return hipSuccess;
 }
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t) {

@@ -20,7 +20,8 @@ pytestmark = pytest.mark.gpu
 # ------------------------------------------------------------------ scan
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("lead,D,S", [((520, 40), 16, 16),            # uncut, two channels a lane
-                                      ((1, 400), 136, 16),             # cut, one
+                                      ((300, 20), 128, 16),            # one
+                                      ((1, 600), 136, 16), ((1, 900), 40, 64), ((1, 900), 40, 32), ((1, 900), 72, 8),   # cut, one
                                       ([1] * 300 + [40, 3], 16, 16),   # sums over more than 256 pieces
                                       ([700, 1, 300], 64, 8)])
 def test_scan_paths(lead, D, S, dtype):
@@ -38,13 +39,23 @@ def test_scan_cut_with_two_channels_a_lane():
     near(final, want[1], scale[1], 24 * 2048 + 64, "final")
 
 
-def test_scan_wide_equals_narrow():
-    # the same sequence alone (one channel a lane) and among many (two)
-    c = scan_case((520, 37), 16, 16, 1, "bf16", seed=9)
+@pytest.mark.parametrize("S", [8, 16, 32, 64])
+def test_scan_of_one_sequence_alone_and_among_others(S):
+    # 520 sequences (two channels a lane), 300 (one) and one (one state a lane, or so): the same states; sums over
+    # states in another order, within S + 2 steps of fp32 on either side and a rounding to bf16
+    D = 128 if S == 8 else 2048 // S
+    c = scan_case((520, 37), D, S, 1, "bf16", seed=9)
     out, final, h = scan_gpu(c, want_h=True)
+    some = dict(c, **{k: c[k][:300].contiguous() for k in ("u", "dt", "gate", "B", "C", "s0")})
+    o, f, hh = scan_gpu(some, want_h=True)
+    assert torch.equal(o, out[:300]) and torch.equal(f, final[:300]) and torch.equal(hh, h[:900])
     one = dict(c, **{k: c[k][77:78].contiguous() for k in ("u", "dt", "gate", "B", "C", "s0")})
     o, f, hh = scan_gpu(one, want_h=True)
-    assert torch.equal(o[0], out[77]) and torch.equal(f[0], final[77]) and torch.equal(hh, h[77 * 3:78 * 3])
+    assert torch.equal(f[0], final[77]) and torch.equal(hh, h[77 * 3:78 * 3])
+    a = [x if x is None or not torch.is_tensor(x) or x.dim() < 3 else x[77:78] for x in scan_args(c)]
+    a[9], a[11], a[12] = [0, 37], None, None
+    _, scale = ref.scan(*a)[0], ref.scan(*a, absolute=True)[0]
+    near(o[0], out[77].double().cpu(), 2 * (S + 2) * scale + out[77].double().cpu().abs() * 2 ** 16, 1, "out")
 
 
 @pytest.mark.parametrize("lead", [(2, 400), [400, 1, 90]])
