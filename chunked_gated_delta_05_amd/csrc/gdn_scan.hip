@@ -152,6 +152,11 @@ __device__ __forceinline__ f32x4 step_sizes(f32x4 raw, int softplus) {
     return r;
 }
 
+// All that was loaded has arrived. Before a tile's stores and the first tile: the
+// loads of the next one, issued a tile ago, would else be waited for behind the
+// stores (B=2 T=4096 D=4096 215 to 207 us, with gradients 763 to 757).
+__device__ __forceinline__ void wait_for_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
 // ------------------------------------------------------------------ segments
 // The states that a segment is entered with, or in reverse the gradients: those
 // in front of the sequence and the segments' own between, added up by the segment
@@ -234,6 +239,7 @@ __global__ __launch_bounds__((Shape<S, K>::NT), (sizeof(T) == 2 && S > 8 && K ==
         st.load(a, k.g, pc.seq.start, t0, pc.end);
     };
     if (pc.first < pc.end) load(pc.first);
+    wait_for_loads();
     for (int t0 = pc.first; t0 < pc.end; t0 += TT) {
         typename Four<T>::raw own_u[Rw::NV], own_gate[Rw::NV];
 #pragma unroll
@@ -306,6 +312,7 @@ __global__ __launch_bounds__((Shape<S, K>::NT), (sizeof(T) == 2 && S > 8 && K ==
             step(odd, q + E);
         }
         lds_barrier();
+        wait_for_loads();
         const rsrc_t out = ro.tile(t0, pc.end, a.D);
 #pragma unroll
         for (int i = 0; i < Rw::NV; ++i) {
@@ -438,6 +445,7 @@ __global__ __launch_bounds__(Narrow<S>::NT, 2) void scan_narrow_kernel(ScanArgs 
         st.load(a, k.g, pc.seq.start, t0, pc.end);
     };
     if (pc.first < pc.end) load(pc.first);
+    wait_for_loads();
     for (int t0 = pc.first; t0 < pc.end; t0 += TT) {
         typename Four<T>::raw own_u[Rw::NV], own_gate[Rw::NV];
 #pragma unroll
@@ -534,6 +542,7 @@ __global__ __launch_bounds__(Narrow<S>::NT, 2) void scan_narrow_kernel(ScanArgs 
             }
         }
         lds_barrier();
+        wait_for_loads();
         const rsrc_t out = ro.tile(t0, pc.end, a.D);
 #pragma unroll
         for (int i = 0; i < Rw::NV; ++i) {
@@ -795,6 +804,7 @@ __global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs
         };
         const int last = pc.first + (pc.end - pc.first - 1) / TT * TT;
         if (pc.first < pc.end) load(last);
+        wait_for_loads();
         for (int t0 = last; t0 >= pc.first && pc.first < pc.end; t0 -= TT) {
             typename Four<T>::raw own_u[Rw::NV], own_dt[Rw::NV], own_gate[Rw::NV], own_dout[Rw::NV];
 #pragma unroll
@@ -889,6 +899,7 @@ __global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs
                 __builtin_amdgcn_sched_barrier(0);
             }
             lds_barrier();
+            wait_for_loads();
             // dB and dC of this workgroup's channels
             const int n = min(TT, pc.end - t0);
             for (int i = threadIdx.x; i < n * 2 * Sh::SV; i += Sh::NT) {
