@@ -11,9 +11,13 @@
 // over states cross few lanes and B and C are read from LDS once for both; what
 // belongs to a token and channel (the softplus, the products with u, the gate)
 // is computed once, by the thread that loads it.
-// Sequences are cut into segments where their channels alone would not fill the
-// card, whose own states are summed up first (summary), carried over (merge) and
-// then entered with.
+// Whole sequences of few channels are walked by one state a lane. Where even that
+// would not fill the card sequences are cut into segments, whose own states are
+// summed up first (summary), carried over (merge) and then entered with.
+// bf16, S = 16, 537 million states times tokens (T=8192 D=4096; 268 MB would take
+// 55 us): 185 us in six prompts, 207 in two rows, 224 in one, cut; 262 of 16 rows
+// of T=1000 by two channels a lane; two rows with their gradients 755, 455 of them
+// the gradients' walk.
 #include "gdn_mixer_device.h"
 
 namespace gdn {
@@ -200,6 +204,9 @@ __device__ __forceinline__ void entry_states(const ScanArgs& a, const Piece& pc,
 }
 
 // ------------------------------------------------------------------ prompts
+// Four waves a SIMD where 128 registers hold what two channels of bf16 need (a
+// training step's forward in 16 segments 9 us faster; one channel a lane, which
+// would spill, 274 to 346 in 9 documents).
 template <typename T, int S, int K>
 __global__ __launch_bounds__((Shape<S, K>::NT), (sizeof(T) == 2 && S > 8 && K == 2 ? 4 : 2)) void scan_fwd_kernel(ScanArgs a) {
     typedef Shape<S, K> Sh;
@@ -1000,8 +1007,9 @@ __device__ __forceinline__ float decayed(float h, float x) {
     return fabsf(x) < 0.25f ? fmaf(h * x, p, h) : h * __builtin_amdgcn_exp2f(x * LOG2E);
 }
 
-// Bound by the bytes of the states, read once and written once; a thread holds
-// four values of the state of N sequences. AROUND: past the caches
+// Bound by the bytes of the states, read once and written once (256 sequences of
+// D=8192 55 us, 5.2 TB/s); a thread holds four values of the state of N sequences.
+// AROUND: past the caches
 template <typename T, int S, int N, bool AROUND>
 __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
     constexpr int LPC = S / 4;
