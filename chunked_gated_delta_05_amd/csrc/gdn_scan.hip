@@ -369,20 +369,24 @@ struct NarrowLane {
         at = (int64_t)d * S + sl;
     }
 };
+// In assembly: a and b added up with those 8 lanes away in a row of 16, a's sum in
+// the lower lanes of a, b's in the upper ones. Adds that write only some quads
+// take the place of selects; a value is exchanged two waits or more after it was
+// written.
+#define GDN_HALVES(a, b) \
+    "v_add_f32_dpp " a ", " a ", " a " row_ror:8 row_mask:0xf bank_mask:0x3\n" \
+    "v_add_f32_dpp " a ", " b ", " b " row_ror:8 row_mask:0xf bank_mask:0xc\n"
+
 // a and b added up with the partner lane's: lanes below it get a's sum, those above b's
 template <int CTRL>
 __device__ __forceinline__ float fold(float a, float b, bool above) {
     return (above ? b : a) + dpp<CTRL>(above ? a : b);
 }
 // Sixteen values over 16 lanes twice so, from 16 to 4 a lane: lanes 4 g .. 4 g + 3
-// get values 4 g .. 4 g + 3 in y[0 .. 3], added up over the other quads. Adds that
-// write only some quads take the place of the selects (119 to 114 us for 5
-// prompts of T=1000 D=4096). A value is exchanged two waits or more after it was
-// written, the one at the end for what follows.
+// get values 4 g .. 4 g + 3 in y[0 .. 3], added up over the other quads (with
+// selects 5 prompts of T=1000 D=4096 take 115 us, so 111). The wait at the end is
+// for what follows.
 __device__ __forceinline__ void fold16(float (&y)[16]) {
-#define GDN_HALVES(a, b) \
-    "v_add_f32_dpp " a ", " a ", " a " row_ror:8 row_mask:0xf bank_mask:0x3\n" \
-    "v_add_f32_dpp " a ", " b ", " b " row_ror:8 row_mask:0xf bank_mask:0xc\n"
 #define GDN_QUADS(a, b) \
     "v_add_f32_dpp " a ", " a ", " a " row_half_mirror row_mask:0xf bank_mask:0x5\n" \
     "v_add_f32_dpp " a ", " b ", " b " row_half_mirror row_mask:0xf bank_mask:0xa\n"
@@ -394,7 +398,6 @@ __device__ __forceinline__ void fold16(float (&y)[16]) {
         "s_nop 1"
         : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]), "+v"(y[4]), "+v"(y[5]), "+v"(y[6]), "+v"(y[7])
         : "v"(y[8]), "v"(y[9]), "v"(y[10]), "v"(y[11]), "v"(y[12]), "v"(y[13]), "v"(y[14]), "v"(y[15]));
-#undef GDN_HALVES
 #undef GDN_QUADS
 }
 
@@ -727,30 +730,50 @@ __global__ __launch_bounds__(NT) void scan_merge_kernel(ScanArgs a, int blocks) 
 
 // ------------------------------------------------------------------ gradients
 // dB and dC are sums over channels, which lie across lanes. Their terms of four
-// tokens (two vectors of four states a lane and token) go through LDS, where a
-// lane finds one vector's terms of eight channels: 2 sums for each element where
-// exchanges of lanes take 5 and the matrix unit, which holds up the vector units
-// in fp32, 64 cycles (B=2 T=4096 D=4096: 455 us, exchanges 750, products with
-// ones 670).
+// tokens (two vectors of four states a lane and token) are added up over lanes 8
+// apart, which leaves one vector a lane, and go through LDS, where a lane finds
+// one vector's terms of eight channels: 3 operations for each element where
+// exchanges of lanes alone take 5 and the matrix unit, which holds up the vector
+// units in fp32, 64 cycles (B=2 T=4096 D=4096: 430 us; both vectors through LDS
+// 455, exchanges 750, products with ones 670; factors from LDS, in the sums, 470).
 template <int S>
 struct ChannelSums {
     static constexpr int LPC = S / 4, OUT = 8 * LPC;           // vectors that come out
+    static constexpr bool FOLD = LPC < 16;                     // a row of 16 lanes has two channels or more
     static constexpr int SHARE = LPC < 8 ? 8 / LPC : 1;        // lanes of one of them
-    static constexpr int TERMS = LPC < 16 ? 8 : 4, ROUNDS = 8 / TERMS;
+    static constexpr int ROUNDS = FOLD ? 1 : 2, VECTORS = FOLD ? 1 : 2;   // of a lane and token
     int first, turn;
     // the terms are read in an order that keeps 16 neighbouring lanes on different banks
     __device__ __forceinline__ ChannelSums(int lane) {
-        const int o = lane / SHARE, part = lane % SHARE;
-        first = o / LPC * 64 + part * 8 * LPC + o % LPC;
-        turn = LPC < 16 ? o / LPC % 2 * SHARE + part : 0;
+        const int o = lane / SHARE, row = o / LPC;
+        turn = lane % SHARE;
+        first = (FOLD ? row / 2 * 64 + row % 2 * 8 : row * 64) + o % LPC;
     }
-    // p: this wave's vectors [token][dB, dC][lane]; out: [token][dB, dC][S / 4]
+    // A token's terms: dB's, added up over pairs of lanes, in the lower halves of
+    // the rows, dC's in the upper ones
+    static __device__ __forceinline__ void put(f32x4 (&to)[VECTORS][64], f32x4 b, f32x4 c, int lane) {
+        if constexpr (FOLD) {
+            float v[4] = {b[0], b[1], b[2], b[3]};
+            asm("s_nop 1\n" GDN_HALVES("%0", "%4") GDN_HALVES("%1", "%5") GDN_HALVES("%2", "%6") GDN_HALVES("%3", "%7")
+                : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])
+                : "v"(c[0]), "v"(c[1]), "v"(c[2]), "v"(c[3]));
+            to[0][lane] = f32x4{v[0], v[1], v[2], v[3]};
+        } else {
+            to[0][lane] = b;
+            to[1][lane] = c;
+        }
+    }
+    // p: this wave's vectors [token][VECTORS][lane]; out: [token][dB, dC][S / 4]
     __device__ __forceinline__ void sum(const f32x4* p, f32x4* out, int lane) const {
+        constexpr int PER = FOLD ? 8 / LPC : 1;    // terms of a row of lanes
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
             f32x4 s = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < TERMS; ++i) s += p[first + r * (64 / LPC) * 64 + ((i + turn) & 7) * LPC];
+            for (int i = 0; i < 4; ++i) {
+                const int k = turn * 4 + ((i + turn) & 3);
+                s += p[first + r * 4 * 64 + k / PER * 16 + k % PER * LPC];
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = lane_sum<SHARE>(s[j]);
             out[lane / SHARE + r * 64] = s;
@@ -768,7 +791,7 @@ __global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs
     __shared__ f32x4 bc[2 * TT * Sh::SV];
     __shared__ __align__(16) float sums[3][TT][Sh::CH + 4];   // over states: B g, E h A, C h
     __shared__ f32x4 parts[Sh::NW][TT][2 * Sh::SV];  // over a wave's channels: dB, dC
-    __shared__ f32x4 terms[Sh::NW][4][2][64];        // of four tokens, by lanes
+    __shared__ f32x4 terms[Sh::NW][4][ChannelSums<S>::VECTORS][64];   // of four tokens, by lanes
 
     const int nb = a.G * Sh::blocks(a), blk = blockIdx.x % nb;
     const Block k = block_of<Sh>(a, blk);
@@ -888,11 +911,11 @@ __global__ __launch_bounds__((Shape<S, 1>::NT), 2) void scan_bwd_kernel(ScanArgs
                         s1 = j ? fmaf(w, A2[j], s1) : w * A2[j];
                         dA[j] = fmaf(w, x[0], dA[j]);
                     }
-                    terms[l.wave][e][0][l.lane] = pb;
-                    terms[l.wave][e][1][l.lane] = pcv;
+                    channels.put(terms[l.wave][e], pb, pcv, l.lane);
                     su[e] = s0;
                     sa[e] = s1;
                 }
+                asm volatile("" : "+v"(dA));         // else added up at the tile's end, its terms in registers until then
                 __builtin_amdgcn_wave_barrier();     // a wave's LDS accesses keep their order
                 channels.sum(&terms[l.wave][0][0][0], &parts[l.wave][t][0], l.lane);
                 __builtin_amdgcn_wave_barrier();
