@@ -16,7 +16,7 @@
 // summed up first (summary), carried over (merge) and then entered with.
 // bf16, S = 16, 537 million states times tokens (T=8192 D=4096; 268 MB would take
 // 55 us): 185 us in six prompts, 207 in two rows, 224 in one, cut; 262 of 16 rows
-// of T=1000 by two channels a lane; two rows with their gradients 755, 455 of them
+// of T=1000 by two channels a lane; two rows with their gradients 730, 430 of them
 // the gradients' walk.
 #include "gdn_mixer_device.h"
 
@@ -158,7 +158,7 @@ __device__ __forceinline__ f32x4 step_sizes(f32x4 raw, int softplus) {
 
 // All that was loaded has arrived. Before a tile's stores and the first tile: the
 // loads of the next one, issued a tile ago, would else be waited for behind the
-// stores (B=2 T=4096 D=4096 215 to 207 us, with gradients 763 to 757).
+// stores (B=2 T=4096 D=4096 215 to 207 us, with gradients 1% less).
 __device__ __forceinline__ void wait_for_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
 // ------------------------------------------------------------------ segments
