@@ -5,8 +5,8 @@
 // A token's value costs W products for the two bytes it is read and written
 // with: bound by memory. A thread walks a piece of a sequence for 16 bytes of
 // neighbouring channels with the last W - 1 inputs in registers, so x is read
-// once but for W - 1 tokens in front of each piece (bf16 T=8191 D=6144: 46 us,
-// 4.4 TB/s; B=4 T=4096: 88 us, 4.6, its gradients 152).
+// once but for W - 1 tokens in front of each piece (bf16 T=8191 D=6144: 43.5 us,
+// 4.6 TB/s; B=4 T=4096 with its gradients 224, the gradients' walk 142 of them).
 #include "gdn_mixer_device.h"
 
 namespace gdn {
@@ -133,14 +133,16 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
     };
     if (pc.first < pc.end) load(pc.first);
     entry<T, W, N>(a, pc, pc.first, ch, past);
-    for (int t0 = pc.first; t0 < pc.end; t0 += AT) {
+    // Whole tiles, and the last one apart: where the number of a tile's stores is
+    // fixed the next tile's loads are waited for without them (45.5 to 43.5 us).
+    auto tile = [&](int t0, auto whole) {
         typename Ch::raw now[AT];
 #pragma unroll
         for (int i = 0; i < AT; ++i) now[i] = next[i];
-        if (t0 + AT < pc.end) load(t0 + AT);
+        if (whole()) load(t0 + AT);
 #pragma unroll
         for (int i = 0; i < AT; ++i) {
-            if (t0 + i >= pc.end) break;
+            if (!whole() && t0 + i >= pc.end) break;
             float v[N], z[N];
             Ch::wide(now[i], v);
             taps.apply(past, v, z);
@@ -151,7 +153,10 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
             Ch::store(y + (int64_t)(t0 + i) * a.D, z);
             shift(past, v);
         }
-    }
+    };
+    int t0 = pc.first;
+    for (; t0 + AT <= pc.end; t0 += AT) tile(t0, std::true_type());
+    if (t0 < pc.end) tile(t0, std::false_type());
     if (a.s_out && pc.end == pc.seq.len) leave<T, W, N>(a, pc, ch, past);
 }
 
@@ -212,20 +217,22 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
         };
         if (len > 0) load(pc.first);
         entry<T, W, N>(a, pc, pc.first, ch, past);
-        for (int t0 = pc.first; t0 < stop; t0 += AT) {
+        // inner: of tiles that neither begin nor end the piece, which store as many
+        // tokens each (228 to 224 us; B=2 T=2048 D=2048 36.5 to 33)
+        auto tile = [&](int t0, auto inner) {
             typename Ch::raw cx[AT], cd[AT];
 #pragma unroll
             for (int i = 0; i < AT; ++i) {
                 cx[i] = nx[i];
                 cd[i] = nd[i];
             }
-            if (t0 + AT < stop && len > 0) load(t0 + AT);
+            if (inner() || (t0 + AT < stop && len > 0)) load(t0 + AT);
 #pragma unroll
             for (int i = 0; i < AT; ++i) {
                 const int t = t0 + i;
-                if (t >= stop) break;
+                if (!inner() && t >= stop) break;
                 float v[N], g[N], z[N];
-                if (t < len) {
+                if (inner() || t < len) {
                     Ch::wide(cx[i], v);
                     Ch::wide(cd[i], g);
                     if (a.silu) {
@@ -237,7 +244,7 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
                     for (int n = 0; n < N; ++n) v[n] = g[n] = 0.0f;
                 }
-                if (t < pc.end) {
+                if (inner() || t < pc.end) {
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
                         db[n] += g[n];
@@ -249,7 +256,7 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
                 shift(past, v);
                 shift(dz, g);
                 const int p = t - (W - 1);         // whose gradient is complete
-                if (p < pc.first && pc.first > 0) continue;
+                if (!inner() && p < pc.first && pc.first > 0) continue;
                 float dx[N];
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
@@ -257,18 +264,23 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
 #pragma unroll
                     for (int j = 0; j < W; ++j) dx[n] = fmaf(taps.w[j][n], dz[W - 1 - j][n], dx[n]);
                 }
-                if (a.dfinal && p >= len - (W - 1)) {
+                if (!inner() && a.dfinal && p >= len - (W - 1)) {
                     float f[N];
                     Ch::wide(Ch::load(static_cast<const T*>(a.dfinal) +
                                       ((int64_t)pc.unit * (W - 1) + p - len + W - 1) * a.D + ch), f);
 #pragma unroll
                     for (int n = 0; n < N; ++n) dx[n] += f[n];
                 }
-                if (p >= 0) Ch::store(static_cast<T*>(a.dx) + (pc.seq.start + p) * a.D + ch, dx);
+                if (inner() || p >= 0) Ch::store(static_cast<T*>(a.dx) + (pc.seq.start + p) * a.D + ch, dx);
                 else if (a.dinitial)
                     Ch::store(static_cast<T*>(a.dinitial) + ((int64_t)pc.unit * (W - 1) + p + W - 1) * a.D + ch, dx);
             }
-        }
+        };
+        static_assert(W - 1 <= AT, "");
+        int t0 = pc.first;
+        tile(t0, std::false_type());
+        for (t0 += AT; t0 + AT <= pc.end; t0 += AT) tile(t0, std::true_type());
+        for (; t0 < stop; t0 += AT) tile(t0, std::false_type());
     }
     // this piece's row of sums: [D][W], then [D]
     float* row = a.parts + (int64_t)piece * a.D * (W + 1);
