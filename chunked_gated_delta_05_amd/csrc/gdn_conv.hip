@@ -6,7 +6,7 @@
 // with: bound by memory. A thread walks a piece of a sequence for 16 bytes of
 // neighbouring channels with the last W - 1 inputs in registers, so x is read
 // once but for W - 1 tokens in front of each piece (bf16 T=8191 D=6144: 43.5 us,
-// 4.6 TB/s; B=4 T=4096 with its gradients 224, the gradients' walk 142 of them).
+// 4.6 TB/s; B=4 T=4096 with its gradients 224, the gradients' walk 140 of them).
 #include "gdn_mixer_device.h"
 
 namespace gdn {
