@@ -21,7 +21,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;                   // sanity boun
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 256;         // of a launch along x, in workgroups of 256
 // Segments of a sequence up to which each adds up those before its own, which
 // saves the launch of a merge (T=160 D=1024 20.1 to 15.8 us, T=800 26.7 to 23.8,
-// gradients of T=400 61 to 53; where 32 of them do, T=1000 D=4096 147 to 156).
+// gradients alone of T=160 29.6 to 27.1, T=400 32 to 30, B=2 T=4096 D=4096 503
+// either way; where 32 of them do, T=1000 D=4096 147 to 156).
 constexpr int64_t kJoin = 16;
 constexpr int32_t kMaxTokens = INT32_MAX - 4096;                  // of a sequence: its tiles' ends are ints
 
@@ -445,7 +446,7 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
         return GDN_ERR_INVALID;
     const uint64_t states = uint64_t(a.un.n_units) * d->D * d->S * 4;
     if (dh0 != dht && overlap(dh0, states, dht, states)) return GDN_ERR_INVALID;
-    if (dh0 == dht) a.join = 0;   // as in gdn_scan_fwd
+    if (dh0 && dh0 == dht) a.join = 0;   // as in gdn_scan_fwd
     scan_inputs(&a, u, dt, A, B, C, skip, gate, dt_bias);
     a.s_in = dht;
     a.s_out = dh0;
