@@ -181,7 +181,7 @@ __global__ __launch_bounds__(NT) void rotary_bwd_kernel(RotaryArgs a, int tokens
         w[1][0] = weight4(a.k_weight, p.lo, a.w_f32);
         w[1][1] = weight4(a.k_weight, p.hi, a.w_f32);
     }
-    const float share = a.norm == GDN_NORM_RMS ? 1.0f / a.D : a.norm == GDN_NORM_L2 ? 1.0f : 0.0f;
+    const float share = a.norm == GDN_NORM_RMS ? 1.0f / a.D : 1.0f;
     for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.tokens; t0 += (int64_t)gridDim.x * tokens) {
         const int n = (int)(a.tokens - t0 < tokens ? a.tokens - t0 : tokens);
         lds_barrier();
@@ -217,11 +217,15 @@ __global__ __launch_bounds__(NT) void rotary_bwd_kernel(RotaryArgs a, int tokens
                 dx *= is_k ? w[1][0] : w[0][0];
                 dy *= is_k ? w[1][1] : w[0][1];
             }
-            const float dot = lane_sum<L>(dot4(dx, x) + dot4(dy, y)) * share;
+            if (a.norm != GDN_NORM_NONE) {   // else the row has no part in it, finite or not
+                const float dot = lane_sum<L>(dot4(dx, x) + dot4(dy, y)) * share;
+                dx = s * (dx - x * dot);
+                dy = s * (dy - y * dot);
+            }
             if (!p.on) continue;
             T* out = (is_k ? static_cast<T*>(a.dk) : static_cast<T*>(a.dq)) + row;
-            store4(out + p.lo, s * (dx - x * dot));
-            store4(out + p.hi, s * (dy - y * dot));
+            store4(out + p.lo, dx);
+            store4(out + p.hi, dy);
         }
     }
     if (!a.parts) return;

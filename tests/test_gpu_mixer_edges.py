@@ -28,3 +28,31 @@ def test_cut_gradients_with_and_without_states(lead, states, dtype):
     assert ("dh0" in r) == states
     for k, t in r.items():
         near(t, want[k], scale[k], 2 * (24 * L + 64) + 72 + c["offs"][-1], k)
+
+
+# ------------------------------------------------------------------ rotation without a norm
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_gradients_without_a_norm_do_not_depend_on_the_rows(interleaved, dtype):
+    # dq is the gradient turned back, whatever q holds: rows that are not finite (padding that was never
+    # written), and products with the gradient beyond fp32
+    g = torch.Generator().manual_seed(31)
+    q, k, dq, dk = (torch.randn(2, 9, h, 80, generator=g).to(dtype).cuda() for h in (3, 1, 3, 1))
+    f = gb.rotary_frequencies(48, device="cuda")
+    dq[0, 2] *= 1e20
+    call = lambda x: gb.gdn_qk_rotary_bwd(x, k, f, None, dq, dk, norm=None, interleaved=interleaved)
+    want = call(q)
+    bad = q.clone()
+    bad[0, 2] *= 1e20
+    bad[1, 5] = float("nan")
+    bad[1, 7, 1, 3] = float("inf")
+    bad[0, 4, 2, 70] = -float("inf")
+    got = call(bad)
+    assert torch.isfinite(want["dq"]).all()
+    assert torch.equal(got["dq"], want["dq"]) and torch.equal(got["dk"], want["dk"])
+    # a gradient that is not finite stays in its pair
+    dq[1, 1, 0, 5] = float("inf")
+    hit = torch.zeros_like(dq, dtype=torch.bool)
+    hit[1, 1, 0, [4, 5] if interleaved else [5, 29]] = True
+    got = call(bad)
+    assert torch.equal(got["dq"][~hit], want["dq"][~hit]) and not torch.isfinite(got["dq"][hit]).any()
