@@ -28,7 +28,9 @@ constexpr int32_t kMaxTokens = INT32_MAX - 4096;                  // of a sequen
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 template <typename... P>
 bool all_aligned16(P... p) {
@@ -529,6 +531,11 @@ gdn_status check_rotary(const gdn_rotary_desc* d, RotaryArgs* a) {
     return GDN_OK;
 }
 
+// what is read one by one may be a slice of a longer array
+bool angles_aligned(const gdn_rotary_desc* d, const double* freqs, const void* positions) {
+    return aligned(freqs, 8) && aligned(positions, d->pos_i64 ? 8 : 4);
+}
+
 bool contiguous(const int64_t* stride, int32_t heads, int32_t D) {
     return stride[0] == int64_t(heads) * D && (heads == 1 || stride[1] == D);
 }
@@ -542,7 +549,7 @@ extern "C" gdn_status gdn_qk_rotary_fwd(const gdn_rotary_desc* d, const void* q,
     const gdn_status st = check_rotary(d, &a);
     if (st != GDN_OK) return st;
     if (a.tokens > 0 && (!q || !k || !q_out || !k_out || (d->R > 0 && !freqs))) return GDN_ERR_INVALID;
-    if (!all_aligned16(q, k, freqs, positions, q_weight, k_weight, q_out, k_out)) return GDN_ERR_INVALID;
+    if (!angles_aligned(d, freqs, positions) || !all_aligned16(q, k, q_weight, k_weight, q_out, k_out)) return GDN_ERR_INVALID;
     if ((q_out == q && !contiguous(d->q_stride, d->Hq, d->D)) || (k_out == k && !contiguous(d->k_stride, d->Hk, d->D)))
         return GDN_ERR_INVALID;
     a.q = q;
@@ -570,7 +577,8 @@ extern "C" gdn_status gdn_qk_rotary_bwd(const gdn_rotary_desc* d, const void* q,
     if (st != GDN_OK || query) return st;
     if (a.tokens > 0 && (!q || !k || !dq_out || !dk_out || !dq || !dk || (d->R > 0 && !freqs))) return GDN_ERR_INVALID;
     if ((q_weight == nullptr) != (dq_weight == nullptr) || (k_weight == nullptr) != (dk_weight == nullptr)) return GDN_ERR_INVALID;
-    if (!all_aligned16(q, k, freqs, positions, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight, dk_weight))
+    if (!angles_aligned(d, freqs, positions) ||
+        !all_aligned16(q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight, dk_weight))
         return GDN_ERR_INVALID;
     a.q = q;
     a.k = k;

@@ -451,7 +451,7 @@ gdn_rotary_desc rotary(const Arguments& a, const RotaryIn& x) {
     d.amplitude = number(a, 9, "amplitude");
     row_strides("q", x.q, d.q_stride);
     row_strides("k", x.k, d.k_stride);
-    need_dense(x.q, {{"freqs", &x.freqs}, {"positions", &x.positions}, {"q_weight", &x.q_weight}, {"k_weight", &x.k_weight}});
+    need_dense(x.q, {{"q_weight", &x.q_weight}, {"k_weight", &x.k_weight}});
     return d;
 }
 

@@ -203,7 +203,8 @@ typedef struct {
  *   q, k       device, B T tokens of Hq and Hk rows (strides as in
  *              gdn_linattn_desc)
  *   freqs      device fp64 [R/2], radians a token
- *   positions  device int32 or int64 [B T]; NULL: a token's place in its row
+ *   positions  device int32 or int64 [B T]; NULL: a token's place in its row.
+ *              Both aligned to their own values, so that they may be slices
  *   q_weight, k_weight  device [D] in w_dtype, or NULL
  *   q_out, k_out        device [tokens][H][D], contiguous. q_out may be q, and
  *              k_out k, where these are contiguous

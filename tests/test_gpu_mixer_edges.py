@@ -56,3 +56,19 @@ def test_gradients_without_a_norm_do_not_depend_on_the_rows(interleaved, dtype):
     hit[1, 1, 0, [4, 5] if interleaved else [5, 29]] = True
     got = call(bad)
     assert torch.equal(got["dq"][~hit], want["dq"][~hit]) and not torch.isfinite(got["dq"][hit]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_positions_and_frequencies_may_be_slices(dtype):
+    g = torch.Generator().manual_seed(32)
+    q, k = (torch.randn(37, h, 64, generator=g).cuda() for h in (3, 1))
+    f = gb.rotary_frequencies(56, device="cuda")
+    at = torch.randint(0, 100000, (40,), generator=g).to(dtype).cuda()
+    for first in (1, 2, 3):
+        own = (f[first:first + 24].clone(), at[first:first + 37].clone())
+        part = (f[first:first + 24], at[first:first + 37])
+        assert part[1].data_ptr() % 16 and (first == 2 or part[0].data_ptr() % 16)
+        want, got = gb.gdn_qk_rotary_fwd(q, k, *own), gb.gdn_qk_rotary_fwd(q, k, *part)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+        want, got = gb.gdn_qk_rotary_bwd(q, k, *own, q, k), gb.gdn_qk_rotary_bwd(q, k, *part, q, k)
+        assert torch.equal(want["dq"], got["dq"]) and torch.equal(want["dk"], got["dk"])

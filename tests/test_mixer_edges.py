@@ -1,0 +1,54 @@
+"""Calls of the operators around the recurrent layers that have to be taken, or
+refused, on the CPU: a call that the binding takes is rejected last, for not
+being on the GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from chunked_gated_delta_05_amd import binding as gb
+
+BF, F32, F64, I32, I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
+OK, INVALID = 0, 1
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def fake(i, off=0):
+    return ctypes.c_void_p((1 << 40) + (i << 32) + off)
+
+
+# ------------------------------------------------------------------ norms and rotation
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hk", "D", "R", "dtype", "w_dtype", "norm", "interleaved", "pos_i64")] + \
+               [("eps", ctypes.c_float), ("amplitude", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("q0", "q1", "k0", "k1")]
+
+
+@pytest.mark.parametrize("dtype", [I32, I64])
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+def test_positions_and_frequencies_may_be_slices(first, dtype):
+    # both are read one by one
+    q, k = z(9, 4, 64), z(9, 2, 64)
+    at, f = torch.arange(first + 9).to(dtype)[first:], gb.rotary_frequencies(2 * (24 + first))[first:]
+    for call in (lambda: gb.gdn_qk_rotary_fwd(q, k, f, at), lambda: gb.gdn_qk_rotary_bwd(q, k, f, at, q, k)):
+        with pytest.raises(ValueError, match="GPU tensors"):
+            call()
+
+
+@pytest.mark.parametrize("pos_i64,off,ok", [(0, 4, True), (0, 2, False), (1, 8, True), (1, 4, False)])
+def test_positions_are_aligned_to_their_own_size(pos_i64, off, ok):
+    # no tokens: what is accepted launches nothing
+    d = RotaryDesc(2, 0, 4, 2, 64, 64, 1, 0, 1, 0, pos_i64, 1e-6, 1.0, 256, 64, 128, 64)
+    f = gb.lib().gdn_qk_rotary_fwd
+    call = lambda pos, freqs: f(ctypes.byref(d), fake(0), fake(1), freqs, pos, None, None, fake(4), fake(5), None)
+    assert call(fake(3, off), fake(2)) == (OK if ok else INVALID)
+    assert call(fake(3), fake(2, 8)) == OK and call(fake(3), fake(2, 4)) == INVALID
+    size = ctypes.c_size_t(256)
+    b = gb.lib().gdn_qk_rotary_bwd
+    call = lambda pos, freqs: b(ctypes.byref(d), fake(0), fake(1), freqs, pos, None, None, fake(4), fake(5), fake(6), fake(7),
+                                None, None, fake(8), ctypes.byref(size), None)
+    assert call(fake(3, off), fake(2)) == (OK if ok else INVALID)
+    assert call(fake(3), fake(2, 8)) == OK and call(fake(3), fake(2, 4)) == INVALID
