@@ -550,7 +550,7 @@ extern "C" gdn_status gdn_qk_rotary_fwd(const gdn_rotary_desc* d, const void* q,
     if (st != GDN_OK) return st;
     if (a.tokens > 0 && (!q || !k || !q_out || !k_out || (d->R > 0 && !freqs))) return GDN_ERR_INVALID;
     if (!angles_aligned(d, freqs, positions) || !all_aligned16(q, k, q_weight, k_weight, q_out, k_out)) return GDN_ERR_INVALID;
-    if ((q_out == q && !contiguous(d->q_stride, d->Hq, d->D)) || (k_out == k && !contiguous(d->k_stride, d->Hk, d->D)))
+    if ((q && q_out == q && !contiguous(d->q_stride, d->Hq, d->D)) || (k && k_out == k && !contiguous(d->k_stride, d->Hk, d->D)))
         return GDN_ERR_INVALID;
     a.q = q;
     a.k = k;

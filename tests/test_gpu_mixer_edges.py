@@ -72,3 +72,13 @@ def test_positions_and_frequencies_may_be_slices(dtype):
         assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
         want, got = gb.gdn_qk_rotary_bwd(q, k, *own, q, k), gb.gdn_qk_rotary_bwd(q, k, *part, q, k)
         assert torch.equal(want["dq"], got["dq"]) and torch.equal(want["dk"], got["dk"])
+
+
+def test_rotation_of_no_tokens_with_strided_heads():
+    wide = torch.zeros(2, 0, 6, 128, device="cuda")
+    q, k, f = wide[:, :, :4, :64], wide[:, :, 4:, :64], gb.rotary_frequencies(64, device="cuda")
+    a, b = gb.gdn_qk_rotary_fwd(q, k, f)
+    assert a.shape == q.shape and b.shape == k.shape
+    w = torch.ones(64, device="cuda")
+    r = gb.gdn_qk_rotary_bwd(q, k, f, None, a, b, q_weight=w, k_weight=w)
+    assert r["dq"].shape == q.shape and not r["dq_weight"].any() and not r["dk_weight"].any()

@@ -52,3 +52,14 @@ def test_positions_are_aligned_to_their_own_size(pos_i64, off, ok):
                                 None, None, fake(8), ctypes.byref(size), None)
     assert call(fake(3, off), fake(2)) == (OK if ok else INVALID)
     assert call(fake(3), fake(2, 8)) == OK and call(fake(3), fake(2, 4)) == INVALID
+
+
+def test_rotation_of_no_tokens_with_strided_heads():
+    # empty tensors have no address: NULL in and out is not "in place"
+    d = RotaryDesc(2, 0, 4, 2, 64, 64, 1, 0, 1, 0, 0, 1e-6, 1.0, 512, 128, 256, 128)
+    f = gb.lib().gdn_qk_rotary_fwd
+    assert f(ctypes.byref(d), None, None, fake(2), None, None, None, None, None, None) == OK
+    assert f(ctypes.byref(d), fake(0), fake(1), fake(2), None, None, None, fake(3), fake(4), None) == OK
+    d.T = 3                                   # in place means contiguous, as before
+    assert f(ctypes.byref(d), fake(0), fake(1), fake(2), None, None, None, fake(0), fake(4), None) == INVALID
+    assert f(ctypes.byref(d), fake(0), fake(1), fake(2), None, None, None, fake(3), fake(1), None) == INVALID
