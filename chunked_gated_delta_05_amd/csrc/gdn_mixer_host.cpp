@@ -105,6 +105,14 @@ gdn_status check_seqs(int32_t B, int32_t T, int32_t n_units, const int32_t* host
     return s->longest > kMaxTokens ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
+// Whether states before and after share memory. False: without page lists they
+// overlap by part, so that one sequence would read what another has written.
+bool check_states(const void* s_in, const int32_t* in_pages, const void* s_out, const int32_t* out_pages, uint64_t page,
+                  int32_t units, int32_t n_pages, bool* in_place) {
+    *in_place = overlap(s_in, page * (in_pages ? n_pages : units), s_out, page * (out_pages ? n_pages : units));
+    return !*in_place || in_pages || out_pages || s_in == s_out;
+}
+
 // numbers of pieces of P tokens: gdn_mixer_internal.h
 int64_t pieces(const MxUnits& u, int64_t P) {
     if (u.dense) return int64_t(u.n_units) * (u.T > P ? (u.T + P - 1) / P : 1);
@@ -181,9 +189,10 @@ extern "C" gdn_status gdn_conv_fwd(const gdn_conv_desc* d, const void* x, const 
     a.out_pages = out_pages;
     a.n_pages = n_pages;
     a.y = y;
-    const uint64_t page = uint64_t(d->W - 1) * d->D * elem_bytes(d->dtype);
-    const bool in_place = overlap(s_in, page * (in_pages ? n_pages : a.un.n_units), s_out,
-                                  page * (out_pages ? n_pages : a.un.n_units));
+    bool in_place;
+    if (!check_states(s_in, in_pages, s_out, out_pages, uint64_t(d->W - 1) * d->D * elem_bytes(d->dtype), a.un.n_units, n_pages,
+                      &in_place))
+        return GDN_ERR_INVALID;
     return run(gdn::launch_conv_fwd(a, in_place, stream));
 }
 
@@ -409,9 +418,10 @@ extern "C" gdn_status gdn_scan_fwd(const gdn_scan_desc* d, const void* u, const 
     a.out = out;
     // a sequence's last segment may replace the state before its others have read
     // it: where the two share memory the merge reads it in front of all
-    const uint64_t page = uint64_t(d->D) * d->S * 4;
-    if (overlap(s_in, page * (in_pages ? n_pages : a.un.n_units), s_out, page * (out_pages ? n_pages : a.un.n_units)))
-        a.join = 0;
+    bool in_place;
+    if (!check_states(s_in, in_pages, s_out, out_pages, uint64_t(d->D) * d->S * 4, a.un.n_units, n_pages, &in_place))
+        return GDN_ERR_INVALID;
+    if (in_place) a.join = 0;
     if (a.cut) {
         a.slots = static_cast<float*>(workspace);
         a.sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + s.slots);

@@ -84,6 +84,12 @@ void check_states(const char* name, const Tensor& t, const char* pages_name, con
     *n_pages = n;
 }
 
+// Without pages the states may be replaced in place, or lie apart
+void check_states_apart(const Tensor& s_in, const Tensor& in_pages, const Tensor& final_out, const Tensor& out_pages) {
+    if (in_pages.defined() || out_pages.defined() || !s_in.defined() || !final_out.defined()) return;
+    if (s_in.data_ptr() != final_out.data_ptr()) check_apart(final_out, {{"initial_state", &s_in}});
+}
+
 int32_t parameters(std::initializer_list<std::pair<const char*, const Tensor*>> all) {
     ScalarType t = ScalarType::Undefined;
     for (const auto& [name, p] : all) {
@@ -154,6 +160,7 @@ PyObject* conv_fwd(const Arguments& a) {
     if (out.defined()) check_tensor("out", out, x.scalar_type(), x.sizes());
     check_apart(out, {{"x", &x}, {"weight", &weight}, {"bias", &bias}, {"initial_state", &s_in}, {"final_out", &final_out}});
     check_apart(final_out, {{"x", &x}, {"weight", &weight}, {"bias", &bias}});
+    check_states_apart(s_in, in_pages, final_out, out_pages);
     need_dense(x, {{"initial_state", &s_in}, {"final_out", &final_out}, {"out", &out}});
     check_devices(x, {{"weight", &weight}, {"bias", &bias}, {"unit metadata", &offsets}, {"initial_state", &s_in},
                       {"initial_pages", &in_pages}, {"final_out", &final_out}, {"final_pages", &out_pages}, {"out", &out}});
@@ -300,6 +307,7 @@ PyObject* scan_fwd(const Arguments& a) {
     scan_apart(out, x);
     check_apart(out, {{"initial_state", &s_in}, {"final_out", &final_out}});
     scan_apart(final_out, x);
+    check_states_apart(s_in, in_pages, final_out, out_pages);
     need_dense(x.u, {{"initial_state", &s_in}, {"final_out", &final_out}, {"out", &out}});
     scan_devices(x, {{"unit metadata", &offsets}, {"initial_state", &s_in}, {"initial_pages", &in_pages},
                      {"final_out", &final_out}, {"final_pages", &out_pages}, {"out", &out}});

@@ -62,7 +62,8 @@ typedef struct {
  *             in_pages device int32 [units]; NULL: zeros
  *   s_out     device, likewise with out_pages; NULL: not wanted. May be s_in
  *             (each sequence's state is replaced); two sequences must not write
- *             one page, nor one write a page that another reads
+ *             one page, nor one write a page that another reads (without page
+ *             lists states that overlap by part are GDN_ERR_INVALID)
  *   y         device [tokens][D], contiguous
  */
 gdn_status gdn_conv_fwd(const gdn_conv_desc* desc, const void* x, const void* weight, const void* bias,

@@ -101,11 +101,56 @@ void joins() {
     }
     expect(joined > 0 && merged > 0, "one kind only", joined);
 }
+// Without page lists the states may be replaced in place or lie apart; where they
+// overlap by part a sequence would read what another has written.
+template <typename F>
+void overlaps(int units, int64_t page, F call) {
+    char* s = at<char>(20);
+    const int32_t *none = nullptr, *pages = at<const int32_t>(21);
+    const struct {
+        int64_t from;
+        bool in_paged, out_paged, ok;
+    } cases[] = {{0, false, false, true},          {page, false, false, false},  {-page, false, false, false},
+                 {64, false, false, false},        {units * page - 16, false, false, false},
+                 {units * page, false, false, true}, {-units * page, false, false, true},
+                 {page, true, true, true},         {page, true, false, true},    {page, false, true, true}};
+    for (const auto& c : cases) {
+        launches.clear();
+        const gdn_status st = call(s, c.in_paged ? pages : none, s + c.from, c.out_paged ? pages : none);
+        expect(st == (c.ok ? GDN_OK : GDN_ERR_INVALID), "states that overlap", c.from);
+        expect(launches.empty() != c.ok, "launches", c.from);
+    }
+    for (int null = 0; null < 3; ++null)
+        expect(call(null != 1 ? nullptr : s, none, null != 2 ? nullptr : s, none) == GDN_OK, "states left out", null);
+}
+void states() {
+    for (int n : {2, 3}) {
+        gdn_conv_desc c;
+        memset(&c, 0, sizeof c);
+        c.B = n, c.T = 2, c.D = 64, c.W = 4, c.dtype = c.w_dtype = GDN_DTYPE_BF16, c.x_stride = 64;
+        overlaps(n, 3 * 64 * 2, [&](char* in, const int32_t* ip, char* out, const int32_t* op) {
+            return gdn_conv_fwd(&c, at(0), at(1), nullptr, in, ip, out, op, 8, at(2), nullptr);
+        });
+        for (int T : {5, 900}) {          // whole and cut
+            const gdn_scan_desc d = scan_desc(n, T, 64, 16);
+            overlaps(n, 64 * 16 * 4, [&](char* in, const int32_t* ip, char* out, const int32_t* op) {
+                size_t bytes = 0;
+                auto run = [&](void* ws) {
+                    return gdn_scan_fwd(&d, at(0), at(1), at<float>(2), at(3), at(4), nullptr, nullptr, nullptr, (float*)in, ip,
+                                        (float*)out, op, 8, nullptr, at(5), ws, &bytes, nullptr);
+                };
+                const gdn_status st = run(nullptr);
+                return st == GDN_OK ? run(at(6)) : st;
+            });
+        }
+    }
+}
 }  // namespace
 
 int main(int argc, char** argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     if (what == "joins") joins();
+    else if (what == "states") states();
     else return 2;
     printf("%s: ok\n", what.c_str());
     return 0;

@@ -63,3 +63,20 @@ def test_rotation_of_no_tokens_with_strided_heads():
     d.T = 3                                   # in place means contiguous, as before
     assert f(ctypes.byref(d), fake(0), fake(1), fake(2), None, None, None, fake(0), fake(4), None) == INVALID
     assert f(ctypes.byref(d), fake(0), fake(1), fake(2), None, None, None, fake(3), fake(1), None) == INVALID
+
+
+# ------------------------------------------------------------------ states
+@pytest.mark.parametrize("first", [0, 1, 2])
+def test_states_may_not_overlap_by_part(first):
+    # two sequences: pool[:2] to pool[1:3] would let one read what the other has written
+    msg = "out overlaps initial_state" if first == 1 else "GPU tensors"
+    pool = z(5, 3, 64)
+    with pytest.raises(ValueError, match=msg):
+        gb.gdn_conv_fwd(z(2, 7, 64), z(64, 4), initial_state=pool[:2], final_out=pool[first:first + 2])
+    pool = z(5, 64, 16, dtype=F32)
+    x, rows, A = z(2, 7, 64), z(2, 7, 1, 16), z(64, 16, dtype=F32)
+    with pytest.raises(ValueError, match=msg):
+        gb.gdn_scan_fwd(x, x, A, rows, rows, initial_state=pool[:2], final_out=pool[first:first + 2])
+    with pytest.raises(ValueError, match="GPU tensors"):     # by pages it is the caller's tables that matter
+        gb.gdn_scan_fwd(x, x, A, rows, rows, initial_state=pool[:3], initial_pages=z(2, dtype=I32),
+                        final_out=pool[1:4], final_pages=z(2, dtype=I32))

@@ -31,3 +31,7 @@ def plans(tmp_path_factory):
 
 def test_gradients_of_few_segments_are_joined_with_and_without_states(plans):
     plans("joins")
+
+
+def test_states_may_not_overlap_by_part(plans):
+    plans("states")
