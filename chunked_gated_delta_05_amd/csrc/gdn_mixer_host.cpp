@@ -448,6 +448,7 @@ extern "C" gdn_status gdn_scan_bwd(const gdn_scan_desc* d, const void* u, const 
     if (rows > kMaxElems / (int64_t(d->D) * (d->S + 2)) ||
         gdn::row_sums_workgroups(a.un.n_pieces, int64_t(d->D) * (d->S + 2)) > kMaxThreads / 256)
         return GDN_ERR_UNSUPPORTED;
+    if (gdn::scan_sum_workgroups(a.un.total, a.un.n_pieces, d->G, d->D, d->S) > kMaxThreads / 256) return GDN_ERR_UNSUPPORTED;
     const int64_t bc = align256(walks * a.un.total * 2 * d->S * 4), ap = align256(rows * d->D * (d->S + 2) * 4);
     bool query = false;
     st = check_workspace(s.slots + s.sums + bc + ap, workspace, workspace_bytes, &query);

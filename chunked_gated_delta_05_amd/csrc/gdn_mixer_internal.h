@@ -91,6 +91,13 @@ struct ScanArgs {
     float *bc_parts;          // [G * bwd_blocks][tokens][2][S]
     float *a_parts;           // [pieces][D (S + 2)]
 };
+// Workgroups of the sums of dB and dC, and behind them those of dA, dskip and
+// ddt_bias where these have few rows (else row_sums adds them up).
+constexpr bool scan_sums_together(int64_t pieces) { return row_sums_rows(pieces) == 0; }
+constexpr int64_t scan_bc_workgroups(int64_t tokens, int G, int S) { return (tokens * G * (S / 2) + 255) / 256; }
+constexpr int64_t scan_sum_workgroups(int64_t tokens, int64_t pieces, int G, int D, int S) {
+    return scan_bc_workgroups(tokens, G, S) + (scan_sums_together(pieces) ? row_sums_workgroups(pieces, int64_t(D) * (S + 2)) : 0);
+}
 // channels of a workgroup
 constexpr int scan_channels(int S) { return S == 8 ? 128 : 2048 / S; }
 constexpr int scan_narrow_channels(int S) { return S == 8 ? 32 : 16; }

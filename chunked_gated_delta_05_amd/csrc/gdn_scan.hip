@@ -1143,9 +1143,9 @@ hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int64_t d = a.D, n = d * (a.S + 2);
     const RowSums out{{a.dA, a.dskip, a.ddt_bias}, {d * a.S, d, d}};
-    const bool few = row_sums_rows(a.un.n_pieces) == 0;
-    const unsigned bc = (unsigned)((a.un.total * a.G * (2 * a.S / 4) + NT - 1) / NT), cols = (unsigned)((n + 63) / 64);
-    const unsigned grid = bc + (few ? cols : 0);
+    const bool few = scan_sums_together(a.un.n_pieces);
+    const unsigned bc = (unsigned)scan_bc_workgroups(a.un.total, a.G, a.S), cols = (unsigned)((n + 63) / 64);
+    const unsigned grid = (unsigned)scan_sum_workgroups(a.un.total, a.un.n_pieces, a.G, a.D, a.S);
     if (grid > 0) {
         if (a.dtype == GDN_DTYPE_BF16) scan_bc_kernel<bf16><<<grid, NT, 0, s>>>(a, a.bwd_blocks, bc, out, cols);
         else scan_bc_kernel<float><<<grid, NT, 0, s>>>(a, a.bwd_blocks, bc, out, cols);

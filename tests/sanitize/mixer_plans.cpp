@@ -145,12 +145,24 @@ void states() {
         }
     }
 }
+// The sums of dB and dC share a launch with those of dA where these are few: both
+// have to fit into one.
+void limits() {
+    for (const auto& [T, ok] : {std::pair{4294965, true}, std::pair{4294966, true}, std::pair{4294967, false}}) {
+        const gdn_scan_desc d = scan_desc(250, T, 8, 8);
+        expect(scan_bwd(d, nullptr, nullptr) == (ok ? GDN_OK : GDN_ERR_UNSUPPORTED), "sums beyond a launch", T);
+        expect(launches.size() == (ok ? 1u : 0u), "launches", T);
+        const int64_t bc = (int64_t(250) * T * 4 + 255) / 256, cols = (8 * (8 + 2) + 63) / 64;
+        expect(((bc + cols) * 256 < int64_t(1) << 32) == ok, "the test's sizes", T);
+    }
+}
 }  // namespace
 
 int main(int argc, char** argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     if (what == "joins") joins();
     else if (what == "states") states();
+    else if (what == "limits") limits();
     else return 2;
     printf("%s: ok\n", what.c_str());
     return 0;

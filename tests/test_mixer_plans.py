@@ -35,3 +35,7 @@ def test_gradients_of_few_segments_are_joined_with_and_without_states(plans):
 
 def test_states_may_not_overlap_by_part(plans):
     plans("states")
+
+
+def test_sums_that_share_a_launch_fit_into_it(plans):
+    plans("limits")
