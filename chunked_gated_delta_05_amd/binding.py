@@ -1048,14 +1048,25 @@ def gdn_scan_bwd(u, dt, A, B, C, skip, gate, dout, h, *, dt_bias=None, dt_softpl
 class SelectiveScan(torch.autograd.Function):
     """gdn_scan_fwd and gdn_scan_bwd as one autograd op: (u, dt, A, B, C, skip,
     gate, dt_bias, initial_state, dt_softplus, meta) -> (out, final state).
-    Second-order gradients raise."""
+    Second-order gradients raise. States are kept for the backward only where one
+    can follow."""
+
+    @staticmethod
+    def _prompts(want_h, u, dt, A, B, C, skip=None, gate=None, dt_bias=None, initial_state=None, dt_softplus=False,
+                 meta=None):
+        return gdn_scan_fwd(u, dt, A, B, C, skip, gate, dt_bias=dt_bias, dt_softplus=dt_softplus, meta=meta,
+                            initial_state=initial_state, output_final_state=True, want_h=want_h)
+
+    @classmethod
+    def apply(cls, *args):
+        # forward cannot tell: it always runs with gradients off, and needs_input_grad is that of the tensors alone
+        return super().apply(*args) if torch.is_grad_enabled() else cls._prompts(False, *args)[:2]
 
     @staticmethod
     def forward(ctx, u, dt, A, B, C, skip=None, gate=None, dt_bias=None, initial_state=None, dt_softplus=False,
                 meta=None):
-        out, final, h = gdn_scan_fwd(u, dt, A, B, C, skip, gate, dt_bias=dt_bias, dt_softplus=dt_softplus, meta=meta,
-                                     initial_state=initial_state, output_final_state=True,
-                                     want_h=any(ctx.needs_input_grad))
+        out, final, h = SelectiveScan._prompts(any(ctx.needs_input_grad), u, dt, A, B, C, skip, gate, dt_bias,
+                                               initial_state, dt_softplus, meta)
         ctx.save_for_backward(u, dt, A, B, C, skip, gate, dt_bias, h)
         ctx.dt_softplus, ctx.meta, ctx.has_s0 = dt_softplus, meta, initial_state is not None
         ctx.set_materialize_grads(False)

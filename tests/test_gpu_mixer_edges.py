@@ -82,3 +82,24 @@ def test_rotation_of_no_tokens_with_strided_heads():
     w = torch.ones(64, device="cuda")
     r = gb.gdn_qk_rotary_bwd(q, k, f, None, a, b, q_weight=w, k_weight=w)
     assert r["dq"].shape == q.shape and not r["dq_weight"].any() and not r["dk_weight"].any()
+
+
+# ------------------------------------------------------------------ autograd
+def test_scan_without_gradients_takes_no_room_for_states():
+    c = scan_case((1, 2048), 1024, 16, 1, "bf16", seed=41)
+    args = [c[k] for k in ("u", "dt", "A", "B", "C", "skip", "gate", "dt_bias", "s0")]
+    args[2] = args[2].clone().requires_grad_()
+    call = lambda: gb.SelectiveScan.apply(*args, True)
+    room = []
+    for off in (False, True):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        with torch.set_grad_enabled(not off):
+            got = call()
+        room.append(torch.cuda.max_memory_allocated() - before)
+        if not off:
+            want = [t.detach().clone() for t in got]
+            del got
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert room[0] - room[1] >= 2048 // 16 * 1024 * 16 * 4 and not got[0].requires_grad

@@ -80,3 +80,31 @@ def test_states_may_not_overlap_by_part(first):
     with pytest.raises(ValueError, match="GPU tensors"):     # by pages it is the caller's tables that matter
         gb.gdn_scan_fwd(x, x, A, rows, rows, initial_state=pool[:3], initial_pages=z(2, dtype=I32),
                         final_out=pool[1:4], final_pages=z(2, dtype=I32))
+
+
+# ------------------------------------------------------------------ autograd
+@pytest.fixture
+def scans(monkeypatch):
+    """want_h of the calls that SelectiveScan makes, which are replaced."""
+    seen = []
+
+    def fwd(u, *rest, initial_state=None, output_final_state=False, want_h=False, **kw):
+        seen.append(want_h)
+        return u.clone(), u.new_zeros(1) if output_final_state else None, u.new_zeros(1) if want_h else None
+
+    monkeypatch.setattr(gb, "gdn_scan_fwd", fwd)
+    return seen
+
+
+@pytest.mark.parametrize("off", [torch.no_grad, torch.inference_mode])
+def test_scan_keeps_states_for_gradients_alone(scans, off):
+    u, A = z(1, 4, 64, dtype=F32), z(64, 16, dtype=F32).requires_grad_()      # A: a parameter
+    rows = z(1, 4, 1, 16, dtype=F32)
+    with off():
+        out, final = gb.SelectiveScan.apply(u, u, A, rows, rows)
+        assert not out.requires_grad and final is not None
+        gb.SelectiveScan.apply(u, u, A, rows, rows, None, u, None, None, True, None)
+    out, _ = gb.SelectiveScan.apply(u, u, A.detach(), rows, rows)
+    assert not out.requires_grad and scans == [False] * 3
+    out, final = gb.SelectiveScan.apply(u, u, A, rows, rows)
+    assert out.requires_grad and final.requires_grad and scans[3:] == [True]
