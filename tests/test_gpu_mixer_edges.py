@@ -6,7 +6,7 @@ import torch
 
 import mixer_ref as ref
 from chunked_gated_delta_05_amd import binding as gb
-from test_gpu_mixer import near, scan_args, scan_case, scan_gpu, scan_gpu_bwd
+from test_gpu_mixer import DT, layout, near, scan_args, scan_case, scan_gpu, scan_gpu_bwd
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,107 @@ def test_cut_gradients_with_and_without_states(lead, states, dtype):
     assert ("dh0" in r) == states
     for k, t in r.items():
         near(t, want[k], scale[k], 2 * (24 * L + 64) + 72 + c["offs"][-1], k)
+
+
+# ------------------------------------------------------------------ long prompts
+def scan_with_errors(u, dt, A, B, C, skip, gate, bias, s0, offs, S, decay_steps):
+    """The scan in 64 bits on the GPU, all sequences side by side, and with every
+    value the error that fp32 arithmetic may have by then, to first order, in
+    steps of 2^-24: out, its error, final states, their error.
+
+    t = softplus(raw): raw is rounded (slope sigmoid), and e^-|raw| is off by the
+    rounding of |raw| log2(e) twice, its own step (2) and that of what becomes of
+    it. A decay is off by t's error times |A|, by `decay_steps` of its exponent (A
+    log2(e), the product; where segments are joined their sums as well) and by
+    two steps of its own; the update and du B round three times and once; y rounds
+    S + 2 times, the gate like e^-|raw|."""
+    n, length = len(offs) - 1, [b - a for a, b in zip(offs, offs[1:])]
+    T, D = max(length), u.shape[-1]
+    at = torch.zeros(T, n, dtype=torch.int64, device="cuda")
+    live = torch.zeros(T, n, dtype=torch.bool, device="cuda")
+    for i, (a, b) in enumerate(zip(offs, offs[1:])):
+        at[:b - a, i] = torch.arange(a, b, device="cuda")
+        live[:b - a, i] = True
+    flat = lambda x, k: x.double().reshape(-1, *x.shape[x.dim() - k:])
+    u, raw, gate = flat(u, 1), flat(dt, 1) + bias.double(), flat(gate, 1)
+    B, C, A, skip = flat(B, 2)[:, 0], flat(C, 2)[:, 0], A.double(), skip.double()
+    t = torch.nn.functional.softplus(raw, threshold=60)
+    e = torch.exp(-raw.abs())
+    et = 2 * torch.sigmoid(raw) * raw.abs() + e * (2 * raw.abs() + 4) + 4 * t
+    y, ey = torch.zeros_like(u), torch.zeros_like(u)
+    h = s0.double().clone()
+    eh = torch.zeros_like(h)
+    for i in range(T):
+        p, on = at[i], live[i]
+        p, hh, ehh = p[on], h[on], eh[on]
+        tt, ett, uu, b, c = t[p, :, None], et[p, :, None], u[p, :, None], B[p, None], C[p, None]
+        a = torch.exp(tt * A)
+        ea = a * (A.abs() * ett + (tt * A).abs() * decay_steps + 2)
+        new = a * hh + tt * uu * b
+        ehh = a * ehh + ea * hh.abs() + (uu * b).abs() * ett + 3 * (tt * uu * b).abs() + new.abs()
+        y[p] = (c * new).sum(-1) + skip * uu[..., 0]
+        ey[p] = (c.abs() * (ehh + (S + 2) * new.abs())).sum(-1) + 2 * (skip * uu[..., 0]).abs()
+        h[on], eh[on] = new, ehh
+    sg = torch.sigmoid(gate)
+    out = y * gate * sg
+    return out, (gate * sg).abs() * ey + out.abs() * (2 * gate.abs() + 8), h, eh
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lead,D,decay_steps", [
+    ([700, 2900, 1, 1500, 2211, 880], 4096, 2),      # one state a lane
+    ((2, 4096), 4096, 2),                            # likewise
+    ((1, 4096), 1024, 32)])                          # segments of 96 tokens at most: sums of 96 / 8 + 8 terms and 3 more
+def test_long_prompts_within_their_own_error(lead, D, decay_steps, dtype):
+    S, dt = 16, DT[dtype]
+    g = torch.Generator("cuda").manual_seed(51)
+    ld, offs, meta = layout(lead)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    u, gate, raw = (randn(*ld, D).to(dt) for _ in range(3))
+    B, C = randn(*ld, 1, S).to(dt), randn(*ld, 1, S).to(dt)
+    A = -torch.arange(1, S + 1, device="cuda").float() * torch.exp(0.1 * randn(D, S))
+    skip, bias, s0 = randn(D), randn(D) - 5, randn(len(offs) - 1, D, S)
+    out, final, _ = gb.gdn_scan_fwd(u, raw, A, B, C, skip, gate, dt_bias=bias, dt_softplus=True, meta=meta, initial_state=s0,
+                                    output_final_state=True)
+    want, e, state, es = scan_with_errors(u, raw, A, B, C, skip, gate, bias, s0, offs, S, decay_steps)
+    for got, w, err, what in ((out.view(-1, D), want, e, "out"), (final, state, es, "final")):
+        tol = torch.finfo(got.dtype).eps / 2 * w.abs() * 1.01 + 1.05 * 2.0 ** -24 * err + 1e-37
+        worst = ((got.double() - w).abs() / tol).max()
+        assert worst <= 1, (what, float(worst))
+
+
+# ------------------------------------------------------------------ what lies around the tensors
+def walled(x, wall):
+    """A copy of x with `wall` of 4096 elements on either side; the whole."""
+    whole = torch.full((x.numel() + 8192,), wall, dtype=x.dtype, device="cuda")
+    inner = whole[4096:4096 + x.numel()].view(x.shape)
+    inner.copy_(x)
+    return inner, whole
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lead,D,S", [
+    ((520, 37), 128, 16), ((520, 33), 128, 8), ((520, 41), 64, 32), ((520, 37), 32, 64),     # two channels a lane
+    ((300, 37), 128, 16), ((300, 35), 128, 8), ((300, 37), 32, 64),                          # one
+    ((1, 61), 40, 16), ((1, 67), 40, 8), ((1, 70), 24, 32), ((1, 61), 24, 64),               # one state a lane
+    ((1, 901), 72, 16), ((1, 913), 72, 8), ((2, 905), 24, 64)])                              # cut
+def test_scan_reads_and_writes_nothing_around_its_tensors(lead, D, S, dtype):
+    # NaN on either side of what is read, and what is on either side of the outputs stays
+    c = scan_case(lead, D, S, 1, dtype, seed=61)
+    want, wfinal, h = scan_gpu(c, want_h=True)
+    grads = scan_gpu_bwd(c, h)
+    w = dict(c)
+    for k in ("u", "dt", "gate", "B", "C", "A", "skip", "dt_bias", "s0", "dout", "dht"):
+        w[k] = walled(c[k], float("nan"))[0]
+    out, around = walled(torch.zeros_like(want), 7.0)
+    final, around_final = walled(torch.zeros_like(wfinal), 7.0)
+    _, _, h2 = scan_gpu(w, want_h=True, out=out, final_out=final)
+    assert torch.equal(out, want) and torch.equal(final, wfinal) and torch.equal(h2, h)
+    for whole in (around, around_final):
+        assert (whole[:4096] == 7).all() and (whole[-4096:] == 7).all()
+    got = scan_gpu_bwd(w, walled(h2, float("nan"))[0])
+    for k, t in grads.items():
+        assert torch.equal(got[k], t), k
 
 
 # ------------------------------------------------------------------ rotation without a norm
