@@ -372,7 +372,7 @@ struct NarrowLane {
 // In assembly: a and b added up with those 8 lanes away in a row of 16, a's sum in
 // the lower lanes of a, b's in the upper ones. Adds that write only some quads
 // take the place of selects; a value is exchanged two waits or more after it was
-// written.
+// written. Results are written before other inputs are read ("+&v").
 #define GDN_HALVES(a, b) \
     "v_add_f32_dpp " a ", " a ", " a " row_ror:8 row_mask:0xf bank_mask:0x3\n" \
     "v_add_f32_dpp " a ", " b ", " b " row_ror:8 row_mask:0xf bank_mask:0xc\n"
@@ -396,7 +396,7 @@ __device__ __forceinline__ void fold16(float (&y)[16]) {
         "s_nop 1\n"
         GDN_QUADS("%0", "%4") GDN_QUADS("%1", "%5") GDN_QUADS("%2", "%6") GDN_QUADS("%3", "%7")
         "s_nop 1"
-        : "+v"(y[0]), "+v"(y[1]), "+v"(y[2]), "+v"(y[3]), "+v"(y[4]), "+v"(y[5]), "+v"(y[6]), "+v"(y[7])
+        : "+&v"(y[0]), "+&v"(y[1]), "+&v"(y[2]), "+&v"(y[3]), "+&v"(y[4]), "+&v"(y[5]), "+&v"(y[6]), "+&v"(y[7])
         : "v"(y[8]), "v"(y[9]), "v"(y[10]), "v"(y[11]), "v"(y[12]), "v"(y[13]), "v"(y[14]), "v"(y[15]));
 #undef GDN_QUADS
 }
@@ -755,7 +755,7 @@ struct ChannelSums {
         if constexpr (FOLD) {
             float v[4] = {b[0], b[1], b[2], b[3]};
             asm("s_nop 1\n" GDN_HALVES("%0", "%4") GDN_HALVES("%1", "%5") GDN_HALVES("%2", "%6") GDN_HALVES("%3", "%7")
-                : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])
+                : "+&v"(v[0]), "+&v"(v[1]), "+&v"(v[2]), "+&v"(v[3])
                 : "v"(c[0]), "v"(c[1]), "v"(c[2]), "v"(c[3]));
             to[0][lane] = f32x4{v[0], v[1], v[2], v[3]};
         } else {
