@@ -5,8 +5,9 @@
 // A token's value costs W products for the two bytes it is read and written
 // with: bound by memory. A thread walks a piece of a sequence for 16 bytes of
 // neighbouring channels with the last W - 1 inputs in registers, so x is read
-// once but for W - 1 tokens in front of each piece (bf16 T=8191 D=6144: 43.5 us,
-// 4.6 TB/s; B=4 T=4096 with its gradients 224, the gradients' walk 140 of them).
+// once but for W - 1 tokens in front of each piece (bf16 T=8191 D=6144: 44 us,
+// 4.6 TB/s, with four inputs in turn, 47 with more; B=4 T=4096 with its gradients
+// 224, the gradients' walk 140 of them).
 #include "gdn_mixer_device.h"
 
 namespace gdn {
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
     if (pc.first < pc.end) load(pc.first);
     entry<T, W, N>(a, pc, pc.first, ch, past);
     // Whole tiles, and the last one apart: where the number of a tile's stores is
-    // fixed the next tile's loads are waited for without them (45.5 to 43.5 us).
+    // fixed the next tile's loads are waited for without them (45.7 to 44 us; in
+    // fp32, T=8191 D=4096, 55.5 and 56).
     auto tile = [&](int t0, auto whole) {
         typename Ch::raw now[AT];
 #pragma unroll
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
         if (len > 0) load(pc.first);
         entry<T, W, N>(a, pc, pc.first, ch, past);
         // inner: of tiles that neither begin nor end the piece, which store as many
-        // tokens each (228 to 224 us; B=2 T=2048 D=2048 36.5 to 33)
+        // tokens each (230 to 225 us; B=2 T=2048 D=2048 35.6 to 33.2)
         auto tile = [&](int t0, auto inner) {
             typename Ch::raw cx[AT], cd[AT];
 #pragma unroll

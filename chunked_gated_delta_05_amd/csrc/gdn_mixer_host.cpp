@@ -282,7 +282,17 @@ int64_t fullest(const MxUnits& u, const int32_t* host, int64_t nb, int64_t P) {
 // four of 1000 113 and 92; D=1024, T=300 16 and 14.3, 400 17.3 and 18.4; 12
 // documents, T=16384, 134 and 172; S=64 D=1024, one and four of T=1000 44 and 87,
 // 112 and 90. Beyond: eight of T=1000 D=4096 156 with one channel a lane and 168
-// with one state).
+// with one state). Other S, cut and whole again: S=8 D=1024, one of T=200 15.6 and
+// 12.4, 400 16.9 and 20.9, four of 400 22 and 21.7, of 1000 33.5 and 47, D=4096 one of
+// 1000 33 and 47; S=32 D=1024, one of T=200 14.8 and 14, 400 17.6 and 23.7, four of 400
+// 33.7 and 25.4, of 1000 61 and 56, of 2000 109 and 105; S=64 D=1024, one of T=200 17.3
+// and 21.5, 400 25 and 37, four of 400 57 and 40, of 2000 202 and 174. fp32 takes as
+// long whole and up to a quarter longer cut (S=8 D=4096 T=1000 41), for which there is
+// no term; storing h adds 2 to 6% whole, 0 to 4% cut. The rule takes the faster side of
+// all these. It takes the slower one for a few ragged documents (five of 210 to 402
+// tokens, D=1536 G=2, cut: 28 and 25, 32 and 27, 47 and 41, 82 and 63 at S=8 to 64; in
+// fp32 29 and 25, 32 and 27.5, 48 and 41, 70 and 64), for two of T=2000 D=4096 S=8
+// (whole: 83 and 92) and, in fp32, four of T=2000 D=1024 S=16 (cut: 79 and 74).
 bool whole_pays(const ScanArgs& a, const int32_t* host, int64_t longest, int64_t P) {
     const double state = a.S == 8 ? 26 : a.S == 16 ? 18.5 : a.S == 32 ? 32 : 67;
     const int ch = gdn::scan_narrow_channels(a.S);

@@ -104,8 +104,9 @@ gdn_status gdn_conv_step(const gdn_conv_desc* desc, const void* x, const void* w
  *     y_t[d] = sum_s C_t[g][s] h_t[d][s] + skip[d] u_t[d]
  *     out_t[d] = y_t[d], or y_t[d] gate_t[d] sigmoid(gate_t[d])
  *
- * All values must be finite. A decay is one fp32 exponential (about 2^-23),
- * so that a state which hardly decays drifts by up to that a token.
+ * All values must be finite. A decay is one fp32 exponential (about 2^-23, and
+ * as much of its exponent), so that a state which hardly decays drifts by up to
+ * that a token (but for gdn_scan_step, which adds what a weak decay takes).
  */
 typedef struct {
     int32_t B, T, D, G;                /* D / G a multiple of 8 */
@@ -182,8 +183,8 @@ gdn_status gdn_scan_step(const gdn_scan_desc* desc, const void* u, const void* d
  *
  * for the R / 2 pairs i of its first R values, a = i and b = i + R/2, or a = 2i
  * and b = 2i + 1 with interleaved; values from R on stay n. The angle of pair i
- * is position * freqs[i], multiplied and reduced to a turn in 64 bits, so that
- * far positions lose nothing.
+ * is position * freqs[i], multiplied and reduced to a turn in 64 bits: off by
+ * up to 2^-51 of itself, 2^-24 of a turn after 2^27 turns.
  */
 enum { GDN_NORM_NONE = 0, GDN_NORM_RMS = 1, GDN_NORM_L2 = 2 };
 typedef struct {
