@@ -958,8 +958,9 @@ def gdn_conv_fwd(x, weight, bias=None, *, activation=None, meta: UnitMeta | None
     bf16 or fp32. initial_state: the W - 1 inputs in front of each sequence,
     oldest first, in x's type, [units,W-1,D], or a pool [n_pages,W-1,D] with
     initial_pages int32 [units] (-1: zeros). final_out likewise with final_pages
-    (-1: not written); it may be the pool that initial_state is. out: contiguous,
-    apart from the inputs. Returns (y, final state or None)."""
+    (-1: not written); it may be what initial_state is (without pages not a tensor
+    that overlaps it by part). out: contiguous, apart from the inputs. Returns (y,
+    final state or None)."""
     return (_NATIVE or _native()).conv_fwd(x, weight, bias, _silu(activation), *_meta_args(meta), initial_state,
                                            initial_pages, output_final_state, final_out, final_pages, out)
 
@@ -1146,8 +1147,8 @@ def gdn_qk_rotary_fwd(q, k, freqs=None, positions=None, *, norm="rms", q_weight=
     q [B,T,Hq,D] and k [B,T,Hk,D], or [T,h,D], bf16 or fp32, D a multiple of 8 up
     to 256; rows contiguous and 16-byte aligned, tokens and heads may be strided.
     freqs: fp64 [R/2], radians a token (rotary_frequencies), R a multiple of 8,
-    or None. positions: int32 or int64 [B,T] or [T]; None: a token's place in its
-    row of [B,T,..]. q_weight, k_weight: [D], bf16 or fp32. q_out and k_out:
+    or None. positions: int32 or int64 [B,T] or [T] (contiguous, as a slice of a
+    longer array is); None: a token's place in its row of [B,T,..]. q_weight, k_weight: [D], bf16 or fp32. q_out and k_out:
     contiguous; q_out may be a contiguous q, k_out a contiguous k. Returns (q,
     k)."""
     return (_NATIVE or _native()).rotary_fwd(q, k, freqs, positions, _norm_code(norm), q_weight, k_weight, eps,
